@@ -69,8 +69,9 @@ enum {
     TSV_DERR_NONFINITE = 16, /* a visited logits row, or a draft row that is read, is not finite */
     TSV_DERR_TIMEOUT = 32,   /* internal: a bounded device-side wait gave up; outputs of the
                                 sequence are not valid (never expected; reported, not trapped) */
-    TSV_DERR_INTERNAL = 64   /* checked builds only (-DTSV_CHECKED, a test build): a device-side
+    TSV_DERR_INTERNAL = 64,  /* checked builds only (-DTSV_CHECKED, a test build): a device-side
                                 index check failed and the access was skipped -- a library bug */
+    TSV_DERR_POOL = 128      /* the pool of free blocks is too small, or its count is wrong */
 };
 
 /* Message for the calling thread's most recent failed call ("" if none). */
@@ -291,6 +292,119 @@ tsv_status tsv_tree_reject_sample_compact_ex(const void *target_logits, const fl
                                              const int32_t *seq_lens, int32_t *new_seq_lens, int Hkv, int D,
                                              int block_size, int max_blocks, int num_blocks, tsv_dtype dtype,
                                              int32_t *compact_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the step: the slot plan, the rotary K/V append and single-token
+ * attention.  They read and write the same paged cache as the calls above (a block
+ * allocator on the device: vLLM PR #2188, "Guide for reviewers", preallocated slots).
+ * A decoding step is
+ *   tsv_kv_plan_slots -> (projection) tsv_rope_kv_append -> tsv_decode_attn     one token
+ *   tsv_kv_plan_slots -> tsv_rope_kv_append -> tsv_tree_verify_attn -> the walk  a tree
+ * with seq_lens of tsv_decode_attn = total_lens of the plan, and seq_lens of
+ * tsv_tree_verify_attn = seq_lens of the plan (its tree tokens are in the cache already).
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * Block tables, slot maps and positions from request lengths, on the device.
+ *
+ * Sequence b has L_b = seq_lens[b] cached tokens, n_b = new_lens[b] tokens about to be
+ * written and blocks_held[b] blocks (the first entries of its table row).  With
+ * want = ceil((L_b + n_b) / block_size):
+ *   1. sequences with want < held give back the blocks of entries want .. held-1, in
+ *      order of (b, entry), onto the stack free_blocks[0 .. free_count) (num_blocks
+ *      places); a finished request is L_b = n_b = 0.  The entries keep their old values;
+ *   2. sequences with want > held take want - held blocks from the top of that stack, in
+ *      order of (b, entry), into entries held .. want-1;
+ *   3. new token j of sequence b is token i = token_offsets[b] + j of the batch
+ *      (token_offsets[0 .. B]: running sums of new_lens) and gets
+ *      slot_map[i] = table[b, (L_b + j) / bs] * bs + (L_b + j) % bs   and
+ *      positions[i] = L_b + j, or, with `parent` [B, N] (a draft tree, n_b <= N; the
+ *      tree's rules are those of the attention call), L_b + depth of node j;
+ *      places of slot_map / positions past the last token are -1.
+ * blocks_held_out[b] = want, total_lens[b] = L_b + n_b, *free_count_out = blocks left.
+ * blocks_held_out, free_count_out and total_lens may be the input arrays blocks_held,
+ * free_count and seq_lens (in-place update); nothing else may overlap.  With separate
+ * outputs, and no change in between, a repeated call gives the same result.
+ *
+ * seq_err[b], overwritten: TSV_DERR_CAPACITY (negative length, L_b + n_b > max_blocks * bs,
+ * blocks_held[b] outside [0, max_blocks], tokens past max_tokens), TSV_DERR_PARENT
+ * (n_b > N), TSV_DERR_POOL (too few free blocks for this sequence after those before it --
+ * no later sequence that needs blocks gets any then; *free_count outside [0, num_blocks];
+ * more blocks given back than the pool has places for): the sequence keeps its
+ * blocks, total_lens[b] = L_b (0 for a negative length), its tokens get slot and position -1,
+ * the others are served.  TSV_DERR_BLOCK (a block id outside [0, num_blocks): its tokens'
+ * slots are -1; one given back goes onto the stack as it is) and TSV_DERR_PARENT for a
+ * parent row that is not a tree (positions of the nodes below the fault are -1) leave
+ * the rest of the sequence as planned.
+ * Negative lengths count as no tokens.  B <= 8192; block_size a power of two in
+ * [8, 128]; max_blocks * block_size, max_tokens and num_blocks up to 2^30.
+ * ------------------------------------------------------------------------- */
+tsv_status tsv_kv_plan_slots(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *parent,
+                             int32_t *block_table, const int32_t *blocks_held, int32_t *blocks_held_out,
+                             int32_t *free_blocks, const int32_t *free_count, int32_t *free_count_out,
+                             int32_t *total_lens, int32_t *token_offsets, int64_t *slot_map,
+                             int32_t *positions, int B, int N, int block_size, int max_blocks,
+                             int num_blocks, int max_tokens, int32_t *seq_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions and the K/V append.
+ *
+ * Token t's rows q[t] [Hq, D], k[t], v[t] [Hkv, D] start q_stride, k_stride, v_stride
+ * elements after the one before (heads and elements contiguous), so they may be parts of one
+ * projection's rows.  Pair i of a head's first rotary_dim elements turns by
+ * theta = positions[axis(i), t] * inv_freq[i] (positions [axes, T], inv_freq
+ * [rotary_dim / 2]):  (x, y) <- (x cos - y sin, y cos + x sin); the rest passes through.
+ * The turned q goes to q_out[t] (q_out_stride; q_out may be q with the same stride), the
+ * turned k and v to cache slot slot_map[t].  The angle is formed to about 2^-22 of a turn for
+ * |position| < 2^24.  Arithmetic is fp32, rounded once to dtype.
+ * slot_map[t] < 0 (padding): nothing is written to the cache and q_out[t] is zero.
+ * slot_map[t] >= num_blocks * block_size: nothing is written to the cache, q_out[t] is NaN
+ * and tok_err[t] = TSV_DERR_BLOCK (otherwise 0; one int32 per token, overwritten).
+ * Slots that are not negative must differ; q, k, v and the caches must not overlap
+ * (but for q_out = q).  D in {64, 128}; rotary_dim a multiple of 16; bases and strides
+ * 16-byte aligned.  opts NULL: {D, 0, 1, 0, {D / 2}}.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int rotary_dim;  /* elements of a head that turn */
+    int neighbours;  /* pairs: 0 -- (i, i + rotary_dim / 2), 1 -- (2i, 2i + 1) */
+    int axes;        /* position axes (time, height, width, ...): 1 to 4 */
+    int rounds;      /* which axis a pair takes: 0 -- section after section, 1 -- the axes in
+                        turn, an axis dropping out when its section is used up */
+    int sections[4]; /* pairs of each axis; their sum is rotary_dim / 2 */
+} tsv_rope_options;
+
+tsv_status tsv_rope_kv_append(const void *q, const void *k, const void *v, const int32_t *positions,
+                              const float *inv_freq, void *q_out, void *k_cache, void *v_cache,
+                              const int64_t *slot_map, int T, int Hq, int Hkv, int D, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t q_out_stride, int block_size,
+                              int num_blocks, tsv_dtype dtype, const tsv_rope_options *opts,
+                              int32_t *tok_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token per sequence over the paged cache.
+ *
+ * For query row (b, h), kv head g = h / (Hq / Hkv), keys = slots 0 .. L_b - 1 with
+ * L_b = seq_lens[b] (the new token's own K/V row included, already written):
+ *   out[b,h,:] = softmax_t(scale * q[b,h,:] . k[t,g,:]) @ v[t,g,:],
+ *   lse[b,h] = ln sum_t exp(scale * q[b,h,:] . k[t,g,:])   (lse may be NULL).
+ * q, out [B, Hq, D]; lse [B, Hq] fp32.  L_b = 0: out is zero and lse -infinity.
+ * Slots past L_b are never read into the result.  The keys of all sequences are divided
+ * evenly between the GPU's SMs; pieces of a sequence are joined by log-sum-exp in a fixed order, so a
+ * repeated call gives the same bits.  `workspace` as in tsv_tree_verify_attn, with
+ * tsv_decode_attn_workspace_size(...) bytes.
+ * seq_err[b]: TSV_DERR_CAPACITY (L_b < 0 or > max_blocks * block_size), TSV_DERR_BLOCK (a
+ * block id covering [0, L_b) outside [0, num_blocks)); rows of a flagged sequence are NaN.
+ * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128];
+ * max_blocks * block_size up to 2^30.
+ * ------------------------------------------------------------------------- */
+size_t tsv_decode_attn_workspace_size(int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
+                                      tsv_dtype dtype);
+
+tsv_status tsv_decode_attn(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_table, const int32_t *seq_lens, void *out, float *lse,
+                           int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
+                           int num_blocks, float scale, tsv_dtype dtype, void *workspace,
+                           size_t workspace_bytes, int32_t *seq_err, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Tree construction (host side).  Sequoia summary, sections "Scalable Speculative

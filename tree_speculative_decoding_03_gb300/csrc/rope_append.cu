@@ -1,0 +1,185 @@
+// rope_append.cu -- rotary positions of q and k on up to four axes, and the K/V rows
+// written into the paged cache at their slots, in one pass.
+//
+// Pair i of a head turns by theta = pos[axis(i)] * inv_freq[i]:
+//   (x, y) <- (x cos - y sin, y cos + x sin),
+// pairs (i, i + R/2) or (2i, 2i + 1) of the head's first R elements; the rest passes through.
+// q goes to q_out, k and v to cache row slot_map[t].
+//
+// The pass reads and writes every element once and is bound by memory.  The angles are the
+// same for all heads of a token, so a block forms the cosines and sines of its tokens once,
+// in shared memory, and each thread keeps those of its part of the head in registers while
+// it goes through the heads.  A thread's item is two 16-byte vectors of one head: with pairs
+// (i, i + R/2) vector c and its partner R/2 elements on, otherwise vectors 2c and 2c + 1.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "serving_args.cuh"
+
+namespace tsv {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+// cos and sin of pos * f.  The turn count pos * f / (2 pi) is formed as a pair of floats
+// (about 44 significant bits), its whole part dropped exactly, and the rest handed to
+// sincospif: far positions keep the accuracy of near ones (a float product at position 10^6
+// would be off by 0.03 rad).
+__device__ __forceinline__ float2 turn_of(int pos, float f) {
+    constexpr float kInvTwoPiHi = 0.15915494f;
+    constexpr float kInvTwoPiLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(0.15915494f));
+    const float fh = f * kInvTwoPiHi;
+    const float fl = fmaf(f, kInvTwoPiHi, -fh) + f * kInvTwoPiLo;
+    const float ph = static_cast<float>(pos);  // pos = ph + pl exactly
+    const float pl = static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph));
+    const float hi = ph * fh;
+    float lo = fmaf(ph, fh, -hi);
+    lo = fmaf(ph, fl, lo);
+    lo = fmaf(pl, fh, lo);
+    const float r = (hi - rintf(hi)) + lo;
+    float s, c;
+    sincospif(2.0f * r, &s, &c);
+    return make_float2(c, s);
+}
+
+template <typename T>
+struct Vec;  // one 16-byte vector
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void unpack(const uint4& u, float* x) {
+        x[0] = __uint_as_float(u.x);
+        x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z);
+        x[3] = __uint_as_float(u.w);
+    }
+    __device__ static uint4 pack(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void unpack(const uint4& u, float* x) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    // the one rounding of the result
+    __device__ static uint4 pack(const float* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Block: `tok` tokens x `hl` head lanes x D / (2 * vector) items of a head; blockIdx.y takes
+// every gridDim.y-th run of head lanes.
+template <typename T, int D, bool NEIGH>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a, int tok) {
+    constexpr int VN = Vec<T>::N, ITEMS = D / (2 * VN), LANES = kRopeThreads / ITEMS;
+    extern __shared__ float s_turn[];  // cos [tok][R / 2], then sin [tok][R / 2]
+    const int tid = threadIdx.x, half = a.R >> 1;
+    const int t0 = blockIdx.x * tok;
+    float* s_cos = s_turn;
+    float* s_sin = s_turn + tok * half;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = tid; i < tok * half; i += kRopeThreads) {
+        const int t = t0 + i / half, p = i % half;
+        float2 cs = make_float2(1.0f, 0.0f);
+        if (t < a.T) cs = turn_of(__ldg(a.positions + (long long)a.axis[p] * a.T + t), __ldg(a.inv_freq + p));
+        s_cos[i] = cs.x;
+        s_sin[i] = cs.y;
+    }
+    __syncthreads();
+    const int item = tid % ITEMS, lane = tid / ITEMS;
+    const int hl = LANES / tok;  // head lanes of a token
+    const int ti = lane / hl, h0 = lane % hl;
+    const int t = t0 + ti;
+    if (t >= a.T) return;
+    const long long slot = __ldg(a.slot_map + t);
+    const bool bad = slot >= a.slots, pad = slot < 0;
+    if (item == 0 && h0 == 0 && blockIdx.y == 0) a.tok_err[t] = bad ? TSV_DERR_BLOCK : 0;
+    // this thread's two vectors of a head, and whether they turn
+    const int turning = half / VN;  // items that turn
+    const bool turns = item < turning;
+    const int rest = a.R + (item - turning) * 2 * VN;
+    const int e0 = turns ? (NEIGH ? 2 * item * VN : item * VN) : rest;
+    const int e1 = turns ? (NEIGH ? e0 + VN : e0 + half) : rest + VN;
+    float cs[VN], sn[VN];
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+        cs[i] = turns ? s_cos[ti * half + item * VN + i] : 1.0f;
+        sn[i] = turns ? s_sin[ti * half + item * VN + i] : 0.0f;
+    }
+    const int heads = a.Hq + 2 * a.Hkv;
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride;
+    const T* v = static_cast<const T*>(a.v) + t * a.v_stride;
+    T* qo = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+    T* kc = static_cast<T*>(a.k_cache) + slot * a.Hkv * D;
+    T* vc = static_cast<T*>(a.v_cache) + slot * a.Hkv * D;
+    for (int h = blockIdx.y * hl + h0; h < heads; h += gridDim.y * hl) {
+        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+        if (!is_q && (pad || bad)) continue;
+        const T* src = is_q ? q + (long long)h * D : is_v ? v + (long long)(h - a.Hq - a.Hkv) * D : k + (long long)(h - a.Hq) * D;
+        T* dst = is_q ? qo + (long long)h * D : is_v ? vc + (long long)(h - a.Hq - a.Hkv) * D : kc + (long long)(h - a.Hq) * D;
+        uint4 u0, u1;
+        if (is_q && (pad || bad)) {  // a padding row is zero, a row with a bad slot NaN
+            float x[VN];
+#pragma unroll
+            for (int i = 0; i < VN; ++i) x[i] = bad ? __int_as_float(0x7fc00000) : 0.0f;
+            u0 = u1 = Vec<T>::pack(x);
+        } else {
+            u0 = *reinterpret_cast<const uint4*>(src + e0);
+            u1 = *reinterpret_cast<const uint4*>(src + e1);
+            if (turns && !is_v) {
+                float x[2 * VN];
+                Vec<T>::unpack(u0, x);
+                Vec<T>::unpack(u1, x + VN);
+#pragma unroll
+                for (int i = 0; i < VN; ++i) {
+                    float& p = x[NEIGH ? 2 * i : i];
+                    float& r = x[NEIGH ? 2 * i + 1 : i + VN];
+                    const float y = p * cs[i] - r * sn[i];
+                    r = r * cs[i] + p * sn[i];
+                    p = y;
+                }
+                u0 = Vec<T>::pack(x);
+                u1 = Vec<T>::pack(x + VN);
+            }
+        }
+        *reinterpret_cast<uint4*>(dst + e0) = u0;
+        *reinterpret_cast<uint4*>(dst + e1) = u1;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+    constexpr int ITEMS = D / (2 * Vec<T>::N), LANES = kRopeThreads / ITEMS;
+    // one token a block while that leaves SMs idle, four otherwise
+    const int tok = a.T <= 4 * num_sms ? 1 : 4;
+    const dim3 grid(static_cast<unsigned>((a.T + tok - 1) / tok), 1);
+    (void)LANES;
+    const size_t smem = (size_t)tok * a.R * sizeof(float);
+    return a.neighbours ? launch_pdl(rope_append_kernel<T, D, true>, grid, dim3(kRopeThreads), smem, stream, 1u, a, tok)
+                        : launch_pdl(rope_append_kernel<T, D, false>, grid, dim3(kRopeThreads), smem, stream, 1u, a, tok);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+    if (bf16)
+        return a.D == 64 ? launch_rope<__nv_bfloat16, 64>(a, num_sms, stream) : launch_rope<__nv_bfloat16, 128>(a, num_sms, stream);
+    return a.D == 64 ? launch_rope<float, 64>(a, num_sms, stream) : launch_rope<float, 128>(a, num_sms, stream);
+}
+
+}  // namespace tsv

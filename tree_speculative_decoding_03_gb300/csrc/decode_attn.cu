@@ -29,6 +29,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
+constexpr int kJoinRows = 4;  // query rows of a CTA of the join
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
@@ -565,60 +566,83 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
     }
 }
 
-// Joins the pieces of the units that lie on more than one CTA.  CTA k looks at the boundary
-// between lanes k and k + 1: when it falls inside a unit and is the first one there, this CTA
-// joins that unit's pieces, in lane order.
+// Joins the pieces of the units that lie on more than one CTA.  CTA (k, y) looks at the
+// boundary between lanes k and k + 1: when it falls inside a unit and is the first one there,
+// this CTA joins the unit's pieces, in lane order, for query rows [kJoinRows y, ...).  A row's
+// D / 4 threads read the pieces' rows as coalesced float4s, kAhead of them in flight.
 template <typename Elem, int D, int TILE>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-    __shared__ Place s_place;
-    __shared__ long long s_T;
-    const int tid = threadIdx.x;
+__global__ void __launch_bounds__(kJoinRows * D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int kAhead = 8;
+    // the schedule needs the lengths alone, which the kernel before this one has waited for
+    // before it let this one start
+    Place p;
+    const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x + 1, n, a.lanes); }, &p);
+    const long long s0 = lane_start(blockIdx.x, T, a.lanes), x = lane_start(blockIdx.x + 1, T, a.lanes);
+    const long long first = x - p.t;  // the unit's first tile
+    // not inside a unit; or an earlier boundary is; or an empty lane, whose end is no new boundary
+    const bool mine = x < T && p.t != 0 && s0 <= first && s0 != x;
+    const int c0 = blockIdx.x, c1 = mine ? lane_of_tile(first + p.tiles - 1, T, a.lanes) : c0;
+    const int side0 = s0 == first ? 0 : 1;
+    const int g = p.unit / a.groups, row0 = (p.unit % a.groups) * a.rows, nrows = min(a.rows, a.G - row0);
+    const int r = blockIdx.y * kJoinRows + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+    const bool sparse = T < a.lanes;  // some lanes are empty
     pdl_wait();
     pdl_launch_dependents();
-    if (tid < 32) {
-        Place p;
-        const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x + 1, n, a.lanes); }, &p);
-        if (tid == 0) {
-            s_place = p;
-            s_T = T;
+    if (!mine || r >= nrows) return;
+    // slot of piece c, or -1 for an empty lane
+    auto slot = [&](int c) {
+        if (sparse && lane_start(c + 1, T, a.lanes) == lane_start(c, T, a.lanes)) return -1;
+        return 2 * c + (c == c0 ? side0 : 0);
+    };
+    float M = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int bad = 0;
+    for (int c = c0; c <= c1; c += kAhead) {
+        float m[kAhead], l[kAhead];
+        float4 o[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int sl = c + i <= c1 ? slot(c + i) : -1;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+            o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (sl >= 0) {
+                const long long pr = (long long)sl * a.rows + r;
+                m[i] = a.part_m[pr];
+                l[i] = a.part_l[pr];
+                o[i] = *reinterpret_cast<const float4*>(a.part_o + pr * D + d);
+                bad |= a.part_bad[sl];
+            }
+        }
+        float m_new = M;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) m_new = fmaxf(m_new, m[i]);
+        const float ms = safe_max(m_new);
+        const float f0 = ex2(M - ms);
+        M = m_new;
+        sum *= f0;
+        acc.x *= f0;
+        acc.y *= f0;
+        acc.z *= f0;
+        acc.w *= f0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float f = ex2(m[i] - ms);
+            sum = fmaf(f, l[i], sum);
+            acc.x = fmaf(f, o[i].x, acc.x);
+            acc.y = fmaf(f, o[i].y, acc.y);
+            acc.z = fmaf(f, o[i].z, acc.z);
+            acc.w = fmaf(f, o[i].w, acc.w);
         }
     }
-    __syncthreads();
-    const long long T = s_T;
-    const long long x = lane_start(blockIdx.x + 1, T, a.lanes);
-    const Place p = s_place;
-    if (x >= T || p.t == 0) return;
-    const long long first = x - p.t;                       // the unit's first tile
-    if (lane_start(blockIdx.x, T, a.lanes) > first) return;  // an earlier boundary lies in this unit
-    if (lane_start(blockIdx.x, T, a.lanes) == x) return;     // an empty lane: its end is not a new boundary
-    const int c0 = blockIdx.x, c1 = lane_of_tile(first + p.tiles - 1, T, a.lanes);
-    const int side0 = lane_start(c0, T, a.lanes) == first ? 0 : 1;
-    const int g = p.unit / a.groups, row0 = (p.unit % a.groups) * a.rows, nrows = min(a.rows, a.G - row0);
-    bool bad = false;
-    for (int c = c0; c <= c1; ++c)
-        if (lane_start(c + 1, T, a.lanes) > lane_start(c, T, a.lanes)) bad |= a.part_bad[2 * c + (c == c0 ? side0 : 0)] != 0;
-    for (int e = tid; e < nrows * D; e += kThreads) {
-        const int r = e / D, d = e - r * D;
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; ++c) {
-            if (lane_start(c + 1, T, a.lanes) == lane_start(c, T, a.lanes)) continue;
-            M = fmaxf(M, a.part_m[(2LL * c + (c == c0 ? side0 : 0)) * a.rows + r]);
-        }
-        const float ms = safe_max(M);
-        float acc = 0.0f, sum = 0.0f;
-        for (int c = c0; c <= c1; ++c) {
-            if (lane_start(c + 1, T, a.lanes) == lane_start(c, T, a.lanes)) continue;
-            const long long pr = (2LL * c + (c == c0 ? side0 : 0)) * a.rows + r;
-            const float f = ex2(a.part_m[pr] - ms);
-            acc = fmaf(f, a.part_o[pr * D + d], acc);
-            sum = fmaf(f, a.part_l[pr], sum);
-        }
-        const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
-        const float nan = __int_as_float(0x7fc00000);
-        static_cast<Elem*>(a.out)[h * D + d] = to_elem<Elem>(bad ? nan : acc / sum);
-        if (d == 0 && a.lse != nullptr) a.lse[h] = bad ? nan : (M + log2f(sum)) * kLn2;
-    }
-    if (tid == 0 && p.unit == 0) a.seq_err[p.b] = bad ? TSV_DERR_BLOCK : 0;
+    const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
+    const float nan = __int_as_float(0x7fc00000), inv = 1.0f / sum;
+    const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    Elem* out = static_cast<Elem*>(a.out) + h * D + d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = to_elem<Elem>(bad ? nan : y[i]);
+    if (d == 0 && a.lse != nullptr) a.lse[h] = bad ? nan : (M + log2f(sum)) * kLn2;
+    if (d == 0 && r == 0 && p.unit == 0) a.seq_err[p.b] = bad ? TSV_DERR_BLOCK : 0;
 }
 
 template <typename Core>
@@ -635,8 +659,10 @@ cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
     }
     e = launch_pdl(decode_attn_kernel<Core>, dim3(static_cast<unsigned>(a.lanes)), dim3(kThreads), smem, stream, 1u, a);
     if (e != cudaSuccess || a.lanes < 2) return e;
+    const int most = min(a.rows, a.G);  // query rows of a unit
     return launch_pdl(decode_join_kernel<typename Core::Elem, Core::D, Core::KEYS * kWarps>,
-                      dim3(static_cast<unsigned>(a.lanes - 1)), dim3(kThreads), 0, stream, 1u, a);
+                      dim3(static_cast<unsigned>(a.lanes - 1), static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)),
+                      dim3(kJoinRows * Core::D / 4), 0, stream, 1u, a);
 }
 
 template <int D>

@@ -412,6 +412,14 @@ __device__ __forceinline__ __nv_bfloat16 to_elem<__nv_bfloat16>(float x) { retur
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// four elements of a result row: o / l, rounded once
+__device__ __forceinline__ void store_row(float* out, float4 o, float inv) {
+    *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* out, float4 o, float inv) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
 template <typename Core>
 constexpr size_t decode_smem() {
     constexpr size_t ring = (size_t)kWarps * kStages * Core::KEYS * Core::ROWB * 2;
@@ -430,20 +438,12 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
     float* s_m = reinterpret_cast<float*>(smem + (RING > JOIN ? RING : JOIN));  // [kWarps][ROWS]
     float* s_l = s_m + kWarps * ROWS;
     float* s_scratch = s_l + kWarps * ROWS;  // [kWarps][(KEYS + 1) * 8]
-    __shared__ Place s_place;
-    __shared__ long long s_T;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units = a.Hkv * a.groups, bs = 1 << a.bs_log2;
     pdl_wait();
     pdl_launch_dependents();
-    if (warp == 0) {
-        Place p;
-        const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x, n, a.lanes); }, &p);
-        if (lane == 0) {
-            s_place = p;
-            s_T = T;
-        }
-    }
+    Place p;  // found by every warp for itself: cheaper than a block barrier
+    const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x, n, a.lanes); }, &p);
     // sequences without keys: nothing to attend to (zeros), or a length that does not fit (NaN)
     for (int b = blockIdx.x; b < a.B; b += a.lanes) {
         if (seq_keys(a, b) > 0) continue;
@@ -455,11 +455,9 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
             for (int h = tid; h < a.Hq; h += kThreads) a.lse[(long long)b * a.Hq + h] = empty ? -INFINITY : x;
         if (tid == 0) a.seq_err[b] = empty ? 0 : TSV_DERR_CAPACITY;
     }
-    __syncthreads();
-    const long long T = s_T;
     long long x = lane_start(blockIdx.x, T, a.lanes);
     const long long x_end = lane_start(blockIdx.x + 1, T, a.lanes);
-    Place p = s_place;
+    const int row_elems = a.Hkv * D;  // elements from one slot to the next
     const uint32_t ring = smem_u32(smem) + warp * kStages * STAGE;
     float* scratch = s_scratch + warp * (KEYS + 1) * 8;
     Core core;
@@ -474,40 +472,49 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
         const Elem* vc = static_cast<const Elem*>(a.v_cache) + head;
         bool bad = false;
 
-        auto load = [&](int i) {  // the segment's i-th tile: this warp's KEYS keys of it
-            const uint32_t dst = ring + (i % kStages) * STAGE;
+        // this warp's KEYS keys of the segment's tiles: a run of 8 keys lies in one cache block
+        constexpr int RUNS = KEYS / 8, LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
+        int ids[RUNS];  // blocks of the next tile to load, fetched a step ahead
+        auto fetch = [&](int i) {
             const int key0 = (p.t + i) * TILE + warp * KEYS;
-            constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
 #pragma unroll
-            for (int r0 = 0; r0 < KEYS; r0 += ROWS_IT) {
-                const int row = r0 + lane / LANES_ROW, c = lane % LANES_ROW;
-                const int t = key0 + row;
-                bool take = t < p.keys;
-                long long at = 0;
-                if (take) {
-                    const int id = __ldg(bt + (t >> a.bs_log2));
-                    if (id < 0 || id >= a.num_blocks) {
-                        bad = true;
-                        take = false;
-                    } else {
-                        at = (((long long)id << a.bs_log2) + (t & (bs - 1))) * a.Hkv * D + c * (16 / (int)sizeof(Elem));
-                    }
+            for (int u = 0; u < RUNS; ++u) ids[u] = key0 + 8 * u < p.keys ? __ldg(bt + ((key0 + 8 * u) >> a.bs_log2)) : -2;
+        };
+        auto load = [&](int i) {
+            const uint32_t dst = ring + (i % kStages) * STAGE;
+            const int key0 = (p.t + i) * TILE + warp * KEYS, row = lane / LANES_ROW, c = lane % LANES_ROW;
+#pragma unroll
+            for (int u = 0; u < RUNS; ++u) {
+                const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
+                bad |= !in && ids[u] != -2;
+                const int t = key0 + 8 * u;
+                long long at = row * row_elems + c * (16 / (int)sizeof(Elem));
+                if (in) at += (((long long)ids[u] << a.bs_log2) + (t & (bs - 1))) * row_elems;
+#pragma unroll
+                for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
+                    const bool take = in && t + r0 + row < p.keys;
+                    const Elem* src = kc + (take ? at + (long long)r0 * row_elems : 0);
+                    cp16(dst + Core::place(8 * u + r0 + row, c), src, take);
+                    cp16(dst + HALF + Core::place(8 * u + r0 + row, c), vc + (src - kc), take);
                 }
-                cp16(dst + Core::place(row, c), kc + at, take);
-                cp16(dst + HALF + Core::place(row, c), vc + at, take);
             }
         };
         core.start(static_cast<const Elem*>(a.q) + ((long long)p.b * a.Hq + g * a.G + row0) * D, nrows);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            if (i < ntl) load(i);
+            if (i < ntl) {
+                fetch(i);
+                load(i);
+            }
             cp_commit();
         }
+        if (kStages - 1 < ntl) fetch(kStages - 1);
         for (int i = 0; i < ntl; ++i) {
             cp_wait<kStages - 2>();
             __syncwarp();
             if (i + kStages - 1 < ntl) load(i + kStages - 1);
             cp_commit();
+            if (i + kStages < ntl) fetch(i + kStages);
             const uint32_t src = ring + (i % kStages) * STAGE;
             const int live = p.keys - ((p.t + i) * TILE + warp * KEYS);
             if (live > 0) core.step(src, src + HALF, live, a.scale_log2, scratch);
@@ -517,28 +524,32 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
         const bool any_bad = __syncthreads_or(bad) != 0;  // and every warp's ring has drained
         core.finish(s_o + warp * ROWS * D, s_m + warp * ROWS, s_l + warp * ROWS);
         __syncthreads();
-        // the warps' states joined
+        // the warps' states joined, four elements of a row a thread
         const long long slot = (long long)blockIdx.x * 2 + (seg == 0 ? 0 : 1);
-        for (int e = tid; e < nrows * D; e += kThreads) {
-            const int r = e / D, d = e - r * D;
+        for (int e = tid; e < nrows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), d = (e % (D / 4)) * 4;
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * ROWS + r]);
             const float ms = safe_max(M);
-            float acc = 0.0f, sum = 0.0f;
+            float sum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = ex2(s_m[w * ROWS + r] - ms);
-                acc = fmaf(f, s_o[(w * ROWS + r) * D + d], acc);
+                const float4 o = *reinterpret_cast<const float4*>(s_o + (w * ROWS + r) * D + d);
                 sum = fmaf(f, s_l[w * ROWS + r], sum);
+                acc.x = fmaf(f, o.x, acc.x);
+                acc.y = fmaf(f, o.y, acc.y);
+                acc.z = fmaf(f, o.z, acc.z);
+                acc.w = fmaf(f, o.w, acc.w);
             }
             if (whole) {
                 const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
-                const float nan = __int_as_float(0x7fc00000);
-                static_cast<Elem*>(a.out)[h * D + d] = to_elem<Elem>(any_bad ? nan : acc / sum);
-                if (d == 0 && a.lse != nullptr) a.lse[h] = any_bad ? nan : (M + log2f(sum)) * kLn2;
+                store_row(static_cast<Elem*>(a.out) + h * D + d, acc, any_bad ? __int_as_float(0x7fc00000) : 1.0f / sum);
+                if (d == 0 && a.lse != nullptr) a.lse[h] = any_bad ? __int_as_float(0x7fc00000) : (M + log2f(sum)) * kLn2;
             } else {
-                a.part_o[(slot * a.rows + r) * D + d] = acc;
+                *reinterpret_cast<float4*>(a.part_o + (slot * a.rows + r) * D + d) = acc;
                 if (d == 0) {
                     a.part_m[slot * a.rows + r] = M;
                     a.part_l[slot * a.rows + r] = sum;
@@ -636,11 +647,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) decode_join_kernel(const __
         }
     }
     const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
-    const float nan = __int_as_float(0x7fc00000), inv = 1.0f / sum;
-    const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-    Elem* out = static_cast<Elem*>(a.out) + h * D + d;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = to_elem<Elem>(bad ? nan : y[i]);
+    const float nan = __int_as_float(0x7fc00000);
+    store_row(static_cast<Elem*>(a.out) + h * D + d, acc, bad ? nan : 1.0f / sum);
     if (d == 0 && a.lse != nullptr) a.lse[h] = bad ? nan : (M + log2f(sum)) * kLn2;
     if (d == 0 && r == 0 && p.unit == 0) a.seq_err[p.b] = bad ? TSV_DERR_BLOCK : 0;
 }

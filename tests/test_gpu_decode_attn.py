@@ -83,7 +83,7 @@ SHAPES = [  # lens, Hq, Hkv, D, bs
     ([31, 32, 33, 63, 64, 65, 127], 8, 1, 128, 16), ([128, 129, 1, 0, 255, 256, 257], 16, 2, 64, 32), ([1000, 3, 0, 77], 32, 8, 128, 16),
     ([511, 513], 20, 4, 64, 64), ([300] * 3, 17, 1, 128, 16), ([205, 1, 400], 32, 1, 64, 16), ([260, 33], 40, 1, 128, 128),
     ([190], 64, 1, 128, 16), ([20011], 8, 2, 128, 16), ([9000, 1, 4500, 0, 12345], 14, 2, 64, 8), (list(range(90)), 4, 4, 64, 16),
-    ([5] * 400, 8, 8, 64, 16), ([2049, 3000, 77, 640] * 9, 12, 4, 128, 32), ([4096] * 8, 32, 8, 128, 16)]
+    ([5] * 400, 8, 8, 64, 16), ([3, 0, 40] * 500, 2, 2, 64, 16), ([2049, 3000, 77, 640] * 9, 12, 4, 128, 32), ([4096] * 8, 32, 8, 128, 16)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -165,6 +165,17 @@ def test_bad_lengths_and_blocks(dtype):
     tsv.decode_attn(**d)
     check(h, d)
     assert d["seq_err"].tolist() == [0, 2, 4, 4, 2, 2]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [-1, -2, -2 ** 31, None])
+def test_every_bad_id_is_found(dtype, block):
+    h = make(40, [300, 17], 4, 2, 64, 16, dtype)
+    h["table"][0, 9] = h["kc"].shape[0] if block is None else block
+    d = on_device(h)
+    tsv.decode_attn(**d)
+    check(h, d)
+    assert d["seq_err"].tolist() == [2, 0]
 
 
 def test_two_graphs_share_a_workspace():

@@ -519,8 +519,9 @@ tsv_status tsv_decode_attn(const void* q, const void* k_cache, const void* v_cac
     a.out = out;
     a.lse = lse;
     a.seq_err = seq_err;
-    const size_t rows = 2 * (size_t)p.lanes * p.rows;
-    a.part_o = static_cast<float*>(workspace);
+    const size_t warps = (size_t)p.lanes * p.team, rows = 2 * warps * p.rows;
+    a.split = static_cast<int4*>(workspace);
+    a.part_o = reinterpret_cast<float*>(a.split + warps);
     a.part_m = a.part_o + rows * D;
     a.part_l = a.part_m + rows;
     a.part_bad = reinterpret_cast<int*>(a.part_l + rows);
@@ -531,6 +532,8 @@ tsv_status tsv_decode_attn(const void* q, const void* k_cache, const void* v_cac
     a.G = Hq / Hkv;
     a.rows = p.rows;
     a.groups = p.groups;
+    a.team = p.team;
+    a.by_unit = p.by_unit;
     a.lanes = p.lanes;
     a.bs_log2 = log2i(block_size);
     a.max_blocks = max_blocks;

@@ -7,17 +7,19 @@
 // multiply-adds per element), so the call is bound by the cache's bytes.
 //
 // Work split: a unit is (sequence, kv head, group of query rows).  Its keys are cut into tiles
-// of kTileKeys keys; the tiles of all units, sequence-major, form one row that is divided
-// evenly between `lanes` CTAs, so every CTA streams the same bytes whatever the mix of
-// lengths.  A CTA goes through its tiles as segments, one per unit it touches.  A segment that
-// is a whole unit writes the result; the others leave (m, l, O) in a slot of the workspace (a
-// CTA has at most two such segments, its first and its last), and a second kernel joins them:
-// O = sum_k 2^{m_k - M} O_k, l likewise, in the order of the CTAs, so a result does not depend
-// on timing.
+// of 16 (bf16) or 8 (fp32) keys.  `team` warps take as many units of one sequence together, each
+// warp one unit and all of them the same keys, so neighbouring heads of a cache row, which are
+// neighbours in memory, are read at about the same time.  The tiles of all teams' units,
+// sequence-major, form one row that is divided evenly between `lanes` teams, so every warp
+// streams the same bytes whatever the mix of lengths.  A warp goes through its tiles as
+// segments, one per unit it touches.  A segment that is a whole unit writes the result; the
+// others leave (m, l, O) in a slot of the workspace (a warp has at most two such segments, its
+// first and its last), and a second kernel joins them: O = sum_k 2^{m_k - M} O_k, l likewise, in
+// the order of the lanes, so a result does not depend on timing.
 //
-// Inside a CTA every warp has its own keys of each tile, its own ring of tiles in shared
-// memory filled with asynchronous copies, and its own running (m, l, O), so the main loop has
-// no block barrier; the warps' states are joined at the end of the segment.
+// A warp works for itself: its own ring of tiles in shared memory, filled with asynchronous
+// copies that run ahead across segment boundaries, its own running (m, l, O) in registers, and
+// no block barrier anywhere.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -28,8 +30,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kJoinRows = 4;  // query rows of a CTA of the join
+constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's share fill an SM's shared memory
+constexpr int kMaxTeam = 8;        // warps of a team
+constexpr int kMinTiles = 4;       // tiles of a lane, at least: fewer pieces to join when there is little work
+constexpr int kJoinRows = 2;       // query rows of a CTA of the join
+constexpr int kJoinGroups = 4;     // threads that share the pieces of an output element
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
@@ -81,7 +86,7 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0
 // product (relative error 2^-9 of each weight, averaged over the keys; l sums the unrounded P).
 template <int D_, int MT>
 struct Bf16Core {
-    static constexpr int D = D_, ROWS = 16 * MT, KEYS = 16, ROWB = D * 2, CH = ROWB / 16;
+    static constexpr int D = D_, KEYS = 16, ROWB = D * 2, CH = ROWB / 16;
     using Elem = __nv_bfloat16;
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4];
@@ -91,7 +96,8 @@ struct Bf16Core {
     // different banks
     static __device__ __forceinline__ uint32_t place(int row, int c) { return row * ROWB + ((c ^ (row & 7)) << 4); }
 
-    __device__ __forceinline__ void start(const Elem* q, int nrows) {
+    // loads a unit's query rows (the running state is untouched: this runs ahead of reset)
+    __device__ __forceinline__ void load_q(const Elem* q, int nrows) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -104,6 +110,11 @@ struct Bf16Core {
                 qf[t][kk][2] = r0 < nrows ? *reinterpret_cast<const uint32_t*>(p + r0 * D + 8) : 0u;
                 qf[t][kk][3] = r1 < nrows ? *reinterpret_cast<const uint32_t*>(p + r1 * D + 8) : 0u;
             }
+        }
+    }
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
             m[t][0] = m[t][1] = -INFINITY;
@@ -185,8 +196,9 @@ struct Bf16Core {
         }
     }
 
-    // this warp's state as rows of fp32: O [ROWS][D], then (m, l) of each row
-    __device__ __forceinline__ void finish(float* so, float* sm, float* sl) {
+    // hands each row's (row, m, l) and pieces of its O to the sink
+    template <typename Sink>
+    __device__ __forceinline__ void finish(int nrows, Sink sink, float*) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -196,13 +208,11 @@ struct Bf16Core {
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 const int row = 16 * t + 8 * r + (lane >> 2);
-                if ((lane & 3) == 0) {
-                    sm[row] = m[t][r];
-                    sl[row] = sum;
-                }
+                if (row >= nrows) continue;
+                if ((lane & 3) == 0) sink.row(row, m[t][r], sum);
+                const float inv = sink.factor(sum);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<float2*>(so + row * D + 8 * i + (lane & 3) * 2) = make_float2(o[t][i][2 * r], o[t][i][2 * r + 1]);
+                for (int i = 0; i < D / 8; ++i) sink.two(row, 8 * i + (lane & 3) * 2, o[t][i][2 * r] * inv, o[t][i][2 * r + 1] * inv);
             }
     }
 };
@@ -213,7 +223,7 @@ struct Bf16Core {
 // shared memory.
 template <int D_, int RR>
 struct F32Core {
-    static constexpr int D = D_, ROWS = RR, KEYS = 8, ROWB = D * 4, CH = ROWB / 16;
+    static constexpr int D = D_, KEYS = 8, ROWB = D * 4, CH = ROWB / 16;
     static constexpr int LPK = D / 8, KPP = 32 / LPK, PASSES = KEYS / KPP, DV = D / 32;
     using Elem = float;
     float qr[RR][8];
@@ -230,7 +240,7 @@ struct F32Core {
         return row;
     }
 
-    __device__ __forceinline__ void start(const Elem* q, int nrows) {
+    __device__ __forceinline__ void load_q(const Elem* q, int nrows) {
         const int i = (threadIdx.x & 31) % LPK;
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
@@ -242,9 +252,13 @@ struct F32Core {
                 qr[r][4 * h + 2] = x.z;
                 qr[r][4 * h + 3] = x.w;
             }
+        }
+    }
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int r = 0; r < RR; ++r)
 #pragma unroll
             for (int d = 0; d < DV; ++d) o[r][d] = 0.0f;
-        }
         m = -INFINITY;
         l = 0.0f;
     }
@@ -330,19 +344,26 @@ struct F32Core {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void finish(float* so, float* sm, float* sl) {
+    template <typename Sink>
+    __device__ __forceinline__ void finish(int nrows, Sink sink, float* scratch) {
         const int lane = threadIdx.x & 31, i = lane % LPK;
         float sum = l;
 #pragma unroll
         for (int y = LPK; y < 32; y <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
         if (lane < LPK && i % (LPK / RR) == 0) {
-            sm[my_row()] = m;
-            sl[my_row()] = sum;
+            const int row = my_row();
+            scratch[row] = sum;
+            if (row < nrows) sink.row(row, m, sum);
         }
+        __syncwarp();
 #pragma unroll
-        for (int r = 0; r < RR; ++r)
+        for (int r = 0; r < RR; ++r) {
+            if (r >= nrows) continue;
+            const float inv = sink.factor(scratch[r]);
 #pragma unroll
-            for (int d = 0; d < DV; ++d) so[r * D + lane * DV + d] = o[r][d];
+            for (int d = 0; d < DV; d += 2) sink.two(r, lane * DV + d, o[r][d] * inv, o[r][d + 1] * inv);
+        }
+        __syncwarp();
     }
 };
 
@@ -359,48 +380,92 @@ __device__ __forceinline__ int lane_of_tile(long long x, long long T, int lanes)
     return static_cast<int>(((x + 1) * lanes - 1) / T);
 }
 
-struct Place {   // global tile x lies in unit `unit` of sequence b (of `keys` keys), tile t of its `tiles`
+// Lanes that share T tiles.
+__device__ __forceinline__ int lanes_of(long long T, int lanes) {
+    const long long n = T / kMinTiles;
+    return n < 1 ? 1 : n < lanes ? static_cast<int>(n) : lanes;
+}
+
+// A position in the row of tiles: tile t of the `tiles` of unit `unit` of sequence b, which has
+// `keys` keys.  A team's warps differ in the unit alone.
+struct Place {
     int b, unit, t, tiles, keys;
+    template <int TILE>
+    __device__ __forceinline__ void next(const DecodeArgs& a) {
+        if (++t < tiles) return;
+        t = 0;
+        unit += a.team;
+        const int units = a.Hkv * a.groups;
+        if (unit < units) return;
+        unit -= units;
+        do {
+            ++b;
+            keys = b < a.B ? seq_keys(a, b) : 1;
+        } while (keys == 0);
+        tiles = (keys + TILE - 1) / TILE;
+    }
 };
 
-// One warp: all tiles of the call, and where tile run_start(T) lies.
-template <int TILE, typename F>
-__device__ __forceinline__ long long locate(const DecodeArgs& a, F run_start, Place* p) {
-    const int lane = threadIdx.x & 31, units = a.Hkv * a.groups;
-    long long T = 0;
-    for (int b = lane; b < a.B; b += 32) T += (seq_keys(a, b) + TILE - 1) / TILE;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
-    T *= units;
-    const long long x = run_start(T);
-    *p = Place{0, 0, 0, 1, 0};
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B && x < T; b0 += 32) {
-        const int b = b0 + lane;
+// One warp: the tiles [x, x_end) of lane `which` and where x lies, for the team's warp `member`;
+// T = all tiles.
+template <int TILE>
+__device__ __forceinline__ Place locate(const DecodeArgs& a, int which, int member, long long* x_, long long* x_end, long long* T_) {
+    const int lane = threadIdx.x & 31, units = a.Hkv * a.groups / a.team;
+    // a run of sequences to each lane: their tiles, then a scan over the lanes
+    const int run = (a.B + 31) >> 5;
+    long long mine = 0;
+    int keys0 = 0;
+    for (int j = 0; j < run; ++j) {
+        const int b = lane * run + j;
         const int keys = b < a.B ? seq_keys(a, b) : 0;
-        const int tiles = (keys + TILE - 1) / TILE;
+        if (j == 0) keys0 = keys;
+        mine += (keys + TILE - 1) / TILE;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const long long T = __shfl_sync(0xffffffffu, incl, 31) * units;
+    const int lanes = lanes_of(T, a.lanes);
+    const long long x = which < lanes ? lane_start(which, T, lanes) : T;
+    *x_ = x;
+    *x_end = which < lanes ? lane_start(which + 1, T, lanes) : T;
+    *T_ = T;
+    Place p{0, 0, 0, 1, 0};
+    if (x >= T) return p;
+    const unsigned holds = __ballot_sync(0xffffffffu, (incl - mine) * units <= x && x < incl * units);
+    const int owner = __ffs(holds) - 1;
+    long long base = __shfl_sync(0xffffffffu, incl - mine, owner) * units;
+    for (int j0 = 0; j0 < run; j0 += 32) {
+        const int b = owner * run + j0 + lane;
+        const bool in = j0 + lane < run && b < a.B;
+        const int keys = run == 1 ? __shfl_sync(0xffffffffu, keys0, owner) : (in ? seq_keys(a, b) : 0);
+        const int tiles = in ? (keys + TILE - 1) / TILE : 0;
         const long long w = (long long)tiles * units;
-        long long incl = w;
+        long long end = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            const long long y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
         }
-        const long long excl = base + incl - w;
-        const unsigned hit = __ballot_sync(0xffffffffu, w > 0 && excl <= x && x < excl + w);
+        end += base;
+        const unsigned hit = __ballot_sync(0xffffffffu, end - w <= x && x < end);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            const long long off = x - excl;
-            p->b = __shfl_sync(0xffffffffu, b, src);
-            p->unit = __shfl_sync(0xffffffffu, static_cast<int>(off / (tiles > 0 ? tiles : 1)), src);
-            p->t = __shfl_sync(0xffffffffu, static_cast<int>(off % (tiles > 0 ? tiles : 1)), src);
-            p->tiles = __shfl_sync(0xffffffffu, tiles, src);
-            p->keys = __shfl_sync(0xffffffffu, keys, src);
+            const long long off = x - __shfl_sync(0xffffffffu, end - w, src);
+            p.b = owner * run + j0 + src;
+            p.tiles = __shfl_sync(0xffffffffu, tiles, src);
+            p.keys = __shfl_sync(0xffffffffu, keys, src);
+            p.unit = static_cast<int>(off / p.tiles);
+            p.t = static_cast<int>(off - (long long)p.unit * p.tiles);
+            p.unit = p.unit * a.team + member;
             break;
         }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        base = __shfl_sync(0xffffffffu, end, 31);
     }
-    return T;
+    return p;
 }
 
 template <typename T>
@@ -412,40 +477,55 @@ __device__ __forceinline__ __nv_bfloat16 to_elem<__nv_bfloat16>(float x) { retur
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// four elements of a result row: o / l, rounded once
-__device__ __forceinline__ void store_row(float* out, float4 o, float inv) {
-    *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* out, float4 o, float inv) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-}
+// Where a segment's rows go: the result (a whole unit), or a slot of the workspace.
+template <typename Elem, int D>
+struct ToResult {
+    Elem* out;   // the unit's first row
+    float* lse;  // or nullptr
+    bool bad;    // a block id outside the cache: NaN
+    __device__ __forceinline__ void row(int r, float m, float l) const {
+        if (lse != nullptr) lse[r] = bad ? __int_as_float(0x7fc00000) : (m + log2f(l)) * kLn2;
+    }
+    __device__ __forceinline__ float factor(float l) const { return bad ? __int_as_float(0x7fc00000) : 1.0f / l; }
+    __device__ __forceinline__ void two(int r, int d, float x, float y) const { store2(out + r * D + d, x, y); }
+    // the one rounding of the result
+    static __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+    static __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
+    }
+};
+template <int D>
+struct ToSlot {
+    float *o, *m, *l;  // of the slot
+    __device__ __forceinline__ void row(int r, float m_, float l_) const {
+        m[r] = m_;
+        l[r] = l_;
+    }
+    __device__ __forceinline__ float factor(float) const { return 1.0f; }
+    __device__ __forceinline__ void two(int r, int d, float x, float y) const {
+        *reinterpret_cast<float2*>(o + r * D + d) = make_float2(x, y);
+    }
+};
 
 template <typename Core>
-constexpr size_t decode_smem() {
-    constexpr size_t ring = (size_t)kWarps * kStages * Core::KEYS * Core::ROWB * 2;
-    constexpr size_t join = (size_t)kWarps * Core::ROWS * Core::D * 4;
-    return (ring > join ? ring : join) + kWarps * 2 * Core::ROWS * 4 + kWarps * (Core::KEYS + 1) * 8 * 4;
-}
+__host__ __device__ constexpr int stages_of() { return kRingBytes / (2 * Core::KEYS * Core::ROWB); }
+template <typename Core>
+constexpr size_t decode_smem() { return (size_t)kWarps * (kRingBytes + 72 * sizeof(float)); }
 
 template <typename Core>
-__global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_constant__ DecodeArgs a) {
     using Elem = typename Core::Elem;
-    constexpr int D = Core::D, KEYS = Core::KEYS, ROWS = Core::ROWS, TILE = KEYS * kWarps;
+    constexpr int D = Core::D, KEYS = Core::KEYS, STAGES = stages_of<Core>(), RUNS = KEYS / 8;
     constexpr uint32_t HALF = KEYS * Core::ROWB, STAGE = 2 * HALF;
-    constexpr size_t RING = (size_t)kWarps * kStages * STAGE, JOIN = (size_t)kWarps * ROWS * D * 4;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* s_o = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D], after the ring has drained
-    float* s_m = reinterpret_cast<float*>(smem + (RING > JOIN ? RING : JOIN));  // [kWarps][ROWS]
-    float* s_l = s_m + kWarps * ROWS;
-    float* s_scratch = s_l + kWarps * ROWS;  // [kWarps][(KEYS + 1) * 8]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int units = a.Hkv * a.groups, bs = 1 << a.bs_log2;
+    const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * 72;
+    const int units = a.Hkv * a.groups;
     pdl_wait();
     pdl_launch_dependents();
-    Place p;  // found by every warp for itself: cheaper than a block barrier
-    const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x, n, a.lanes); }, &p);
     // sequences without keys: nothing to attend to (zeros), or a length that does not fit (NaN)
-    for (int b = blockIdx.x; b < a.B; b += a.lanes) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (seq_keys(a, b) > 0) continue;
         const bool empty = __ldg(a.seq_lens + b) == 0;
         const float x = empty ? 0.0f : __int_as_float(0x7fc00000);
@@ -454,175 +534,166 @@ __global__ void __launch_bounds__(kThreads) decode_attn_kernel(const __grid_cons
         if (a.lse != nullptr)
             for (int h = tid; h < a.Hq; h += kThreads) a.lse[(long long)b * a.Hq + h] = empty ? -INFINITY : x;
         if (tid == 0) a.seq_err[b] = empty ? 0 : TSV_DERR_CAPACITY;
+        if (a.by_unit)
+            for (int u = tid; u < units; u += kThreads) a.split[(long long)b * units + u] = make_int4(b, u, -1, 0);
     }
-    long long x = lane_start(blockIdx.x, T, a.lanes);
-    const long long x_end = lane_start(blockIdx.x + 1, T, a.lanes);
-    const int row_elems = a.Hkv * D;  // elements from one slot to the next
-    const uint32_t ring = smem_u32(smem) + warp * kStages * STAGE;
-    float* scratch = s_scratch + warp * (KEYS + 1) * 8;
-    Core core;
-    for (int seg = 0; x < x_end; ++seg) {
-        const int g = p.unit / a.groups, row0 = (p.unit % a.groups) * a.rows;
-        const int nrows = min(a.rows, a.G - row0);
-        const int ntl = static_cast<int>(min((long long)(p.tiles - p.t), x_end - x));
-        const bool whole = ntl == p.tiles;
-        const int32_t* bt = a.block_table + (long long)p.b * a.max_blocks;
-        const long long head = (long long)g * D;
-        const Elem* kc = static_cast<const Elem*>(a.k_cache) + head;
-        const Elem* vc = static_cast<const Elem*>(a.v_cache) + head;
-        bool bad = false;
+    const int me = blockIdx.x * kWarps + warp;
+    const int lane_me = me / a.team;
+    if (lane_me >= a.lanes) return;
+    long long x, x_end, T;
+    Place p = locate<KEYS>(a, lane_me, me % a.team, &x, &x_end, &T);
+    // for the join: a unit's last lane, where this lane leaves its first piece
+    int4 left = make_int4(0, 0, -1, 0);
+    const int n = static_cast<int>(x_end - x), row_elems = a.Hkv * D;
+    const Elem* kc = static_cast<const Elem*>(a.k_cache);
+    const Elem* vc = static_cast<const Elem*>(a.v_cache);
 
-        // this warp's KEYS keys of the segment's tiles: a run of 8 keys lies in one cache block
-        constexpr int RUNS = KEYS / 8, LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
-        int ids[RUNS];  // blocks of the next tile to load, fetched a step ahead
-        auto fetch = [&](int i) {
-            const int key0 = (p.t + i) * TILE + warp * KEYS;
+    // The copies run STAGES - 1 tiles ahead and the block ids one more: `f` is the tile whose
+    // ids are fetched last, `ids` its blocks (8 keys lie in one block).  All lanes hold the same
+    // ids.
+    Place f = p;
+    int ids[RUNS];
+    uint32_t bad_stage = 0;  // stages holding a tile with a block id outside the cache
+    auto fetch = [&] {
+        const int32_t* bt = a.block_table + (long long)f.b * a.max_blocks;
 #pragma unroll
-            for (int u = 0; u < RUNS; ++u) ids[u] = key0 + 8 * u < p.keys ? __ldg(bt + ((key0 + 8 * u) >> a.bs_log2)) : -2;
-        };
-        auto load = [&](int i) {
-            const uint32_t dst = ring + (i % kStages) * STAGE;
-            const int key0 = (p.t + i) * TILE + warp * KEYS, row = lane / LANES_ROW, c = lane % LANES_ROW;
-#pragma unroll
-            for (int u = 0; u < RUNS; ++u) {
-                const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
-                bad |= !in && ids[u] != -2;
-                const int t = key0 + 8 * u;
-                long long at = row * row_elems + c * (16 / (int)sizeof(Elem));
-                if (in) at += (((long long)ids[u] << a.bs_log2) + (t & (bs - 1))) * row_elems;
-#pragma unroll
-                for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
-                    const bool take = in && t + r0 + row < p.keys;
-                    const Elem* src = kc + (take ? at + (long long)r0 * row_elems : 0);
-                    cp16(dst + Core::place(8 * u + r0 + row, c), src, take);
-                    cp16(dst + HALF + Core::place(8 * u + r0 + row, c), vc + (src - kc), take);
-                }
-            }
-        };
-        core.start(static_cast<const Elem*>(a.q) + ((long long)p.b * a.Hq + g * a.G + row0) * D, nrows);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (i < ntl) {
-                fetch(i);
-                load(i);
-            }
-            cp_commit();
+        for (int u = 0; u < RUNS; ++u) {
+            const int key = f.t * KEYS + 8 * u;
+            ids[u] = key < f.keys ? __ldg(bt + (key >> a.bs_log2)) : 0;
         }
-        if (kStages - 1 < ntl) fetch(kStages - 1);
-        for (int i = 0; i < ntl; ++i) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            if (i + kStages - 1 < ntl) load(i + kStages - 1);
-            cp_commit();
-            if (i + kStages < ntl) fetch(i + kStages);
-            const uint32_t src = ring + (i % kStages) * STAGE;
-            const int live = p.keys - ((p.t + i) * TILE + warp * KEYS);
-            if (live > 0) core.step(src, src + HALF, live, a.scale_log2, scratch);
-            __syncwarp();
-        }
-        cp_wait<0>();
-        const bool any_bad = __syncthreads_or(bad) != 0;  // and every warp's ring has drained
-        core.finish(s_o + warp * ROWS * D, s_m + warp * ROWS, s_l + warp * ROWS);
-        __syncthreads();
-        // the warps' states joined, four elements of a row a thread
-        const long long slot = (long long)blockIdx.x * 2 + (seg == 0 ? 0 : 1);
-        for (int e = tid; e < nrows * (D / 4); e += kThreads) {
-            const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-            float M = -INFINITY;
+    };
+    constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
+    const int lrow = lane / LANES_ROW, lch = lane % LANES_ROW;
+    const int lane_elems = lrow * row_elems + lch * (16 / (int)sizeof(Elem));
+    auto load = [&](int stage) {
+        const uint32_t dst = ring + stage * STAGE;
+        const long long head = (long long)(f.unit / a.groups) * D + lane_elems;
+        bool bad = false;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w * ROWS + r]);
-            const float ms = safe_max(M);
-            float sum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int u = 0; u < RUNS; ++u) {
+            const int key = f.t * KEYS + 8 * u;
+            const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
+            bad |= !in && key < f.keys;
+            const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(s_m[w * ROWS + r] - ms);
-                const float4 o = *reinterpret_cast<const float4*>(s_o + (w * ROWS + r) * D + d);
-                sum = fmaf(f, s_l[w * ROWS + r], sum);
-                acc.x = fmaf(f, o.x, acc.x);
-                acc.y = fmaf(f, o.y, acc.y);
-                acc.z = fmaf(f, o.z, acc.z);
-                acc.w = fmaf(f, o.w, acc.w);
-            }
-            if (whole) {
-                const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
-                store_row(static_cast<Elem*>(a.out) + h * D + d, acc, any_bad ? __int_as_float(0x7fc00000) : 1.0f / sum);
-                if (d == 0 && a.lse != nullptr) a.lse[h] = any_bad ? __int_as_float(0x7fc00000) : (M + log2f(sum)) * kLn2;
-            } else {
-                *reinterpret_cast<float4*>(a.part_o + (slot * a.rows + r) * D + d) = acc;
-                if (d == 0) {
-                    a.part_m[slot * a.rows + r] = M;
-                    a.part_l[slot * a.rows + r] = sum;
-                }
+            for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
+                const bool take = in && key + r0 + lrow < f.keys;
+                const long long off = take ? at + (long long)r0 * row_elems : 0;
+                cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
+                cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
             }
         }
-        if (tid == 0) {
-            if (!whole)
-                a.part_bad[slot] = any_bad ? 1 : 0;
-            else if (p.unit == 0)
-                a.seq_err[p.b] = any_bad ? TSV_DERR_BLOCK : 0;
+        bad_stage = (bad_stage & ~(1u << stage)) | (bad ? 1u << stage : 0u);
+    };
+    auto q_of = [&](const Place& u) {
+        return static_cast<const Elem*>(a.q) + ((long long)u.b * a.Hq + (u.unit / a.groups) * a.G + (u.unit % a.groups) * a.rows) * D;
+    };
+    auto rows_of = [&](const Place& u) { return min(a.rows, a.G - (u.unit % a.groups) * a.rows); };
+
+    Core core;
+    int loaded = 0;
+    if (n > 0) {
+        fetch();
+        core.load_q(q_of(p), rows_of(p));
+        core.reset();
+    }
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (loaded < n) {
+            load(i);
+            if (++loaded < n) {
+                f.next<KEYS>(a);
+                fetch();
+            }
         }
-        __syncthreads();
-        x += ntl;
-        // the next unit that has keys
-        p.t = 0;
-        if (++p.unit == units) {
-            p.unit = 0;
-            do {
-                ++p.b;
-                p.keys = p.b < a.B ? seq_keys(a, p.b) : 1;
-            } while (p.keys == 0);
-            p.tiles = (p.keys + TILE - 1) / TILE;
+        cp_commit();
+    }
+    bool seg_bad = false;
+    int seg = 0, stage = 0, fill = STAGES - 1, t_first = p.t;
+    for (int i = 0; i < n; ++i) {
+        cp_wait<STAGES - 2>();
+        __syncwarp();
+        if (loaded < n) {
+            load(fill);
+            if (++loaded < n) {
+                f.next<KEYS>(a);
+                fetch();
+            }
+        }
+        cp_commit();
+        if (++fill == STAGES) fill = 0;
+        seg_bad |= ((bad_stage >> stage) & 1u) != 0;
+        const uint32_t src = ring + stage * STAGE;
+        core.step(src, src + HALF, p.keys - p.t * KEYS, a.scale_log2, scratch);
+        __syncwarp();
+        if (++stage == STAGES) stage = 0;
+        if (p.t + 1 < p.tiles && i + 1 < n) {
+            ++p.t;
+            continue;
+        }
+        // the segment's end
+        const int nrows = rows_of(p);
+        if (t_first == 0 && p.t + 1 == p.tiles) {
+            const long long h = (long long)p.b * a.Hq + (p.unit / a.groups) * a.G + (p.unit % a.groups) * a.rows;
+            core.finish(nrows, ToResult<Elem, D>{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, seg_bad}, scratch);
+            if (p.unit == 0 && lane == 0) a.seq_err[p.b] = seg_bad ? TSV_DERR_BLOCK : 0;
+            if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
+        } else {
+            const long long slot = 2LL * me + (seg == 0 ? 0 : 1);
+            core.finish(nrows, ToSlot<D>{a.part_o + slot * a.rows * D, a.part_m + slot * a.rows, a.part_l + slot * a.rows}, scratch);
+            if (lane == 0) a.part_bad[slot] = seg_bad;
+            if (t_first == 0) {
+                left = make_int4(p.b, p.unit, lane_of_tile(x + i - p.t + p.tiles - 1, T, lanes_of(T, a.lanes)), me * 2 + (seg == 0 ? 0 : 1));
+                if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
+            }
+        }
+        if (i + 1 < n) {
+            p.next<KEYS>(a);
+            t_first = 0;
+            seg_bad = false;
+            ++seg;
+            core.load_q(q_of(p), rows_of(p));
+            core.reset();
         }
     }
+    if (!a.by_unit && lane == 0) a.split[me] = left;
 }
 
-// Joins the pieces of the units that lie on more than one CTA.  CTA (k, y) looks at the
-// boundary between lanes k and k + 1: when it falls inside a unit and is the first one there,
-// this CTA joins the unit's pieces, in lane order, for query rows [kJoinRows y, ...).  A row's
-// D / 4 threads read the pieces' rows as coalesced float4s, kAhead of them in flight.
-template <typename Elem, int D, int TILE>
-__global__ void __launch_bounds__(kJoinRows * D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int kAhead = 8;
-    // the schedule needs the lengths alone, which the kernel before this one has waited for
-    // before it let this one start
-    Place p;
-    const long long T = locate<TILE>(a, [&](long long n) { return lane_start(blockIdx.x + 1, n, a.lanes); }, &p);
-    const long long s0 = lane_start(blockIdx.x, T, a.lanes), x = lane_start(blockIdx.x + 1, T, a.lanes);
-    const long long first = x - p.t;  // the unit's first tile
-    // not inside a unit; or an earlier boundary is; or an empty lane, whose end is no new boundary
-    const bool mine = x < T && p.t != 0 && s0 <= first && s0 != x;
-    const int c0 = blockIdx.x, c1 = mine ? lane_of_tile(first + p.tiles - 1, T, a.lanes) : c0;
-    const int side0 = s0 == first ? 0 : 1;
-    const int g = p.unit / a.groups, row0 = (p.unit % a.groups) * a.rows, nrows = min(a.rows, a.G - row0);
-    const int r = blockIdx.y * kJoinRows + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
-    const bool sparse = T < a.lanes;  // some lanes are empty
+// Joins the pieces of the units that lie on more than one lane, in lane order.  CTA (k, y) joins
+// query rows [kJoinRows y, ...) of the k-th unit, or of the unit whose first piece warp k has left,
+// whichever are fewer.  kJoinGroups threads share an element's pieces, each with kAhead of them in
+// flight.
+template <typename Elem, int D>
+__global__ void __launch_bounds__(kJoinRows* kJoinGroups* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+    constexpr int kAhead = 8, VEC = D / 4;
+    __shared__ float s_part[kJoinGroups - 1][kJoinRows * VEC][6];
     pdl_wait();
     pdl_launch_dependents();
-    if (!mine || r >= nrows) return;
-    // slot of piece c, or -1 for an empty lane
-    auto slot = [&](int c) {
-        if (sparse && lane_start(c + 1, T, a.lanes) == lane_start(c, T, a.lanes)) return -1;
-        return 2 * c + (c == c0 ? side0 : 0);
-    };
+    const int4 sp = a.split[blockIdx.x];
+    if (sp.z < 0) return;
+    const int first_warp = sp.w >> 1, member = first_warp % a.team, k = first_warp / a.team, last = sp.z;
+    const int b = sp.x, unit = sp.y;
+    const int row0 = (unit % a.groups) * a.rows, nrows = min(a.rows, a.G - row0);
+    const int e = threadIdx.x % (kJoinRows * VEC), grp = threadIdx.x / (kJoinRows * VEC);
+    const int r = blockIdx.y * kJoinRows + e / VEC, d = (e % VEC) * 4;
+    if (blockIdx.y * kJoinRows >= nrows) return;
     float M = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int bad = 0;
-    for (int c = c0; c <= c1; c += kAhead) {
+    for (int c = k + grp * kAhead; c <= last; c += kAhead * kJoinGroups) {
         float m[kAhead], l[kAhead];
         float4 o[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int sl = c + i <= c1 ? slot(c + i) : -1;
             m[i] = -INFINITY;
             l[i] = 0.0f;
             o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (sl >= 0) {
-                const long long pr = (long long)sl * a.rows + r;
+            if (c + i <= last && r < nrows) {
+                const long long slot = 2LL * ((c + i) * a.team + member) + (c + i == k ? sp.w & 1 : 0), pr = slot * a.rows + r;
                 m[i] = a.part_m[pr];
                 l[i] = a.part_l[pr];
                 o[i] = *reinterpret_cast<const float4*>(a.part_o + pr * D + d);
-                bad |= a.part_bad[sl];
+                bad |= a.part_bad[slot];
             }
         }
         float m_new = M;
@@ -632,25 +703,41 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) decode_join_kernel(const __
         const float f0 = ex2(M - ms);
         M = m_new;
         sum *= f0;
-        acc.x *= f0;
-        acc.y *= f0;
-        acc.z *= f0;
-        acc.w *= f0;
+        acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const float f = ex2(m[i] - ms);
             sum = fmaf(f, l[i], sum);
-            acc.x = fmaf(f, o[i].x, acc.x);
-            acc.y = fmaf(f, o[i].y, acc.y);
-            acc.z = fmaf(f, o[i].z, acc.z);
-            acc.w = fmaf(f, o[i].w, acc.w);
+            acc = make_float4(fmaf(f, o[i].x, acc.x), fmaf(f, o[i].y, acc.y), fmaf(f, o[i].z, acc.z), fmaf(f, o[i].w, acc.w));
         }
     }
-    const long long h = (long long)p.b * a.Hq + g * a.G + row0 + r;
-    const float nan = __int_as_float(0x7fc00000);
-    store_row(static_cast<Elem*>(a.out) + h * D + d, acc, bad ? nan : 1.0f / sum);
-    if (d == 0 && a.lse != nullptr) a.lse[h] = bad ? nan : (M + log2f(sum)) * kLn2;
-    if (d == 0 && r == 0 && p.unit == 0) a.seq_err[p.b] = bad ? TSV_DERR_BLOCK : 0;
+    if (grp > 0) {
+        float* s = s_part[grp - 1][e];
+        s[0] = M;
+        s[1] = sum;
+        s[2] = acc.x;
+        s[3] = acc.y;
+        s[4] = acc.z;
+        s[5] = acc.w;
+    }
+    bad = __syncthreads_or(bad);
+    if (grp > 0 || r >= nrows) return;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups - 1; ++i) {
+        const float* s = s_part[i][e];
+        const float m_new = fmaxf(M, s[0]), ms = safe_max(m_new);
+        const float f0 = ex2(M - ms), f1 = ex2(s[0] - ms);
+        M = m_new;
+        sum = sum * f0 + s[1] * f1;
+        acc = make_float4(acc.x * f0 + s[2] * f1, acc.y * f0 + s[3] * f1, acc.z * f0 + s[4] * f1, acc.w * f0 + s[5] * f1);
+    }
+    const long long h = (long long)b * a.Hq + (unit / a.groups) * a.G + row0 + r;
+    const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, bad != 0};
+    const float inv = to.factor(sum);
+    to.two(0, d, acc.x * inv, acc.y * inv);
+    to.two(0, d + 2, acc.z * inv, acc.w * inv);
+    if (d == 0) to.row(0, M, sum);
+    if (d == 0 && r == 0 && unit == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : 0;
 }
 
 template <typename Core>
@@ -665,12 +752,14 @@ cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         smem_dev = dev;
     }
-    e = launch_pdl(decode_attn_kernel<Core>, dim3(static_cast<unsigned>(a.lanes)), dim3(kThreads), smem, stream, 1u, a);
+    const int warps = a.lanes * a.team;
+    e = launch_pdl(decode_attn_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), smem,
+                   stream, 1u, a);
     if (e != cudaSuccess || a.lanes < 2) return e;
     const int most = min(a.rows, a.G);  // query rows of a unit
-    return launch_pdl(decode_join_kernel<typename Core::Elem, Core::D, Core::KEYS * kWarps>,
-                      dim3(static_cast<unsigned>(a.lanes - 1), static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)),
-                      dim3(kJoinRows * Core::D / 4), 0, stream, 1u, a);
+    return launch_pdl(decode_join_kernel<typename Core::Elem, Core::D>,
+                      dim3(static_cast<unsigned>(a.by_unit ? a.B * a.Hkv * a.groups : warps - a.team), static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)),
+                      dim3(kJoinRows * kJoinGroups * Core::D / 4), 0, stream, 1u, a);
 }
 
 template <int D>
@@ -692,13 +781,19 @@ DecodePlan make_decode_plan(int B, int Hq, int Hkv, int D, int block_size, int m
     // a unit's rows: one or two 16-row fragments (bf16); a power of two up to 8 (fp32)
     p.rows = bf16 ? (G <= 16 ? 16 : 32) : (G >= 5 ? 8 : G >= 3 ? 4 : G);
     p.groups = (G + p.rows - 1) / p.rows;
-    const int tile = (bf16 ? 16 : 8) * kWarps;
-    // two CTAs an SM, as many as the shared memory takes; never more than the table has tiles
-    const long long cap = (long long)B * Hkv * p.groups * (((long long)max_blocks * block_size + tile - 1) / tile);
-    long long lanes = 2LL * num_sms;
-    if (lanes > cap) lanes = cap;
+    const int tile = bf16 ? 16 : 8, units = Hkv * p.groups;
+    p.team = 1;
+    for (int t = 2; t <= kMaxTeam; ++t)
+        if (units % t == 0) p.team = t;
+    // eight warps an SM, as many as the shared memory takes; never more than the table's capacity
+    // gives kMinTiles each
+    const long long cap = (long long)B * (units / p.team) * (((long long)max_blocks * block_size + tile - 1) / tile);
+    long long lanes = 2LL * kWarps * num_sms / p.team;
+    if (lanes > cap / kMinTiles) lanes = cap / kMinTiles;
     p.lanes = lanes < 1 ? 1 : static_cast<int>(lanes);
-    p.ws_bytes = 2 * (size_t)p.lanes * ((size_t)p.rows * (D + 2) * sizeof(float) + sizeof(int));
+    const size_t warps = (size_t)p.lanes * p.team;
+    p.by_unit = (long long)B * units <= static_cast<long long>(warps);
+    p.ws_bytes = 2 * warps * ((size_t)p.rows * (D + 2) * sizeof(float) + sizeof(int)) + warps * sizeof(int4);
     return p;
 }
 

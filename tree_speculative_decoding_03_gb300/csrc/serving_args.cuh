@@ -56,7 +56,9 @@ cudaError_t launch_rope_append(const RopeArgs& a, bool bf16, int num_sms, cudaSt
 struct DecodePlan {
     int rows;     // query rows one unit covers (of one kv head)
     int groups;   // row groups per kv head
-    int lanes;    // CTAs the key tiles are divided between
+    int team;     // warps that go through the same keys, each with a unit of its own
+    int lanes;    // teams the key tiles are divided between
+    bool by_unit; // the join has a record per unit (they are fewer than the warps), else per warp
     size_t ws_bytes;
 };
 DecodePlan make_decode_plan(int B, int Hq, int Hkv, int D, int block_size, int max_blocks, bool bf16, int num_sms);
@@ -70,11 +72,13 @@ struct DecodeArgs {
     void* out;
     float* lse;  // [B, Hq] or nullptr
     int32_t* seq_err;
-    float* part_o;  // [2 * lanes][rows][D]
-    float* part_m;  // [2 * lanes][rows]
-    float* part_l;  // [2 * lanes][rows]
-    int* part_bad;  // [2 * lanes]
-    int B, Hq, Hkv, D, G, rows, groups, lanes;
+    // pieces of units, two slots a warp (warp = lane * team + member)
+    float* part_o;  // [2 * warps][rows][D]
+    float* part_m;  // [2 * warps][rows]
+    float* part_l;  // [2 * warps][rows]
+    int4* split;    // [warps]: sequence, unit, last lane (-1: in one piece) and first slot of a unit in pieces
+    int* part_bad;  // [2 * warps]
+    int B, Hq, Hkv, D, G, rows, groups, team, lanes, by_unit;
     int bs_log2, max_blocks, num_blocks;
     float scale_log2;  // scale * log2(e)
 };

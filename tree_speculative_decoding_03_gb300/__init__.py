@@ -43,8 +43,14 @@ def lib_path(variant=None) -> str:
 def build(verbose: bool = False, variant=None) -> str:
     """Builds the library: the product build, or a test build ("checked": device-side
     index checks; "hooks": short bounded waits and a stall switch)."""
-    from .builder import build_library
-    return build_library(verbose=verbose, variant=variant)
+    from concurrent.futures import ThreadPoolExecutor
+
+    from .builder import build_library, build_marshal
+    with ThreadPoolExecutor(max_workers=1) as ex:  # beside the library
+        marshal = ex.submit(build_marshal)
+        lib = build_library(verbose=verbose, variant=variant)
+        marshal.result()
+    return lib
 
 
 def use_variant(variant=None):
@@ -109,6 +115,9 @@ def load(variant=None):
     if hasattr(lib, "tsv_test_set_stall"):  # the "hooks" test build only
         lib.tsv_test_set_stall.restype = i32
         lib.tsv_test_set_stall.argtypes = [i32]
+    # entry points that the compiled marshalling calls
+    lib.addresses = {n: ctypes.cast(getattr(lib, n), P).value
+                     for n in ("tsv_kv_plan_slots", "tsv_rope_kv_append", "tsv_decode_attn")}
     _libs[v] = lib
     return lib
 
@@ -252,26 +261,34 @@ def kv_compact_accepted(k_cache, v_cache, block_table, seq_lens, accepted_nodes,
 
 # ----------------------------------------------------------------------------- around the step
 # The slot plan, the rotary K/V append and single-token attention (see include/tsv.h).
-# Shapes and types are checked here, since a wrong one would read or write out of range.
+# Types, shapes and devices are checked by the compiled marshalling (binding/marshal.cpp): a
+# wrong one would read or write out of range.
 
-def _need(t, name, dtype, shape):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
+_marshal_module = None
 
 
-def _current_stream(stream, *ts):
-    """The stream to launch on; every tensor (and the stream) on the current device."""
-    import torch
-    dev = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on one CUDA device")
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
+def _marshal():
+    global _marshal_module
+    if _marshal_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module resolves against its libraries)
+
+        from .builder import MARSHAL
+        if not os.path.exists(MARSHAL):
+            raise RuntimeError(f"_marshal.so not built at {MARSHAL}; run build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL)
+        _marshal_module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(_marshal_module)
+    return _marshal_module
+
+
+def _raw_stream(stream, t):
+    """The stream's handle (None: the current one), which must belong to the device of t."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    if stream.device.index != dev:
+        return None
+    if t.is_cuda and stream.device != t.device:
         raise ValueError("the stream must belong to the tensors' device")
     return stream.cuda_stream
 
@@ -285,49 +302,16 @@ def kv_plan_slots(seq_lens, new_lens, block_table, blocks_held, blocks_held_out,
     free_blocks [num_blocks], free_count, free_count_out [1], positions [max_tokens] int32;
     slot_map [max_tokens] int64; parent [B,N] int32 for draft trees.  blocks_held_out,
     free_count_out and total_lens may be blocks_held, free_count and seq_lens."""
-    import torch
-    i32 = torch.int32
-    B, max_blocks = block_table.shape
-    max_tokens = slot_map.numel()
-    one, per_seq, per_tok = (1,), (B,), (max_tokens,)
-    _need(block_table, "block_table", i32, (B, max_blocks))
-    _need(free_blocks, "free_blocks", i32, (free_blocks.numel(),))
-    _need(slot_map, "slot_map", torch.int64, per_tok)
-    _need(positions, "positions", i32, per_tok)
-    _need(token_offsets, "token_offsets", i32, (B + 1,))
-    _need(seq_lens, "seq_lens", i32, per_seq)
-    _need(new_lens, "new_lens", i32, per_seq)
-    _need(blocks_held, "blocks_held", i32, per_seq)
-    _need(blocks_held_out, "blocks_held_out", i32, per_seq)
-    _need(total_lens, "total_lens", i32, per_seq)
-    _need(seq_err, "seq_err", i32, per_seq)
-    _need(free_count, "free_count", i32, one)
-    _need(free_count_out, "free_count_out", i32, one)
-    N = 0
-    if parent is not None:
-        N = parent.shape[-1]
-        _need(parent, "parent", i32, (B, N))
-    s = _current_stream(stream, seq_lens, new_lens, parent, block_table, blocks_held, blocks_held_out, free_blocks,
-                        free_count, free_count_out, total_lens, token_offsets, slot_map, positions, seq_err)
-    _check(load().tsv_kv_plan_slots(
-        _ptr(seq_lens), _ptr(new_lens), _ptr(parent), _ptr(block_table), _ptr(blocks_held), _ptr(blocks_held_out),
-        _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out), _ptr(total_lens), _ptr(token_offsets),
-        _ptr(slot_map), _ptr(positions), B, N, block_size, max_blocks, free_blocks.numel(), max_tokens,
-        _ptr(seq_err), s))
+    _check(_marshal().kv_plan_slots(
+        load().addresses["tsv_kv_plan_slots"], seq_lens, new_lens, block_table, blocks_held, blocks_held_out, free_blocks,
+        free_count, free_count_out, total_lens, token_offsets, slot_map, positions, block_size, seq_err, parent,
+        _raw_stream(stream, seq_lens)))
 
 
 class RopeOptions(ctypes.Structure):
     """tsv_rope_options (include/tsv.h)."""
     _fields_ = [("rotary_dim", ctypes.c_int), ("neighbours", ctypes.c_int), ("axes", ctypes.c_int),
                 ("rounds", ctypes.c_int), ("sections", ctypes.c_int * 4)]
-
-
-def _token_rows(t, name, dtype, T, H, D):
-    """The token stride, in elements, of [T, H, D] rows whose heads are contiguous."""
-    st = t.stride()
-    if t.dtype is not dtype or t.shape != (T, H, D) or st[2] != 1 or (H > 1 and st[1] != D):
-        raise ValueError(f"{name} must be [{T}, {H}, {D}] {dtype} with contiguous heads")
-    return st[0] if T > 1 else H * D
 
 
 def rope_kv_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_map, tok_err, sections=None,
@@ -337,30 +321,11 @@ def rope_kv_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_m
     [axes,T] int32; inv_freq [rotary_dim/2] float32; tok_err [T] int32.  sections: rotary
     pairs of each axis, taken in "blocks" or in "rounds"; pairs: "halves" (i, i + rotary_dim/2)
     or "neighbours" (2i, 2i+1).  Tokens of q, k, v and q_out may be strided."""
-    import torch
-    T, Hq, D = q.shape
-    num_blocks, bs, Hkv, _ = k_cache.shape
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    half = inv_freq.numel()
-    sections = [half] if sections is None else list(sections)
-    if len(sections) != axes or axes > 4:
-        raise ValueError(f"{len(sections)} sections for {axes} position axes (at most 4)")
     if order not in ("blocks", "rounds") or pairs not in ("halves", "neighbours"):
         raise ValueError('order must be "blocks" or "rounds", pairs "halves" or "neighbours"')
-    qs, ks, vs = (_token_rows(t, n, q.dtype, T, h, D) for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)))
-    qos = _token_rows(q_out, "q_out", q.dtype, T, Hq, D)
-    _need(k_cache, "k_cache", q.dtype, (num_blocks, bs, Hkv, D))
-    _need(v_cache, "v_cache", q.dtype, (num_blocks, bs, Hkv, D))
-    _need(positions, "positions", torch.int32, (axes, T) if positions.dim() == 2 else (T,))
-    _need(inv_freq, "inv_freq", torch.float32, (half,))
-    _need(slot_map, "slot_map", torch.int64, (T,))
-    _need(tok_err, "tok_err", torch.int32, (T,))
-    opts = RopeOptions(2 * half, pairs == "neighbours", axes, order == "rounds", (ctypes.c_int * 4)(*sections))
-    s = _current_stream(stream, q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_map, tok_err)
-    _check(load().tsv_rope_kv_append(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-        _ptr(slot_map), T, Hq, Hkv, D, qs, ks, vs, qos, bs, num_blocks, _dtype_code(q), ctypes.byref(opts),
-        _ptr(tok_err), s))
+    _check(_marshal().rope_kv_append(
+        load().addresses["tsv_rope_kv_append"], q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_map, tok_err,
+        sections, order == "rounds", pairs == "neighbours", _raw_stream(stream, q)))
 
 
 def decode_attn_workspace_size(B, Hq, Hkv, D, block_size, max_blocks, dtype_code) -> int:
@@ -372,31 +337,9 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, out, scale: float, w
     """Attention of one new token per sequence over the paged cache (see include/tsv.h).
     q/out [B,Hq,D]; caches [num_blocks,bs,Hkv,D]; seq_lens [B]: keys, the new token's
     included; lse [B,Hq] float32, if given, takes the log-sum-exp of the scaled scores."""
-    import torch
-    B, Hq, D = q.shape
-    num_blocks, bs, Hkv, _ = k_cache.shape
-    max_blocks = block_table.shape[-1]
-    cache = (num_blocks, bs, Hkv, D)
-    _need(q, "q", q.dtype, (B, Hq, D))
-    _need(out, "out", q.dtype, (B, Hq, D))
-    _need(k_cache, "k_cache", q.dtype, cache)
-    _need(v_cache, "v_cache", q.dtype, cache)
-    _need(block_table, "block_table", torch.int32, (B, max_blocks))
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
-    if seq_err is None:
-        raise ValueError("seq_err [B] int32 is needed")
-    _need(seq_err, "seq_err", torch.int32, (B,))
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq))
-    ws_bytes = 0
-    if workspace is not None:
-        _contig(workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    s = _current_stream(stream, q, k_cache, v_cache, block_table, seq_lens, out, workspace, seq_err, lse)
-    _check(load().tsv_decode_attn(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse),
-        B, Hq, Hkv, D, bs, max_blocks, num_blocks, float(scale), _dtype_code(q), _ptr(workspace), ws_bytes,
-        _ptr(seq_err), s))
+    _check(_marshal().decode_attn(
+        load().addresses["tsv_decode_attn"], q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, seq_err, lse,
+        _raw_stream(stream, q)))
 
 
 # ----------------------------------------------------------------------------- tree construction

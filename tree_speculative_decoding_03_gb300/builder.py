@@ -3,12 +3,14 @@
 Each translation unit compiles in parallel into `_build/`, then the objects are
 linked into `_build/libtsv.so` (static CUDA runtime, so the library needs no
 runtime search path).  Rebuilds only when a source or header is newer than the
-library.
+library.  The serving operators' argument marshalling (`binding/marshal.cpp`, against torch's
+headers) is compiled beside it with the host compiler into `_build/_marshal.so`.
 """
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
 
@@ -16,6 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libtsv.so")
+MARSHAL_SRC = os.path.join(HERE, "binding", "marshal.cpp")
+MARSHAL = os.path.join(OUT_DIR, "_marshal.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -81,5 +85,28 @@ def build_library(verbose: bool = False, extra_flags=(), variant=None) -> str:
     return lib
 
 
+def build_marshal() -> str:
+    """Compiles the argument marshalling of the serving operators (host code)."""
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-isystem{d}" for d in inc),
+           MARSHAL_SRC, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {os.path.basename(MARSHAL_SRC)} failed:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_marshal())

@@ -51,6 +51,8 @@ def check(c, d):
     (1, 16, 0, 1, {}), (1, 8, 40, 3, {}), (2, 128, 300, 200, {}), (7, 16, 100, 1, dict(ended=0.3)),
     (64, 16, 2000, 0, dict(tree=64)), (33, 32, 500, 0, dict(tree=128)), (5, 8, 50, 0, dict(tree=1)),
     (257, 16, 700, 60, dict(ended=0.2, pad=37)), (1025, 64, 900, 20, dict(ended=0.1)), (8192, 8, 60, 9, dict(ended=0.1, pad=5)),
+    (2330, 16, 300, 40, dict(ended=0.1, tree=7)), (64, 16, 200, 7, dict(pad=60)), (65, 16, 200, 3, {}), (300, 16, 100, 0, dict(tree=64)),
+    (3000, 16, 90, 0, dict(tree=6, pad=900)), (700, 32, 300, 60, dict(pool="short", ended=0.1)),
     (3, 16, 20, 9000, {}), (40, 16, 300, 40, dict(pool="exact")), (40, 16, 300, 40, dict(pool="exact", ended=0.4)),
     (60, 16, 300, 80, dict(pool="short")), (60, 16, 300, 0, dict(pool="short", tree=33)), (12, 16, 90, 0, dict(spare=1.0))])
 def test_plan(B, bs, max_len, max_new, kw):
@@ -124,6 +126,32 @@ def test_bad_data_is_reported_and_the_others_served(what):
     want = check_saturated(c, d) if what == "huge" else check(c, d)
     # (with "pool_ids" the returned blocks, which are popped first, are enough)
     assert want["err"].any() == (what != "pool_ids")
+
+
+@pytest.mark.parametrize("what", ["length", "capacity", "tokens", "ids", "pool_ids", "pool_ids_taken", "trees"])
+def test_bad_data_in_a_large_batch(what):
+    # the slot map is filled by a second kernel
+    r = np.random.default_rng(12)
+    c = U.plan_case(r, 900, 16, 300, 40, ended=0.0 if what == "pool_ids_taken" else 0.1, tree=33 if what == "trees" else None,
+                    spare=0.1, pad=50)
+    some = r.permutation(900)[:40]
+    if what == "length":
+        c["seq_lens"][some] = -3
+    elif what == "capacity":
+        c["held"][some] = c["table"].shape[1] + 7
+    elif what == "tokens":
+        c["max_tokens"] = c["max_tokens"] * 2 // 3
+    elif what == "ids":
+        c["table"][some, np.maximum(c["held"][some] - 1, 0)] = -1
+    elif what.startswith("pool_ids"):
+        c["free_blocks"][r.integers(0, c["free_count"], 40)] = 2 ** 30
+    else:
+        c["parent"][some, r.integers(1, 33, 40)] = 99
+        c["new_lens"][some[:5]] = 40
+    d = device_plan(c)
+    call(d)
+    # (with "pool_ids" the returned blocks, which are popped first, are enough)
+    assert check(c, d)["err"].any() == (what != "pool_ids")
 
 
 def check_saturated(c, d):

@@ -8,11 +8,13 @@
 // block, and the k-th fresh block is at place top - 1 - k with top = count + sum(back).  So
 // no thread waits for another's push or pop, and the result does not depend on timing.
 //
-// One cluster: every CTA loads all lengths and scans them (they are a few KB, and reading
-// them is cheaper than passing the scans on); after a cluster barrier, from which on outputs
-// that share memory with inputs may be written, the tokens, the fresh table entries and the
-// returned blocks are divided between all threads, each finding its sequence by bisection of
-// the scans in shared memory.
+// One cluster (one CTA for small batches): every CTA loads all lengths and scans them -- they are
+// a few KB, and reading them is cheaper than passing the scans on.  After a cluster barrier, from
+// which on outputs that share memory with inputs may be written, the tokens, the fresh table
+// entries and the returned blocks are one list of items, divided between all threads; each
+// item finds its sequence by bisection of the scans in shared memory.  The work is a chain of
+// latencies (launch, lengths, scan, ids, stores), not bytes.  Large slot maps are filled by a
+// second kernel over all SMs instead, from the outputs of the first.
 #include <climits>
 #include <cooperative_groups.h>
 
@@ -23,8 +25,10 @@ namespace tsv {
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;
+constexpr int kPlanSmallSeqs = 64, kPlanSmallTokens = 512;  // one CTA up to here
+constexpr int kPlanClusterTokens = 32768;                  // tokens by the cluster up to here
+constexpr int kFillThreads = 256, kFillTokens = 4;  // the second kernel: threads, tokens of a thread
 
 // First i in [0, n) with end[i] > x (n when there is none): the sequence item x falls in.
 __device__ __forceinline__ int first_above(const int* end, int n, int x) {
@@ -39,59 +43,66 @@ __device__ __forceinline__ int first_above(const int* end, int n, int x) {
     return lo;
 }
 
-__device__ __forceinline__ int sat_int(long long x) { return x > INT_MAX ? INT_MAX : static_cast<int>(x); }
+// Sums of counts stay at INT_MAX once they reach it (associative, so a scan may use it).
+__device__ __forceinline__ int sat_add(int a, int b) {
+    const unsigned s = static_cast<unsigned>(a) + static_cast<unsigned>(b);
+    return s > static_cast<unsigned>(INT_MAX) ? INT_MAX : static_cast<int>(s);
+}
 
-// Inclusive block-wide scan of three sums at once; *carry holds the totals of the passes before.
+// Three running sums: tokens, fresh blocks, returned blocks.
 struct Three {
-    long long a, b, c;
+    int a, b, c;
+    __device__ __forceinline__ void add(const Three& o) {
+        a = sat_add(a, o.a);
+        b = sat_add(b, o.b);
+        c = sat_add(c, o.c);
+    }
 };
-__device__ __forceinline__ Three block_scan(Three v, Three* s_warp, Three* carry) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ Three warp_scan(Three v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o),
-                        c = __shfl_up_sync(0xffffffffu, v.c, o);
-        if (lane >= o) {
-            v.a += a;
-            v.b += b;
-            v.c += c;
-        }
+        const Three y{__shfl_up_sync(0xffffffffu, v.a, o), __shfl_up_sync(0xffffffffu, v.b, o), __shfl_up_sync(0xffffffffu, v.c, o)};
+        if (lane >= o) v.add(y);
     }
+    return v;
+}
+// Inclusive scan over the block; `carry` (the same in every thread) holds the sums of the passes
+// before.
+template <int THREADS>
+__device__ __forceinline__ Three block_scan(Three v, Three* s_warp, Three* carry) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v);
     if (lane == 31) s_warp[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        Three w = lane < kPlanThreads / 32 ? s_warp[lane] : Three{0, 0, 0};
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long a = __shfl_up_sync(0xffffffffu, w.a, o), b = __shfl_up_sync(0xffffffffu, w.b, o),
-                            c = __shfl_up_sync(0xffffffffu, w.c, o);
-            if (lane >= o) {
-                w.a += a;
-                w.b += b;
-                w.c += c;
-            }
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    if (warp > 0) {
-        v.a += s_warp[warp - 1].a;
-        v.b += s_warp[warp - 1].b;
-        v.c += s_warp[warp - 1].c;
-    }
-    v.a += carry->a;
-    v.b += carry->b;
-    v.c += carry->c;
-    carry->a += s_warp[31].a;
-    carry->b += s_warp[31].b;
-    carry->c += s_warp[31].c;
+    // every warp scans the warps' sums for itself
+    const Three w = warp_scan(lane < THREADS / 32 ? s_warp[lane] : Three{0, 0, 0});
+    const int from = warp > 0 ? warp - 1 : 0;
+    Three before{__shfl_sync(0xffffffffu, w.a, from), __shfl_sync(0xffffffffu, w.b, from), __shfl_sync(0xffffffffu, w.c, from)};
+    if (warp > 0) v.add(before);
+    v.add(*carry);
+    carry->add(Three{__shfl_sync(0xffffffffu, w.a, 31), __shfl_sync(0xffffffffu, w.b, 31), __shfl_sync(0xffffffffu, w.c, 31)});
     __syncthreads();
     return v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs a) {
+// Distance of node j from the root, or -1 where the path leaves the rules of a tree.  Every node
+// is checked by its own first step.
+__device__ __forceinline__ int depth_of(const int32_t* par, int j) {
+    int depth = 0, x = j;
+    while (x > 0) {
+        const int p = __ldg(par + x);
+        if (p < 0 || p >= x) return -1;
+        x = p;
+        ++depth;
+    }
+    return __ldg(par) == -1 ? depth : -1;
+}
+
+template <int THREADS, int CLUSTER, bool TOKENS>
+__global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int s_dyn[];
-    int* s_len = s_dyn;              // cached length (0 for a sequence whose lengths are bad)
+    int* s_len = s_dyn;              // cached length (0 for a negative one)
     int* s_held = s_len + a.B;       // blocks held
     int* s_tok = s_held + a.B;       // end of the sequence's tokens
     int* s_grow = s_tok + a.B;       // end of its fresh blocks
@@ -99,8 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
     uint8_t* s_err = reinterpret_cast<uint8_t*>(s_back + a.B);
     __shared__ Three s_warp[32];
     __shared__ int s_top, s_grown;
-    cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, bs = 1 << a.bs_log2;
+    const int rank = CLUSTER > 1 ? static_cast<int>(blockIdx.x) : 0;  // the grid is one cluster
     const long long cap = (long long)a.max_blocks << a.bs_log2;
     pdl_wait();
     pdl_launch_dependents();
@@ -110,176 +121,245 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const PlanArgs
     }
     const int count = *a.free_count;
     const bool pool_ok = count >= 0 && count <= a.num_blocks;
-    Three carry{0, 0, 0};
-    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int L = 0, n = 0, held = 0, err = 0;
-        long long want = 0, grow = 0, back = 0;
-        if (b < a.B) {
-            L = a.seq_lens[b];
-            n = a.new_lens[b];
-            held = a.held[b];
-            if (L < 0 || n < 0 || (long long)L + n > cap || held < 0 || held > a.max_blocks) err |= TSV_DERR_CAPACITY;
-            if (a.parent != nullptr && n > a.N) err |= TSV_DERR_PARENT;
-            if (!pool_ok) err |= TSV_DERR_POOL;
-            if (n < 0) n = 0;
-            if (L < 0) L = 0;
-            if (err == 0) {
-                want = ((long long)L + n + bs - 1) >> a.bs_log2;
-                grow = want > held ? want - held : 0;
-                back = held > want ? held - want : 0;
+    // The running sums of all three counts.  A sequence whose tokens pass the map's end takes and
+    // returns nothing, which the token sums decide: where that happens the scan is repeated
+    // without those sequences' blocks.
+    int total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        Three carry{0, 0, 0};
+        bool past = false;
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            const int b = b0 + tid;
+            int L = 0, n = 0, held = 0, err = 0, grow = 0, back = 0;
+            if (b < a.B) {
+                L = a.seq_lens[b];
+                n = a.new_lens[b];
+                held = a.held[b];
+                if (L < 0 || n < 0 || (long long)L + n > cap || held < 0 || held > a.max_blocks) err |= TSV_DERR_CAPACITY;
+                if (a.parent != nullptr && n > a.N) err |= TSV_DERR_PARENT;
+                if (!pool_ok) err |= TSV_DERR_POOL;
+                n = max(n, 0);
+                L = max(L, 0);
+                if (pass == 1 && n > 0 && s_tok[b] > a.max_tokens) err |= TSV_DERR_CAPACITY;
+                if (err == 0) {
+                    const int want = static_cast<int>(((long long)L + n + bs - 1) >> a.bs_log2);
+                    grow = max(want - held, 0);
+                    back = max(held - want, 0);
+                }
+            }
+            const Three e = block_scan<THREADS>(Three{n, grow, back}, s_warp, &carry);
+            if (b < a.B) {
+                past |= n > 0 && e.a > a.max_tokens;
+                // more blocks come back than the pool has places for: the caller's counts are wrong
+                if (back > 0 && (long long)count + e.c > a.num_blocks) err |= TSV_DERR_POOL;
+                s_len[b] = L;
+                s_held[b] = held;
+                s_tok[b] = e.a;
+                s_grow[b] = e.b;
+                s_back[b] = e.c;
+                s_err[b] = static_cast<uint8_t>(err);
+                // the last sequence that gives back decides the stack's height
+                if (back > 0 && err == 0) atomicMax(&s_top, e.c);
             }
         }
-        // tokens first: a sequence whose tokens do not all fit the map takes and returns nothing
-        Three v{n, grow, back};
-        Three e = block_scan(v, s_warp, &carry);
-        if (b < a.B) {
-            if (e.a > a.max_tokens && n > 0) err |= TSV_DERR_CAPACITY;
-            s_len[b] = L;
-            s_held[b] = held;
-            s_tok[b] = sat_int(e.a);
-            s_grow[b] = static_cast<int>(grow);
-            s_back[b] = static_cast<int>(back);
-            s_err[b] = static_cast<uint8_t>(err);
-        }
+        total = carry.a;
+        if (!__syncthreads_or(past) || pass == 1) break;
+        if (tid == 0) s_top = 0;
+        __syncthreads();
     }
-    __syncthreads();
-    const long long total = carry.a;
-    carry = Three{0, 0, 0};
-    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        const bool live = b < a.B && s_err[b] == 0;
-        const long long grow = live ? s_grow[b] : 0, back = live ? s_back[b] : 0;
-        const Three e = block_scan(Three{0, grow, back}, s_warp, &carry);
-        if (b < a.B) {
-            int err = s_err[b];
-            // more blocks come back than the pool has places for: the caller's counts are wrong
-            if (back > 0 && count + e.c > a.num_blocks) err |= TSV_DERR_POOL;
-            if (back > 0 && err == 0) atomicMax(&s_top, static_cast<int>(e.c));
-            s_err[b] = static_cast<uint8_t>(err);
-            s_grow[b] = sat_int(e.b);
-            s_back[b] = sat_int(e.c);
-        }
-    }
-    __syncthreads();
     const int top = (pool_ok ? count : 0) + s_top;
-    for (int b = tid; b < a.B; b += kPlanThreads) {
+    for (int b = tid; b < a.B; b += THREADS) {
         const int before = b > 0 ? s_grow[b - 1] : 0;
-        if (s_grow[b] > before) {
+        int err = s_err[b];
+        if (s_grow[b] > before && err == 0) {
             if (s_grow[b] > top)
-                s_err[b] |= static_cast<uint8_t>(TSV_DERR_POOL);
+                err |= TSV_DERR_POOL;
             else
                 atomicMax(&s_grown, s_grow[b]);
+            s_err[b] = static_cast<uint8_t>(err);
         }
+        if (b % CLUSTER == rank) a.seq_err[b] = err;
     }
-    // every CTA of the cluster has read the inputs: from here on outputs may be written
-    cluster.sync();
-    const int grown = s_grown;
-    const int left = top - grown;
-    const int t0 = static_cast<int>(cluster.block_rank()) * kPlanThreads + tid;
-    const int nthreads = kPlanCluster * kPlanThreads;
+    // every CTA of the cluster has read the inputs: from here on their memory may be written.  The
+    // error words are in place too; bits are added to them below.
+    if (CLUSTER > 1)
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
+    const int grown = s_grown, left = top - grown;
 
+    auto begin = [&](const int* end, int b) { return b > 0 ? end[b - 1] : 0; };
     auto want_of = [&](int b) {
-        const int n = s_tok[b] - (b > 0 ? s_tok[b - 1] : 0);
-        return static_cast<int>(((long long)s_len[b] + n + bs - 1) >> a.bs_log2);
+        return static_cast<int>(((long long)s_len[b] + s_tok[b] - begin(s_tok, b) + bs - 1) >> a.bs_log2);
     };
     // block id at place p of the stack
     auto stack_at = [&](int p) {
         if (p < count) return a.free_blocks[p];
-        const int i = p - count;
-        const int b = first_above(s_back, a.B, i);
+        const int i = p - count, b = first_above(s_back, a.B, i);
         if (b >= a.B) return -1;
-        return a.block_table[(long long)b * a.max_blocks + want_of(b) + (i - (b > 0 ? s_back[b - 1] : 0))];
+        return a.block_table[(long long)b * a.max_blocks + want_of(b) + (i - begin(s_back, b))];
     };
 
-    for (int b = t0; b < a.B; b += nthreads) {
-        const int err = s_err[b];
-        const int n = s_tok[b] - (b > 0 ? s_tok[b - 1] : 0);
-        a.seq_err[b] = err;
-        a.token_offsets[b + 1] = s_tok[b];
-        if (err == 0) {
-            a.held_out[b] = want_of(b);
-            a.total_lens[b] = s_len[b] + n;
-        } else {
-            a.held_out[b] = s_held[b];
-            a.total_lens[b] = s_len[b];
-        }
-    }
-    if (t0 == 0) {
-        a.token_offsets[0] = 0;
-        *a.free_count_out = pool_ok ? left : count;
-    }
-    // errors found below are added to words that another CTA may be writing above
-    cluster.sync();
-
-    for (int t = t0; t < a.max_tokens; t += nthreads) {
-        long long slot = -1;
-        int pos = -1;
-        if (t < total) {
-            const int b = first_above(s_tok, a.B, t);
-            if (s_err[b] == 0) {
-                const int j = t - (b > 0 ? s_tok[b - 1] : 0);
-                const int at = s_len[b] + j, blk = at >> a.bs_log2, held = s_held[b];
+    const int t0 = rank * THREADS + tid;
+    constexpr int kAll = CLUSTER * THREADS;
+    const int tokens = TOKENS ? a.max_tokens : 0, pushed = pool_ok ? max(left - count, 0) : 0;
+    const long long items = (long long)tokens + a.B + grown + pushed;
+    for (long long item = t0; item < items; item += kAll) {
+        if (item < tokens) {
+            const int t = static_cast<int>(item);
+            long long slot = -1;
+            int pos = -1;
+            const int b = t < total ? first_above(s_tok, a.B, t) : a.B;
+            if (b < a.B && s_err[b] == 0) {
+                const int j = t - begin(s_tok, b), at = s_len[b] + j, blk = at >> a.bs_log2, held = s_held[b];
                 const int id = blk < held ? a.block_table[(long long)b * a.max_blocks + blk]
-                                          : stack_at(top - 1 - ((b > 0 ? s_grow[b - 1] : 0) + blk - held));
-                if (id >= 0 && id < a.num_blocks)
+                                          : stack_at(top - 1 - (begin(s_grow, b) + blk - held));
+                const int depth = a.parent != nullptr ? depth_of(a.parent + (long long)b * a.N, j) : j;
+                int err = 0;
+                if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
                     slot = ((long long)id << a.bs_log2) + (at & (bs - 1));
                 else
-                    atomicOr(&a.seq_err[b], TSV_DERR_BLOCK);
-                int depth = j;
-                if (a.parent != nullptr) {
-                    // distance to the root; every node is checked by its own first step
-                    const int32_t* par = a.parent + (long long)b * a.N;
-                    depth = 0;
-                    int x = j;
-                    while (x > 0) {
-                        const int p = __ldg(par + x);
-                        if (p < 0 || p >= x) break;
-                        x = p;
-                        ++depth;
-                    }
-                    if (x != 0 || __ldg(par) != -1) {
-                        depth = -1 - s_len[b];  // position -1
-                        atomicOr(&a.seq_err[b], TSV_DERR_PARENT);
-                    }
-                }
-                pos = s_len[b] + depth;
+                    err |= TSV_DERR_BLOCK;
+                if (depth >= 0)
+                    pos = s_len[b] + depth;
+                else
+                    err |= TSV_DERR_PARENT;
+                if (err) atomicOr(&a.seq_err[b], err);
             }
+            a.slot_map[t] = slot;
+            a.positions[t] = pos;
+            continue;
         }
-        a.slot_map[t] = slot;
-        a.positions[t] = pos;
-    }
-    for (int k = t0; k < grown; k += nthreads) {
-        const int b = first_above(s_grow, a.B, k);
-        const int j = s_held[b] + (k - (b > 0 ? s_grow[b - 1] : 0));
-        a.block_table[(long long)b * a.max_blocks + j] = stack_at(top - 1 - k);
-    }
-    for (int p = (pool_ok ? count : left) + t0; p < left; p += nthreads) {
-        const int id = stack_at(p);
-        a.free_blocks[p] = id;
-        if (id < 0 || id >= a.num_blocks) {
-            const int b = first_above(s_back, a.B, p - count);
+        int k = static_cast<int>(item - tokens);
+        if (k < a.B) {
+            const bool ok = s_err[k] == 0;
+            const int end = s_tok[k];
+            a.token_offsets[k + 1] = end;
+            if (k == 0) {
+                a.token_offsets[0] = 0;
+                *a.free_count_out = pool_ok ? left : count;
+            }
+            a.held_out[k] = ok ? want_of(k) : s_held[k];
+            a.total_lens[k] = s_len[k] + (ok ? end - begin(s_tok, k) : 0);
+            continue;
+        }
+        k -= a.B;
+        if (k < grown) {
+            const int b = first_above(s_grow, a.B, k);
+            a.block_table[(long long)b * a.max_blocks + s_held[b] + (k - begin(s_grow, b))] = stack_at(top - 1 - k);
+            continue;
+        }
+        k -= grown;  // a returned block that stays on the stack
+        const int id = stack_at(count + k);
+        a.free_blocks[count + k] = id;
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
+            const int b = first_above(s_back, a.B, k);
             if (b < a.B) atomicOr(&a.seq_err[b], TSV_DERR_BLOCK);
         }
     }
 }
 
+// The slots and positions of a large map, from the first kernel's outputs: a CTA's tokens lie in
+// the sequences between two places of token_offsets, which it copies to shared memory.
+__global__ void __launch_bounds__(kFillThreads) kv_plan_fill_kernel(const __grid_constant__ PlanArgs a) {
+    constexpr int kTok = kFillThreads * kFillTokens;
+    __shared__ int s_end[kTok + 1];
+    __shared__ int s_b[2];
+    const int tid = threadIdx.x, bs = 1 << a.bs_log2;
+    const int t0 = blockIdx.x * kTok, t1 = min(t0 + kTok, a.max_tokens);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int* end = a.token_offsets + 1;
+    const int total = min(end[a.B - 1], a.max_tokens);
+    if (tid < 64) {
+        // warp 0: the sequence of the CTA's first token, warp 1: of its last; 32 probes a step
+        const int lane = tid & 31, x = tid < 32 ? t0 : min(t1, total) - 1;
+        int lo = 0, n = a.B;  // the first i with end[i] > x lies in [lo, lo + n)
+        while (n > 0) {
+            const int step = (n + 31) >> 5, i = lo + min(lane * step + step, n) - 1;
+            const unsigned above = __ballot_sync(0xffffffffu, end[i] > x);
+            if (above == 0) {
+                lo += n;
+                break;
+            }
+            const int f = __ffs(above) - 1;
+            const int next = lo + f * step;
+            n = min(step, n - f * step) - 1;  // the probe itself is above: what is left lies before it
+            lo = next;
+        }
+        if (lane == 0) s_b[tid >> 5] = lo;
+    }
+    __syncthreads();
+    const int b0 = s_b[0], nb = t0 < total ? s_b[1] - b0 + 1 : 0;
+    // a sequence without tokens holds no token, so at most kTok of them do; the others in between
+    // would not fit: those CTAs bisect in global memory
+    const bool local = nb <= kTok;
+    if (local)
+        for (int i = tid; i < nb; i += kFillThreads) s_end[i] = end[b0 + i];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kFillTokens; ++u) {
+        const int t = t0 + u * kFillThreads + tid;
+        if (t >= a.max_tokens) break;
+        long long slot = -1;
+        int pos = -1;
+        if (t < total) {
+            const int b = b0 + (local ? first_above(s_end, nb, t) : first_above(end + b0, nb, t));
+            const int first = a.token_offsets[b], j = t - first, n = end[b] - first;
+            const int tot = a.total_lens[b], e = a.seq_err[b];
+            // a sequence that was not served keeps its length, so these hold its tokens back
+            const bool held_back = (e & (TSV_DERR_CAPACITY | TSV_DERR_POOL)) != 0 || (a.parent != nullptr && n > a.N);
+            if (!held_back) {
+                const int at = tot - n + j;
+                const int id = a.block_table[(long long)b * a.max_blocks + (at >> a.bs_log2)];
+                const int depth = a.parent != nullptr ? depth_of(a.parent + (long long)b * a.N, j) : j;
+                int err = 0;
+                if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+                    slot = ((long long)id << a.bs_log2) + (at & (bs - 1));
+                else
+                    err |= TSV_DERR_BLOCK;
+                if (depth >= 0)
+                    pos = tot - n + depth;
+                else
+                    err |= TSV_DERR_PARENT;
+                if (err) atomicOr(&a.seq_err[b], err);
+            }
+        }
+        a.slot_map[t] = slot;
+        a.positions[t] = pos;
+    }
+}
+
+template <int THREADS, int CLUSTER, bool TOKENS>
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
+    const size_t smem = (size_t)a.B * (5 * sizeof(int) + 1) + 16;
+    if (smem > 40 * 1024) {  // with the static part, past what a launch gets unasked
+        thread_local int smem_dev = -1;
+        thread_local size_t smem_set = 0;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev != smem_dev || smem > smem_set) {
+            e = cudaFuncSetAttribute(kv_plan_kernel<THREADS, CLUSTER, TOKENS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+            smem_dev = dev;
+            smem_set = smem;
+        }
+    }
+    return launch_pdl(kv_plan_kernel<THREADS, CLUSTER, TOKENS>, dim3(CLUSTER), dim3(THREADS), smem, stream, CLUSTER, a);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
-    const size_t smem = (size_t)a.B * (5 * sizeof(int) + 1) + 16;
-    thread_local int smem_dev = -1;
-    thread_local size_t smem_set = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    if (a.B <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens) return launch_plan<512, 1, true>(a, stream);
+    if (a.max_tokens <= kPlanClusterTokens) return launch_plan<1024, kPlanCluster, true>(a, stream);
+    const cudaError_t e = launch_plan<1024, kPlanCluster, false>(a, stream);
     if (e != cudaSuccess) return e;
-    if (dev != smem_dev || smem > smem_set) {
-        e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        smem_dev = dev;
-        smem_set = smem;
-    }
-    return launch_pdl(kv_plan_kernel, dim3(kPlanCluster), dim3(kPlanThreads), smem, stream, kPlanCluster, a);
+    constexpr int kTok = kFillThreads * kFillTokens;
+    return launch_pdl(kv_plan_fill_kernel, dim3(static_cast<unsigned>((a.max_tokens + kTok - 1) / kTok)), dim3(kFillThreads), 0,
+                      stream, 1u, a);
 }
 
 }  // namespace tsv

@@ -30,12 +30,11 @@ __device__ __forceinline__ float2 turn_of(int pos, float f) {
     constexpr float kInvTwoPiLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(0.15915494f));
     const float fh = f * kInvTwoPiHi;
     const float fl = fmaf(f, kInvTwoPiHi, -fh) + f * kInvTwoPiLo;
-    const float ph = static_cast<float>(pos);  // pos = ph + pl exactly
-    const float pl = static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph));
+    const float ph = static_cast<float>(pos);  // exact up to 2^24; past that the rest is added below
     const float hi = ph * fh;
-    float lo = fmaf(ph, fh, -hi);
-    lo = fmaf(ph, fl, lo);
-    lo = fmaf(pl, fh, lo);
+    float lo = fmaf(ph, fl, fmaf(ph, fh, -hi));
+    if (pos > (1 << 24) || pos < -(1 << 24))
+        lo = fmaf(static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph)), fh, lo);
     const float r = (hi - rintf(hi)) + lo;
     float s, c;
     sincospif(2.0f * r, &s, &c);
@@ -80,95 +79,119 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
-// Block: `tok` tokens x `hl` head lanes x D / (2 * vector) items of a head; blockIdx.y takes
-// every gridDim.y-th run of head lanes.
+// Block: `tok` tokens x head lanes x D / (2 * vector) items of a head.  A thread's first vectors
+// are on their way while the block forms the angles, and the next head's while it turns one.
 template <typename T, int D, bool NEIGH>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a, int tok) {
     constexpr int VN = Vec<T>::N, ITEMS = D / (2 * VN), LANES = kRopeThreads / ITEMS;
-    extern __shared__ float s_turn[];  // cos [tok][R / 2], then sin [tok][R / 2]
+    extern __shared__ __align__(16) float s_turn[];  // cos [tok][R / 2], then sin [tok][R / 2]
     const int tid = threadIdx.x, half = a.R >> 1;
     const int t0 = blockIdx.x * tok;
-    float* s_cos = s_turn;
-    float* s_sin = s_turn + tok * half;
-    pdl_wait();
-    pdl_launch_dependents();
-    for (int i = tid; i < tok * half; i += kRopeThreads) {
-        const int t = t0 + i / half, p = i % half;
-        float2 cs = make_float2(1.0f, 0.0f);
-        if (t < a.T) cs = turn_of(__ldg(a.positions + (long long)a.axis[p] * a.T + t), __ldg(a.inv_freq + p));
-        s_cos[i] = cs.x;
-        s_sin[i] = cs.y;
-    }
-    __syncthreads();
     const int item = tid % ITEMS, lane = tid / ITEMS;
     const int hl = LANES / tok;  // head lanes of a token
     const int ti = lane / hl, h0 = lane % hl;
     const int t = t0 + ti;
-    if (t >= a.T) return;
-    const long long slot = __ldg(a.slot_map + t);
-    const bool bad = slot >= a.slots, pad = slot < 0;
-    if (item == 0 && h0 == 0 && blockIdx.y == 0) a.tok_err[t] = bad ? TSV_DERR_BLOCK : 0;
     // this thread's two vectors of a head, and whether they turn
     const int turning = half / VN;  // items that turn
     const bool turns = item < turning;
     const int rest = a.R + (item - turning) * 2 * VN;
     const int e0 = turns ? (NEIGH ? 2 * item * VN : item * VN) : rest;
     const int e1 = turns ? (NEIGH ? e0 + VN : e0 + half) : rest + VN;
+    const int heads = a.Hq + 2 * a.Hkv;
+    const bool live = t < a.T && h0 < heads;
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride - (long long)a.Hq * D;
+    const T* v = static_cast<const T*>(a.v) + t * a.v_stride - (long long)(a.Hq + a.Hkv) * D;
+    auto source = [&](int h) { return (h < a.Hq ? q : h < a.Hq + a.Hkv ? k : v) + (long long)h * D; };
+    pdl_wait();
+    pdl_launch_dependents();
+    long long slot = -1;
+    uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
+    if (live) {
+        slot = __ldg(a.slot_map + t);
+        u0 = *reinterpret_cast<const uint4*>(source(h0) + e0);
+        u1 = *reinterpret_cast<const uint4*>(source(h0) + e1);
+    }
+    float* s_cos = s_turn;
+    float* s_sin = s_turn + tok * half;
+    for (int i = tid, ts = t0 + tid / half, p = tid % half; i < tok * half; i += kRopeThreads) {
+        float2 cs = make_float2(1.0f, 0.0f);
+        if (ts < a.T) cs = turn_of(__ldg(a.positions + (long long)a.axis[p] * a.T + ts), __ldg(a.inv_freq + p));
+        s_cos[i] = cs.x;
+        s_sin[i] = cs.y;
+        ts += kRopeThreads / half;
+        p += kRopeThreads % half;
+        if (p >= half) {
+            p -= half;
+            ++ts;
+        }
+    }
+    __syncthreads();
+    if (!live) return;
+    T* qo = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+    const bool bad = slot >= a.slots;
+    if (item == 0 && h0 == 0) a.tok_err[t] = bad ? TSV_DERR_BLOCK : 0;
+    if (slot < 0 || bad) {  // a padding row is zero, a row with a bad slot NaN
+        float x[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) x[i] = bad ? __int_as_float(0x7fc00000) : 0.0f;
+        const uint4 u = Vec<T>::pack(x);
+        for (int h = h0; h < a.Hq; h += hl) {
+            *reinterpret_cast<uint4*>(qo + (long long)h * D + e0) = u;
+            *reinterpret_cast<uint4*>(qo + (long long)h * D + e1) = u;
+        }
+        return;
+    }
     float cs[VN], sn[VN];
 #pragma unroll
-    for (int i = 0; i < VN; ++i) {
-        cs[i] = turns ? s_cos[ti * half + item * VN + i] : 1.0f;
-        sn[i] = turns ? s_sin[ti * half + item * VN + i] : 0.0f;
+    for (int i = 0; i < VN; i += 4) {
+        const float4 c4 = turns ? *reinterpret_cast<const float4*>(s_cos + ti * half + item * VN + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+        const float4 s4 = turns ? *reinterpret_cast<const float4*>(s_sin + ti * half + item * VN + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        cs[i] = c4.x, cs[i + 1] = c4.y, cs[i + 2] = c4.z, cs[i + 3] = c4.w;
+        sn[i] = s4.x, sn[i + 1] = s4.y, sn[i + 2] = s4.z, sn[i + 3] = s4.w;
     }
-    const int heads = a.Hq + 2 * a.Hkv;
-    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
-    const T* k = static_cast<const T*>(a.k) + t * a.k_stride;
-    const T* v = static_cast<const T*>(a.v) + t * a.v_stride;
-    T* qo = static_cast<T*>(a.q_out) + t * a.q_out_stride;
-    T* kc = static_cast<T*>(a.k_cache) + slot * a.Hkv * D;
-    T* vc = static_cast<T*>(a.v_cache) + slot * a.Hkv * D;
-    for (int h = blockIdx.y * hl + h0; h < heads; h += gridDim.y * hl) {
-        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-        if (!is_q && (pad || bad)) continue;
-        const T* src = is_q ? q + (long long)h * D : is_v ? v + (long long)(h - a.Hq - a.Hkv) * D : k + (long long)(h - a.Hq) * D;
-        T* dst = is_q ? qo + (long long)h * D : is_v ? vc + (long long)(h - a.Hq - a.Hkv) * D : kc + (long long)(h - a.Hq) * D;
-        uint4 u0, u1;
-        if (is_q && (pad || bad)) {  // a padding row is zero, a row with a bad slot NaN
-            float x[VN];
-#pragma unroll
-            for (int i = 0; i < VN; ++i) x[i] = bad ? __int_as_float(0x7fc00000) : 0.0f;
-            u0 = u1 = Vec<T>::pack(x);
-        } else {
-            u0 = *reinterpret_cast<const uint4*>(src + e0);
-            u1 = *reinterpret_cast<const uint4*>(src + e1);
-            if (turns && !is_v) {
-                float x[2 * VN];
-                Vec<T>::unpack(u0, x);
-                Vec<T>::unpack(u1, x + VN);
-#pragma unroll
-                for (int i = 0; i < VN; ++i) {
-                    float& p = x[NEIGH ? 2 * i : i];
-                    float& r = x[NEIGH ? 2 * i + 1 : i + VN];
-                    const float y = p * cs[i] - r * sn[i];
-                    r = r * cs[i] + p * sn[i];
-                    p = y;
-                }
-                u0 = Vec<T>::pack(x);
-                u1 = Vec<T>::pack(x + VN);
-            }
+    T* kc = static_cast<T*>(a.k_cache) + (slot * a.Hkv - a.Hq) * D;
+    T* vc = static_cast<T*>(a.v_cache) + (slot * a.Hkv - a.Hq - a.Hkv) * D;
+    for (int h = h0; h < heads; h += hl) {
+        uint4 n0 = u0, n1 = u1;
+        if (h + hl < heads) {
+            n0 = *reinterpret_cast<const uint4*>(source(h + hl) + e0);
+            n1 = *reinterpret_cast<const uint4*>(source(h + hl) + e1);
         }
+        if (turns && h < a.Hq + a.Hkv) {
+            float x[2 * VN];
+            Vec<T>::unpack(u0, x);
+            Vec<T>::unpack(u1, x + VN);
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                float& p = x[NEIGH ? 2 * i : i];
+                float& r = x[NEIGH ? 2 * i + 1 : i + VN];
+                const float y = p * cs[i] - r * sn[i];
+                r = r * cs[i] + p * sn[i];
+                p = y;
+            }
+            u0 = Vec<T>::pack(x);
+            u1 = Vec<T>::pack(x + VN);
+        }
+        T* dst = (h < a.Hq ? qo : h < a.Hq + a.Hkv ? kc : vc) + (long long)h * D;
         *reinterpret_cast<uint4*>(dst + e0) = u0;
         *reinterpret_cast<uint4*>(dst + e1) = u1;
+        u0 = n0;
+        u1 = n1;
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-    constexpr int ITEMS = D / (2 * Vec<T>::N), LANES = kRopeThreads / ITEMS;
-    // one token a block while that leaves SMs idle, four otherwise
-    const int tok = a.T <= 4 * num_sms ? 1 : 4;
-    const dim3 grid(static_cast<unsigned>((a.T + tok - 1) / tok), 1);
-    (void)LANES;
+    // Tokens a block: as many as leave a thread up to 8 heads to go through (fewer heads do not
+    // pay for the block's angles and start-up, more leave a ragged last wave), but at least three
+    // blocks an SM.  4096 tokens of 80 heads: 1 / 2 / 4 / 8 tokens take 30.8 / 29.1 / 28.9 / 29.3
+    // us; 20011 of 48 heads: 97 / 82 / 78 / 82 us; 20000 of 24 heads of 64: 59 / 36 / 27 / 24 us (16: 26);
+    // 1024 of 80 heads: 9.6 / 8.8 / 10.9 / 16.4 us.
+    constexpr int LANES = kRopeThreads * 2 * Vec<T>::N / D;
+    int tok = 1;
+    while (tok < 8 && (a.Hq + 2LL * a.Hkv) * 2 * tok <= 8 * LANES && a.T >= 3LL * num_sms * 2 * tok) tok *= 2;
+    const dim3 grid(static_cast<unsigned>((a.T + tok - 1) / tok));
     const size_t smem = (size_t)tok * a.R * sizeof(float);
     return a.neighbours ? launch_pdl(rope_append_kernel<T, D, true>, grid, dim3(kRopeThreads), smem, stream, 1u, a, tok)
                         : launch_pdl(rope_append_kernel<T, D, false>, grid, dim3(kRopeThreads), smem, stream, 1u, a, tok);

@@ -48,7 +48,7 @@ def on_device(h):
     dt = h["dtype"]
     cu = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
     n = tsv.decode_attn_workspace_size(B, Hq, Hkv, D, bs, h["table"].shape[1], tsv.TSV_BF16 if dt == torch.bfloat16 else tsv.TSV_F32)
-    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN wherever it is read unwritten
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None  # NaN wherever it is read unwritten
     return dict(q=cu(h["q"]).to(dt), k_cache=cu(h["kc"]).to(dt), v_cache=cu(h["vc"]).to(dt), block_table=cu(h["table"]),
                 seq_lens=cu(h["lens"]), out=torch.full((B, Hq, D), 7.0, dtype=dt, device="cuda"), scale=h["scale"], workspace=ws,
                 seq_err=torch.full((B,), -9, dtype=torch.int32, device="cuda"), lse=torch.full((B, Hq), 7.0, device="cuda"))
@@ -87,14 +87,16 @@ SHAPES = [  # lens, Hq, Hkv, D, bs
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap", [0, 50000])  # a long table: lanes for more tiles than there are
 @pytest.mark.parametrize("lens,Hq,Hkv,D,bs", SHAPES)
-def test_decode(dtype, lens, Hq, Hkv, D, bs):
-    h = make(len(lens) + Hq + D, lens, Hq, Hkv, D, bs, dtype)
+def test_decode(dtype, cap, lens, Hq, Hkv, D, bs):
+    h = make(len(lens) + Hq + D, lens, Hq, Hkv, D, bs, dtype, cap=cap)
     d = on_device(h)
     tsv.decode_attn(**d)
     check(h, d)
     first, first_lse = d["out"].clone(), d["lse"].clone()
-    d["workspace"].fill_(127)
+    if d["workspace"] is not None:
+        d["workspace"].fill_(127)
     d["lse"] = None
     tsv.decode_attn(**d)
     torch.cuda.synchronize()
@@ -121,8 +123,9 @@ def test_large_scores(dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("L", [40, 5000])
-def test_infinities(dtype, L):
-    h = make(7, [L, L], 2, 2, 64, 16, dtype)
+@pytest.mark.parametrize("cap", [0, 50000])
+def test_infinities(dtype, L, cap):
+    h = make(7, [L, L], 2, 2, 64, 16, dtype, cap=cap)
     h["q"] = np.abs(h["q"])
     where = h["table"][0, (L // 2) // 16]
     h["kc"][where, (L // 2) % 16, 0] = -np.inf  # a key that no row attends to
@@ -153,8 +156,9 @@ def test_infinities(dtype, L):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_bad_lengths_and_blocks(dtype):
-    h = make(8, [100, 9000, 33, 700, 5000, 1], 8, 2, 64, 16, dtype)
+@pytest.mark.parametrize("cap", [0, 70000])
+def test_bad_lengths_and_blocks(dtype, cap):
+    h = make(8, [100, 9000, 33, 700, 5000, 1], 8, 2, 64, 16, dtype, cap=cap)
     nb = h["kc"].shape[0]
     h["lens"][2] = -1
     h["lens"][3] = h["table"].shape[1] * 16 + 1
@@ -169,8 +173,9 @@ def test_bad_lengths_and_blocks(dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("block", [-1, -2, -2 ** 31, None])
-def test_every_bad_id_is_found(dtype, block):
-    h = make(40, [300, 17], 4, 2, 64, 16, dtype)
+@pytest.mark.parametrize("cap", [0, 50000])
+def test_every_bad_id_is_found(dtype, block, cap):
+    h = make(40, [300, 17], 4, 2, 64, 16, dtype, cap=cap)
     h["table"][0, 9] = h["kc"].shape[0] if block is None else block
     d = on_device(h)
     tsv.decode_attn(**d)
@@ -178,11 +183,11 @@ def test_every_bad_id_is_found(dtype, block):
     assert d["seq_err"].tolist() == [2, 0]
 
 
-def test_two_graphs_share_a_workspace():
-    a, b = make(9, [3000, 10, 801], 8, 2, 128, 16, torch.bfloat16), make(10, [1, 2500, 0], 8, 2, 128, 16, torch.bfloat16, cap=3000)
+@pytest.mark.parametrize("cap", [3000, 40000])
+def test_two_graphs_share_a_workspace(cap):
+    a, b = (make(s, lens, 8, 2, 128, 16, torch.bfloat16, cap=cap) for s, lens in ((9, [3000, 10, 801]), (10, [1, 2500, 0])))
     da, db = on_device(a), on_device(b)
-    ws = da["workspace"] if da["workspace"].numel() >= db["workspace"].numel() else db["workspace"]
-    da["workspace"] = db["workspace"] = ws
+    db["workspace"] = da["workspace"]  # of the same size
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
@@ -208,7 +213,7 @@ def test_two_graphs_share_a_workspace():
 
 
 def test_two_streams_with_a_workspace_each():
-    hs = [make(20 + i, [4000, 17, 2300], 16, 2, 128, 16, torch.bfloat16) for i in range(2)]
+    hs = [make(20 + i, [4000, 17, 2300], 16, 2, 128, 16, torch.bfloat16, cap=60000 * i) for i in range(2)]
     ds = [on_device(h) for h in hs]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
@@ -238,7 +243,7 @@ def test_offsets_past_32_bits(dtype):
 
 
 def test_workspace_of_another_size_is_refused():
-    h = make(31, [4000], 8, 2, 128, 16, torch.bfloat16)
+    h = make(31, [4000], 8, 2, 128, 16, torch.bfloat16, cap=100000)
     d = on_device(h)
     d["workspace"] = d["workspace"][:-16]
     with pytest.raises(tsv.TsvError, match="workspace"):

@@ -68,13 +68,13 @@ def test_rope_empty_batch(lib):
     assert _rope(lib, q=P, k=P, v=P, qo=P, kc=P, vc=P, pos=P, T=0, err=P) == tsv.TSV_OK
 
 
-def _decode(lib, q=A, kc=A, vc=A, bt=A, sl=A, out=A, lse=P, B=2, Hq=8, Hkv=2, D=64, bs=16, mb=4, nb=8, scale=0.125, dt=0,
+def _decode(lib, q=A, kc=A, vc=A, bt=A, sl=A, out=A, lse=P, B=2, Hq=8, Hkv=2, D=64, bs=16, mb=4096, nb=8, scale=0.125, dt=0,
             ws=A, wsb=1 << 30, err=A):
     return lib.tsv_decode_attn(q, kc, vc, bt, sl, out, lse, B, Hq, Hkv, D, bs, mb, nb, scale, dt, ws, wsb, err, P)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(B=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1), (dict(D=96), 2), (dict(D=256), 2), (dict(bs=48), 2),
+    (dict(B=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1), (dict(B=1 << 28), 2), (dict(D=96), 2), (dict(D=256), 2), (dict(bs=48), 2),
     (dict(mb=0), 1), (dict(nb=0), 1), (dict(mb=1 << 27), 2), (dict(dt=2), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(q=M), 1), (dict(out=M), 1), (dict(kc=M), 1),
     (dict(vc=M), 1), (dict(q=P), 1), (dict(bt=P), 1), (dict(sl=P), 1), (dict(err=P), 1), (dict(ws=P), 1), (dict(wsb=16), 1),
@@ -88,7 +88,7 @@ def test_decode_workspace_query(lib):
     assert _decode(lib, B=0, q=P, out=P, ws=P, wsb=0) == tsv.TSV_OK
     assert tsv.decode_attn_workspace_size(2, 8, 2, 96, 16, 4, tsv.TSV_BF16) == 0
     assert tsv.decode_attn_workspace_size(0, 8, 2, 64, 16, 4, tsv.TSV_BF16) == 0
-    small, large = (tsv.decode_attn_workspace_size(B, 8, 2, 64, 16, 64, tsv.TSV_BF16) for B in (1, 64))
+    small, large = (tsv.decode_attn_workspace_size(B, 8, 2, 64, 16, 4096, tsv.TSV_BF16) for B in (1, 64))
     assert 0 < small <= large
 
 

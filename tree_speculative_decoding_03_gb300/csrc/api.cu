@@ -369,6 +369,7 @@ tsv_status check_decode_shapes(int B, int Hq, int Hkv, int D, int block_size, in
     if (st != TSV_OK) return st;
     if (Hq % Hkv) return fail(TSV_ERR_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
     if ((long long)max_blocks * block_size > (1LL << 30)) return fail(TSV_ERR_UNSUPPORTED, "a table row covers more than 2^30 slots");
+    if ((long long)B * Hq > (1LL << 30)) return fail(TSV_ERR_UNSUPPORTED, "B * Hq exceeds 2^30 query rows");
     return TSV_OK;
 }
 }  // namespace

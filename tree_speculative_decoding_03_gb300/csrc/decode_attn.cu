@@ -20,6 +20,10 @@
 // A warp works for itself: its own ring of tiles in shared memory, filled with asynchronous
 // copies that run ahead across segment boundaries, its own running (m, l, O) in registers, and
 // no block barrier anywhere.
+//
+// Joining inside the launch, through the shared memory of a cluster that owns a sequence's units,
+// was slower at every size tried: 8 sequences of 2048 keys 30.5 us (16 CTAs a cluster) against 20.1,
+// one of 100 keys 9.8 against 8.3.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -33,8 +37,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's share fill an SM's shared memory
 constexpr int kMaxTeam = 8;        // warps of a team
 constexpr int kMinTiles = 4;       // tiles of a lane, at least: fewer pieces to join when there is little work
-constexpr int kJoinRows = 2;       // query rows of a CTA of the join
-constexpr int kJoinGroups = 4;     // threads that share the pieces of an output element
+constexpr int kScratch = 72;       // floats of a warp beside its ring
+constexpr int kManyPieces = 4;     // pieces of a unit, on average, from which the join divides them
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
@@ -509,18 +513,103 @@ struct ToSlot {
 
 template <typename Core>
 __host__ __device__ constexpr int stages_of() { return kRingBytes / (2 * Core::KEYS * Core::ROWB); }
+constexpr size_t kDecodeSmem = (size_t)kWarps * (kRingBytes + kScratch * sizeof(float));
+
+// A warp's stream of tiles: the copies run STAGES - 1 tiles ahead and the block ids one more.
 template <typename Core>
-constexpr size_t decode_smem() { return (size_t)kWarps * (kRingBytes + 72 * sizeof(float)); }
+struct Stream {
+    using Elem = typename Core::Elem;
+    static constexpr int D = Core::D, KEYS = Core::KEYS, STAGES = stages_of<Core>(), RUNS = KEYS / 8;
+    static constexpr uint32_t HALF = KEYS * Core::ROWB, STAGE = 2 * HALF;
+    static constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
+    const DecodeArgs& a;
+    const uint32_t ring;
+    const int row_elems, lrow, lch, lane_elems;
+    Place f;           // the tile whose ids were fetched last
+    int ids[RUNS];     // its blocks (8 keys lie in one block); all lanes hold the same
+    uint32_t bad = 0;  // stages holding a tile with a block id outside the cache
+    int left;          // tiles not yet on their way
+    int fill = 0, stage = 0;
+
+    __device__ __forceinline__ Stream(const DecodeArgs& args, uint32_t ring_, const Place& p, int n)
+        : a(args), ring(ring_), row_elems(args.Hkv * D), lrow((threadIdx.x & 31) / LANES_ROW), lch((threadIdx.x & 31) % LANES_ROW),
+          lane_elems(lrow * row_elems + lch * (16 / (int)sizeof(Elem))), f(p), left(n) {}
+
+    __device__ __forceinline__ void fetch() {
+        const int32_t* bt = a.block_table + (long long)f.b * a.max_blocks;
+#pragma unroll
+        for (int u = 0; u < RUNS; ++u) {
+            const int key = f.t * KEYS + 8 * u;
+            ids[u] = key < f.keys ? __ldg(bt + (key >> a.bs_log2)) : 0;
+        }
+    }
+    // sends tile f on its way into stage `fill`, then fetches the next tile's ids
+    __device__ __forceinline__ void load() {
+        if (left > 0) {
+            const uint32_t dst = ring + fill * STAGE;
+            const Elem* kc = static_cast<const Elem*>(a.k_cache);
+            const Elem* vc = static_cast<const Elem*>(a.v_cache);
+            const long long head = (long long)(f.unit / a.groups) * D + lane_elems;
+            bool wrong = false;
+#pragma unroll
+            for (int u = 0; u < RUNS; ++u) {
+                const int key = f.t * KEYS + 8 * u;
+                const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
+                wrong |= !in && key < f.keys;
+                const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
+#pragma unroll
+                for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
+                    const bool take = in && key + r0 + lrow < f.keys;
+                    const long long off = take ? at + (long long)r0 * row_elems : 0;
+                    cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
+                    cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
+                }
+            }
+            bad = (bad & ~(1u << fill)) | (wrong ? 1u << fill : 0u);
+            if (--left > 0) {
+                f.next<KEYS>(a);
+                fetch();
+            }
+        }
+        cp_commit();
+        if (++fill == STAGES) fill = 0;
+    }
+    __device__ __forceinline__ void begin() {
+        if (left > 0) fetch();
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) load();
+    }
+    // the next tile: waits for it, keeps the copies ahead, adds it to the core's state
+    __device__ __forceinline__ bool step(Core& core, int live, float* scratch) {
+        cp_wait<STAGES - 2>();
+        __syncwarp();
+        load();
+        const uint32_t src = ring + stage * STAGE;
+        const bool wrong = ((bad >> stage) & 1u) != 0;
+        core.step(src, src + HALF, live, a.scale_log2, scratch);
+        __syncwarp();
+        if (++stage == STAGES) stage = 0;
+        return wrong;
+    }
+};
+
+template <typename Elem>
+__device__ __forceinline__ const Elem* q_of(const DecodeArgs& a, int D, const Place& u) {
+    return static_cast<const Elem*>(a.q) + ((long long)u.b * a.Hq + (u.unit / a.groups) * a.G + (u.unit % a.groups) * a.rows) * D;
+}
+__device__ __forceinline__ int rows_of(const DecodeArgs& a, int unit) { return min(a.rows, a.G - (unit % a.groups) * a.rows); }
+__device__ __forceinline__ long long first_head(const DecodeArgs& a, int b, int unit) {
+    return (long long)b * a.Hq + (unit / a.groups) * a.G + (unit % a.groups) * a.rows;
+}
 
 template <typename Core>
 __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_constant__ DecodeArgs a) {
     using Elem = typename Core::Elem;
-    constexpr int D = Core::D, KEYS = Core::KEYS, STAGES = stages_of<Core>(), RUNS = KEYS / 8;
-    constexpr uint32_t HALF = KEYS * Core::ROWB, STAGE = 2 * HALF;
+    constexpr int D = Core::D, KEYS = Core::KEYS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * 72;
+    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
     const int units = a.Hkv * a.groups;
     pdl_wait();
     pdl_launch_dependents();
@@ -544,97 +633,26 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
     Place p = locate<KEYS>(a, lane_me, me % a.team, &x, &x_end, &T);
     // for the join: a unit's last lane, where this lane leaves its first piece
     int4 left = make_int4(0, 0, -1, 0);
-    const int n = static_cast<int>(x_end - x), row_elems = a.Hkv * D;
-    const Elem* kc = static_cast<const Elem*>(a.k_cache);
-    const Elem* vc = static_cast<const Elem*>(a.v_cache);
-
-    // The copies run STAGES - 1 tiles ahead and the block ids one more: `f` is the tile whose
-    // ids are fetched last, `ids` its blocks (8 keys lie in one block).  All lanes hold the same
-    // ids.
-    Place f = p;
-    int ids[RUNS];
-    uint32_t bad_stage = 0;  // stages holding a tile with a block id outside the cache
-    auto fetch = [&] {
-        const int32_t* bt = a.block_table + (long long)f.b * a.max_blocks;
-#pragma unroll
-        for (int u = 0; u < RUNS; ++u) {
-            const int key = f.t * KEYS + 8 * u;
-            ids[u] = key < f.keys ? __ldg(bt + (key >> a.bs_log2)) : 0;
-        }
-    };
-    constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
-    const int lrow = lane / LANES_ROW, lch = lane % LANES_ROW;
-    const int lane_elems = lrow * row_elems + lch * (16 / (int)sizeof(Elem));
-    auto load = [&](int stage) {
-        const uint32_t dst = ring + stage * STAGE;
-        const long long head = (long long)(f.unit / a.groups) * D + lane_elems;
-        bool bad = false;
-#pragma unroll
-        for (int u = 0; u < RUNS; ++u) {
-            const int key = f.t * KEYS + 8 * u;
-            const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
-            bad |= !in && key < f.keys;
-            const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
-#pragma unroll
-            for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
-                const bool take = in && key + r0 + lrow < f.keys;
-                const long long off = take ? at + (long long)r0 * row_elems : 0;
-                cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
-                cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
-            }
-        }
-        bad_stage = (bad_stage & ~(1u << stage)) | (bad ? 1u << stage : 0u);
-    };
-    auto q_of = [&](const Place& u) {
-        return static_cast<const Elem*>(a.q) + ((long long)u.b * a.Hq + (u.unit / a.groups) * a.G + (u.unit % a.groups) * a.rows) * D;
-    };
-    auto rows_of = [&](const Place& u) { return min(a.rows, a.G - (u.unit % a.groups) * a.rows); };
-
+    const int n = static_cast<int>(x_end - x);
+    Stream<Core> stream(a, ring, p, n);
+    stream.begin();
     Core core;
-    int loaded = 0;
     if (n > 0) {
-        fetch();
-        core.load_q(q_of(p), rows_of(p));
+        core.load_q(q_of<Elem>(a, D, p), rows_of(a, p.unit));
         core.reset();
     }
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-        if (loaded < n) {
-            load(i);
-            if (++loaded < n) {
-                f.next<KEYS>(a);
-                fetch();
-            }
-        }
-        cp_commit();
-    }
     bool seg_bad = false;
-    int seg = 0, stage = 0, fill = STAGES - 1, t_first = p.t;
+    int seg = 0, t_first = p.t;
     for (int i = 0; i < n; ++i) {
-        cp_wait<STAGES - 2>();
-        __syncwarp();
-        if (loaded < n) {
-            load(fill);
-            if (++loaded < n) {
-                f.next<KEYS>(a);
-                fetch();
-            }
-        }
-        cp_commit();
-        if (++fill == STAGES) fill = 0;
-        seg_bad |= ((bad_stage >> stage) & 1u) != 0;
-        const uint32_t src = ring + stage * STAGE;
-        core.step(src, src + HALF, p.keys - p.t * KEYS, a.scale_log2, scratch);
-        __syncwarp();
-        if (++stage == STAGES) stage = 0;
+        seg_bad |= stream.step(core, p.keys - p.t * KEYS, scratch);
         if (p.t + 1 < p.tiles && i + 1 < n) {
             ++p.t;
             continue;
         }
         // the segment's end
-        const int nrows = rows_of(p);
+        const int nrows = rows_of(a, p.unit);
         if (t_first == 0 && p.t + 1 == p.tiles) {
-            const long long h = (long long)p.b * a.Hq + (p.unit / a.groups) * a.G + (p.unit % a.groups) * a.rows;
+            const long long h = first_head(a, p.b, p.unit);
             core.finish(nrows, ToResult<Elem, D>{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, seg_bad}, scratch);
             if (p.unit == 0 && lane == 0) a.seq_err[p.b] = seg_bad ? TSV_DERR_BLOCK : 0;
             if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
@@ -652,21 +670,23 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
             t_first = 0;
             seg_bad = false;
             ++seg;
-            core.load_q(q_of(p), rows_of(p));
+            core.load_q(q_of<Elem>(a, D, p), rows_of(a, p.unit));
             core.reset();
         }
     }
     if (!a.by_unit && lane == 0) a.split[me] = left;
 }
 
-// Joins the pieces of the units that lie on more than one lane, in lane order.  CTA (k, y) joins
-// query rows [kJoinRows y, ...) of the k-th unit, or of the unit whose first piece warp k has left,
-// whichever are fewer.  kJoinGroups threads share an element's pieces, each with kAhead of them in
-// flight.
-template <typename Elem, int D>
-__global__ void __launch_bounds__(kJoinRows* kJoinGroups* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+// Joins the pieces of the units that lie on more than one lane, in lane order.  CTA k joins the
+// k-th unit, or the unit whose first piece warp k has left, whichever are fewer: ROWS query rows at a
+// time, GROUPS threads to an output element, each with kAhead pieces in flight.  With many pieces a
+// unit, 8 threads share an element's pieces and blockIdx.y divides the rows; with few, small
+// CTAs go through all rows (256 sequences of 128 keys: 38 us, and 46 us with the shape for many;
+// one of 4096 keys: 12.7 and 10.4 us the other way round).
+template <typename Elem, int D, int GROUPS, int ROWS>
+__global__ void __launch_bounds__(ROWS* GROUPS* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kAhead = 8, VEC = D / 4;
-    __shared__ float s_part[kJoinGroups - 1][kJoinRows * VEC][6];
+    __shared__ float s_part[GROUPS > 1 ? GROUPS - 1 : 1][ROWS * VEC][6];
     pdl_wait();
     pdl_launch_dependents();
     const int4 sp = a.split[blockIdx.x];
@@ -674,92 +694,98 @@ __global__ void __launch_bounds__(kJoinRows* kJoinGroups* D / 4) decode_join_ker
     const int first_warp = sp.w >> 1, member = first_warp % a.team, k = first_warp / a.team, last = sp.z;
     const int b = sp.x, unit = sp.y;
     const int row0 = (unit % a.groups) * a.rows, nrows = min(a.rows, a.G - row0);
-    const int e = threadIdx.x % (kJoinRows * VEC), grp = threadIdx.x / (kJoinRows * VEC);
-    const int r = blockIdx.y * kJoinRows + e / VEC, d = (e % VEC) * 4;
-    if (blockIdx.y * kJoinRows >= nrows) return;
-    float M = -INFINITY, sum = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    int bad = 0;
-    for (int c = k + grp * kAhead; c <= last; c += kAhead * kJoinGroups) {
-        float m[kAhead], l[kAhead];
-        float4 o[kAhead];
+    const int e = threadIdx.x % (ROWS * VEC), grp = threadIdx.x / (ROWS * VEC), d = (e % VEC) * 4;
+    for (int r0 = blockIdx.y * ROWS; r0 < nrows; r0 += gridDim.y * ROWS) {
+        const int r = r0 + e / VEC;
+        if (GROUPS > 1 && r0 > static_cast<int>(blockIdx.y) * ROWS) __syncthreads();  // the last round's sums have been read
+        float M = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int bad = 0;
+        for (int c = k + grp * kAhead; c <= last; c += kAhead * GROUPS) {
+            float m[kAhead], l[kAhead];
+            float4 o[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
-            o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c + i <= last && r < nrows) {
-                const long long slot = 2LL * ((c + i) * a.team + member) + (c + i == k ? sp.w & 1 : 0), pr = slot * a.rows + r;
-                m[i] = a.part_m[pr];
-                l[i] = a.part_l[pr];
-                o[i] = *reinterpret_cast<const float4*>(a.part_o + pr * D + d);
-                bad |= a.part_bad[slot];
+            for (int i = 0; i < kAhead; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.0f;
+                o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c + i <= last && r < nrows) {
+                    const long long slot = 2LL * ((c + i) * a.team + member) + (c + i == k ? sp.w & 1 : 0), pr = slot * a.rows + r;
+                    m[i] = a.part_m[pr];
+                    l[i] = a.part_l[pr];
+                    o[i] = *reinterpret_cast<const float4*>(a.part_o + pr * D + d);
+                    bad |= a.part_bad[slot];
+                }
+            }
+            float m_new = M;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) m_new = fmaxf(m_new, m[i]);
+            const float ms = safe_max(m_new);
+            const float f0 = ex2(M - ms);
+            M = m_new;
+            sum *= f0;
+            acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float f = ex2(m[i] - ms);
+                sum = fmaf(f, l[i], sum);
+                acc = make_float4(fmaf(f, o[i].x, acc.x), fmaf(f, o[i].y, acc.y), fmaf(f, o[i].z, acc.z), fmaf(f, o[i].w, acc.w));
             }
         }
-        float m_new = M;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) m_new = fmaxf(m_new, m[i]);
-        const float ms = safe_max(m_new);
-        const float f0 = ex2(M - ms);
-        M = m_new;
-        sum *= f0;
-        acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const float f = ex2(m[i] - ms);
-            sum = fmaf(f, l[i], sum);
-            acc = make_float4(fmaf(f, o[i].x, acc.x), fmaf(f, o[i].y, acc.y), fmaf(f, o[i].z, acc.z), fmaf(f, o[i].w, acc.w));
+        if (grp > 0) {
+            float* s = s_part[grp - 1][e];
+            s[0] = M;
+            s[1] = sum;
+            s[2] = acc.x;
+            s[3] = acc.y;
+            s[4] = acc.z;
+            s[5] = acc.w;
         }
-    }
-    if (grp > 0) {
-        float* s = s_part[grp - 1][e];
-        s[0] = M;
-        s[1] = sum;
-        s[2] = acc.x;
-        s[3] = acc.y;
-        s[4] = acc.z;
-        s[5] = acc.w;
-    }
-    bad = __syncthreads_or(bad);
-    if (grp > 0 || r >= nrows) return;
+        if (GROUPS > 1) bad = __syncthreads_or(bad);
+        if (grp > 0 || r >= nrows) continue;
 #pragma unroll
-    for (int i = 0; i < kJoinGroups - 1; ++i) {
-        const float* s = s_part[i][e];
-        const float m_new = fmaxf(M, s[0]), ms = safe_max(m_new);
-        const float f0 = ex2(M - ms), f1 = ex2(s[0] - ms);
-        M = m_new;
-        sum = sum * f0 + s[1] * f1;
-        acc = make_float4(acc.x * f0 + s[2] * f1, acc.y * f0 + s[3] * f1, acc.z * f0 + s[4] * f1, acc.w * f0 + s[5] * f1);
+        for (int i = 0; i < GROUPS - 1; ++i) {
+            const float* s = s_part[i][e];
+            const float m_new = fmaxf(M, s[0]), ms = safe_max(m_new);
+            const float f0 = ex2(M - ms), f1 = ex2(s[0] - ms);
+            M = m_new;
+            sum = sum * f0 + s[1] * f1;
+            acc = make_float4(acc.x * f0 + s[2] * f1, acc.y * f0 + s[3] * f1, acc.z * f0 + s[4] * f1, acc.w * f0 + s[5] * f1);
+        }
+        const long long h = (long long)b * a.Hq + (unit / a.groups) * a.G + row0 + r;
+        const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, bad != 0};
+        const float inv = to.factor(sum);
+        to.two(0, d, acc.x * inv, acc.y * inv);
+        to.two(0, d + 2, acc.z * inv, acc.w * inv);
+        if (d == 0) to.row(0, M, sum);
+        if (d == 0 && r == 0 && unit == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : 0;
     }
-    const long long h = (long long)b * a.Hq + (unit / a.groups) * a.G + row0 + r;
-    const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, bad != 0};
-    const float inv = to.factor(sum);
-    to.two(0, d, acc.x * inv, acc.y * inv);
-    to.two(0, d + 2, acc.z * inv, acc.w * inv);
-    if (d == 0) to.row(0, M, sum);
-    if (d == 0 && r == 0 && unit == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : 0;
 }
 
 template <typename Core>
 cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
-    constexpr size_t smem = decode_smem<Core>();
     thread_local int smem_dev = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev != smem_dev) {
-        e = cudaFuncSetAttribute(decode_attn_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        constexpr int smem = static_cast<int>(kDecodeSmem);
+        e = cudaFuncSetAttribute(decode_attn_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         smem_dev = dev;
     }
     const int warps = a.lanes * a.team;
-    e = launch_pdl(decode_attn_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), smem,
-                   stream, 1u, a);
+    e = launch_pdl(decode_attn_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads),
+                   kDecodeSmem, stream, 1u, a);
     if (e != cudaSuccess || a.lanes < 2) return e;
-    const int most = min(a.rows, a.G);  // query rows of a unit
-    return launch_pdl(decode_join_kernel<typename Core::Elem, Core::D>,
-                      dim3(static_cast<unsigned>(a.by_unit ? a.B * a.Hkv * a.groups : warps - a.team), static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)),
-                      dim3(kJoinRows * kJoinGroups * Core::D / 4), 0, stream, 1u, a);
+    using Elem = typename Core::Elem;
+    constexpr int D = Core::D;
+    const int all = a.B * a.Hkv * a.groups;  // units
+    const unsigned records = static_cast<unsigned>(a.by_unit ? all : warps - a.team);
+    if (warps >= kManyPieces * (long long)all)
+        return launch_pdl(decode_join_kernel<Elem, D, 8, 1>, dim3(records, static_cast<unsigned>(min(a.rows, a.G))), dim3(8 * D / 4), 0,
+                          stream, 1u, a);
+    return launch_pdl(decode_join_kernel<Elem, D, 1, 4>, dim3(records), dim3(4 * D / 4), 0, stream, 1u, a);
 }
 
 template <int D>
@@ -782,12 +808,13 @@ DecodePlan make_decode_plan(int B, int Hq, int Hkv, int D, int block_size, int m
     p.rows = bf16 ? (G <= 16 ? 16 : 32) : (G >= 5 ? 8 : G >= 3 ? 4 : G);
     p.groups = (G + p.rows - 1) / p.rows;
     const int tile = bf16 ? 16 : 8, units = Hkv * p.groups;
+    const long long cap_tiles = ((long long)max_blocks * block_size + tile - 1) / tile;
     p.team = 1;
     for (int t = 2; t <= kMaxTeam; ++t)
         if (units % t == 0) p.team = t;
     // eight warps an SM, as many as the shared memory takes; never more than the table's capacity
     // gives kMinTiles each
-    const long long cap = (long long)B * (units / p.team) * (((long long)max_blocks * block_size + tile - 1) / tile);
+    const long long cap = (long long)B * (units / p.team) * cap_tiles;
     long long lanes = 2LL * kWarps * num_sms / p.team;
     if (lanes > cap / kMinTiles) lanes = cap / kMinTiles;
     p.lanes = lanes < 1 ? 1 : static_cast<int>(lanes);

@@ -38,7 +38,6 @@ constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's sha
 constexpr int kMaxTeam = 8;        // warps of a team
 constexpr int kMinTiles = 4;       // tiles of a lane, at least: fewer pieces to join when there is little work
 constexpr int kScratch = 72;       // floats of a warp beside its ring
-constexpr int kManyPieces = 4;     // pieces of a unit, on average, from which the join divides them
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
@@ -680,9 +679,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
 // Joins the pieces of the units that lie on more than one lane, in lane order.  CTA k joins the
 // k-th unit, or the unit whose first piece warp k has left, whichever are fewer: ROWS query rows at a
 // time, GROUPS threads to an output element, each with kAhead pieces in flight.  With many pieces a
-// unit, 8 threads share an element's pieces and blockIdx.y divides the rows; with few, small
-// CTAs go through all rows (256 sequences of 128 keys: 38 us, and 46 us with the shape for many;
-// one of 4096 keys: 12.7 and 10.4 us the other way round).
+// unit, 4 or 8 threads share an element's pieces and blockIdx.y divides the rows; with few, small
+// CTAs go through all rows.  Time of a call with 1, 4 and 8 threads: 0.6 pieces a unit 32 / - / 46
+// us; 9.5 pieces 14.2 / - / 16.2; 11.7 pieces 85.6 / 77.7 / 79.4; 19 pieces 59.7 / 50.2 / 52.9; 64
+// pieces - / 12.5 / 10.4.
 template <typename Elem, int D, int GROUPS, int ROWS>
 __global__ void __launch_bounds__(ROWS* GROUPS* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kAhead = 8, VEC = D / 4;
@@ -782,9 +782,9 @@ cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
     constexpr int D = Core::D;
     const int all = a.B * a.Hkv * a.groups;  // units
     const unsigned records = static_cast<unsigned>(a.by_unit ? all : warps - a.team);
-    if (warps >= kManyPieces * (long long)all)
-        return launch_pdl(decode_join_kernel<Elem, D, 8, 1>, dim3(records, static_cast<unsigned>(min(a.rows, a.G))), dim3(8 * D / 4), 0,
-                          stream, 1u, a);
+    const dim3 by_row(records, static_cast<unsigned>(min(a.rows, a.G)));
+    if (warps >= 32LL * all) return launch_pdl(decode_join_kernel<Elem, D, 8, 1>, by_row, dim3(8 * D / 4), 0, stream, 1u, a);
+    if (warps >= 10LL * all) return launch_pdl(decode_join_kernel<Elem, D, 4, 1>, by_row, dim3(4 * D / 4), 0, stream, 1u, a);
     return launch_pdl(decode_join_kernel<Elem, D, 1, 4>, dim3(records), dim3(4 * D / 4), 0, stream, 1u, a);
 }
 

@@ -391,11 +391,12 @@ tsv_status tsv_rope_kv_append(const void *q, const void *k, const void *v, const
  * Slots past L_b are never read into the result.  The keys of all sequences are divided
  * evenly between the GPU's SMs; pieces of a sequence are joined by log-sum-exp in a fixed order, so a
  * repeated call gives the same bits.  `workspace` as in tsv_tree_verify_attn, with
- * tsv_decode_attn_workspace_size(...) bytes.
+ * tsv_decode_attn_workspace_size(...) bytes; calls that may overlap on the GPU need one each.
+ * out and lse must not overlap the inputs.
  * seq_err[b]: TSV_DERR_CAPACITY (L_b < 0 or > max_blocks * block_size), TSV_DERR_BLOCK (a
  * block id covering [0, L_b) outside [0, num_blocks)); rows of a flagged sequence are NaN.
  * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128];
- * max_blocks * block_size up to 2^30.
+ * max_blocks * block_size and B * Hq up to 2^30.
  * ------------------------------------------------------------------------- */
 size_t tsv_decode_attn_workspace_size(int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
                                       tsv_dtype dtype);

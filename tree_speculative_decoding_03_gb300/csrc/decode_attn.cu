@@ -539,7 +539,7 @@ struct Stream {
 #pragma unroll
         for (int u = 0; u < RUNS; ++u) {
             const int key = f.t * KEYS + 8 * u;
-            ids[u] = key < f.keys ? __ldg(bt + (key >> a.bs_log2)) : 0;
+            ids[u] = key < f.keys ? (TSV_IN_BOUNDS(key >> a.bs_log2, a.max_blocks, nullptr) ? __ldg(bt + (key >> a.bs_log2)) : -1) : 0;
         }
     }
     // sends tile f on its way into stage `fill`, then fetches the next tile's ids
@@ -558,8 +558,11 @@ struct Stream {
                 const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
 #pragma unroll
                 for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
-                    const bool take = in && key + r0 + lrow < f.keys;
+                    bool take = in && key + r0 + lrow < f.keys;
                     const long long off = take ? at + (long long)r0 * row_elems : 0;
+                    // (an index check that fails is reported as a bad block)
+                    if (!TSV_IN_BOUNDS(off + 16 / (int)sizeof(Elem) - 1, ((long long)a.num_blocks << a.bs_log2) * row_elems, nullptr))
+                        wrong = true, take = false;
                     cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
                     cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
                 }
@@ -657,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
             if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
         } else {
             const long long slot = 2LL * me + (seg == 0 ? 0 : 1);
+            if (!TSV_IN_BOUNDS(slot, 2LL * a.lanes * a.team, a.seq_err + p.b)) return;
             core.finish(nrows, ToSlot<D>{a.part_o + slot * a.rows * D, a.part_m + slot * a.rows, a.part_l + slot * a.rows}, scratch);
             if (lane == 0) a.part_bad[slot] = seg_bad;
             if (t_first == 0) {

@@ -194,10 +194,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_consta
     };
     // block id at place p of the stack
     auto stack_at = [&](int p) {
-        if (p < count) return a.free_blocks[p];
+        if (p < count) return TSV_IN_BOUNDS(p, a.num_blocks, a.seq_err) ? a.free_blocks[p] : -1;
         const int i = p - count, b = first_above(s_back, a.B, i);
         if (b >= a.B) return -1;
-        return a.block_table[(long long)b * a.max_blocks + want_of(b) + (i - begin(s_back, b))];
+        const long long at = (long long)b * a.max_blocks + want_of(b) + (i - begin(s_back, b));
+        return TSV_IN_BOUNDS(at, (long long)a.B * a.max_blocks, a.seq_err + b) ? a.block_table[at] : -1;
     };
 
     const int t0 = rank * THREADS + tid;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_consta
             const int b = t < total ? first_above(s_tok, a.B, t) : a.B;
             if (b < a.B && s_err[b] == 0) {
                 const int j = t - begin(s_tok, b), at = s_len[b] + j, blk = at >> a.bs_log2, held = s_held[b];
-                const int id = blk < held ? a.block_table[(long long)b * a.max_blocks + blk]
+                const int id = blk < held ? (TSV_IN_BOUNDS(blk, a.max_blocks, a.seq_err + b) ? a.block_table[(long long)b * a.max_blocks + blk] : -1)
                                           : stack_at(top - 1 - (begin(s_grow, b) + blk - held));
                 const int depth = a.parent != nullptr ? depth_of(a.parent + (long long)b * a.N, j) : j;
                 int err = 0;
@@ -246,12 +247,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_consta
         k -= a.B;
         if (k < grown) {
             const int b = first_above(s_grow, a.B, k);
-            a.block_table[(long long)b * a.max_blocks + s_held[b] + (k - begin(s_grow, b))] = stack_at(top - 1 - k);
+            const int j = s_held[b] + (k - begin(s_grow, b));
+            if (TSV_IN_BOUNDS(j, a.max_blocks, a.seq_err + b)) a.block_table[(long long)b * a.max_blocks + j] = stack_at(top - 1 - k);
             continue;
         }
         k -= grown;  // a returned block that stays on the stack
         const int id = stack_at(count + k);
-        a.free_blocks[count + k] = id;
+        if (TSV_IN_BOUNDS(count + k, a.num_blocks, a.seq_err)) a.free_blocks[count + k] = id;
         if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
             const int b = first_above(s_back, a.B, k);
             if (b < a.B) atomicOr(&a.seq_err[b], TSV_DERR_BLOCK);
@@ -311,7 +313,8 @@ __global__ void __launch_bounds__(kFillThreads) kv_plan_fill_kernel(const __grid
             const bool held_back = (e & (TSV_DERR_CAPACITY | TSV_DERR_POOL)) != 0 || (a.parent != nullptr && n > a.N);
             if (!held_back) {
                 const int at = tot - n + j;
-                const int id = a.block_table[(long long)b * a.max_blocks + (at >> a.bs_log2)];
+                const int blk = at >> a.bs_log2;
+                const int id = TSV_IN_BOUNDS(blk, a.max_blocks, a.seq_err + b) ? a.block_table[(long long)b * a.max_blocks + blk] : -1;
                 const int depth = a.parent != nullptr ? depth_of(a.parent + (long long)b * a.N, j) : j;
                 int err = 0;
                 if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     }
     T* kc = static_cast<T*>(a.k_cache) + (slot * a.Hkv - a.Hq) * D;
     T* vc = static_cast<T*>(a.v_cache) + (slot * a.Hkv - a.Hq - a.Hkv) * D;
+    if (!TSV_IN_BOUNDS((slot + 1) * a.Hkv * D - 1, a.slots * a.Hkv * D, a.tok_err + t)) return;
     for (int h = h0; h < heads; h += hl) {
         uint4 n0 = u0, n1 = u1;
         if (h + hl < heads) {

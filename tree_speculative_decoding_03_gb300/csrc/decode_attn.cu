@@ -220,7 +220,10 @@ struct Bf16Core {
     }
 };
 
-// fp32: multiply-adds on the FMA pipe.  For the scores 8 dimensions of each row sit in a lane,
+// fp32: multiply-adds on the FMA pipe.  Up to 8 rows a unit it follows memory (1 row 94 % of the
+// copy rate, 4 rows 91 %, 8 rows 79 %); 16 rows are two units that read the keys twice.  Pairs of
+// multiply-adds to an instruction, and 16 rows to a unit, took as long (16 rows: 201 us against
+// 198; 8 rows: 52 against 51).  For the scores 8 dimensions of each row sit in a lane,
 // D / 8 lanes a key, and the lanes' sums are exchanged so that each ends with one row's score;
 // for the second product a lane owns D / 32 dimensions of all rows and the weights come from
 // shared memory.
@@ -683,10 +686,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
 // Joins the pieces of the units that lie on more than one lane, in lane order.  CTA k joins the
 // k-th unit, or the unit whose first piece warp k has left, whichever are fewer: ROWS query rows at a
 // time, GROUPS threads to an output element, each with kAhead pieces in flight.  With many pieces a
-// unit, 4 or 8 threads share an element's pieces and blockIdx.y divides the rows; with few, small
+// unit, 4 to 16 threads share an element's pieces and blockIdx.y divides the rows; with few, small
 // CTAs go through all rows.  Time of a call with 1, 4 and 8 threads: 0.6 pieces a unit 32 / - / 46
 // us; 9.5 pieces 14.2 / - / 16.2; 11.7 pieces 85.6 / 77.7 / 79.4; 19 pieces 59.7 / 50.2 / 52.9; 64
-// pieces - / 12.5 / 10.4.
+// pieces - / 12.5 / 10.4; 304 pieces - / - / 28.5, with 16 threads 22.2.
 template <typename Elem, int D, int GROUPS, int ROWS>
 __global__ void __launch_bounds__(ROWS* GROUPS* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kAhead = 8, VEC = D / 4;
@@ -787,6 +790,7 @@ cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
     const int all = a.B * a.Hkv * a.groups;  // units
     const unsigned records = static_cast<unsigned>(a.by_unit ? all : warps - a.team);
     const dim3 by_row(records, static_cast<unsigned>(min(a.rows, a.G)));
+    if (warps >= 96LL * all) return launch_pdl(decode_join_kernel<Elem, D, 16, 1>, by_row, dim3(16 * D / 4), 0, stream, 1u, a);
     if (warps >= 32LL * all) return launch_pdl(decode_join_kernel<Elem, D, 8, 1>, by_row, dim3(8 * D / 4), 0, stream, 1u, a);
     if (warps >= 10LL * all) return launch_pdl(decode_join_kernel<Elem, D, 4, 1>, by_row, dim3(4 * D / 4), 0, stream, 1u, a);
     return launch_pdl(decode_join_kernel<Elem, D, 1, 4>, dim3(records), dim3(4 * D / 4), 0, stream, 1u, a);

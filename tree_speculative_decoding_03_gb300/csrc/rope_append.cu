@@ -184,14 +184,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 
 template <typename T, int D>
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
-    // Tokens a block: as many as leave a thread up to 8 heads to go through (fewer heads do not
-    // pay for the block's angles and start-up, more leave a ragged last wave), but at least three
-    // blocks an SM.  4096 tokens of 80 heads: 1 / 2 / 4 / 8 tokens take 30.8 / 29.1 / 28.9 / 29.3
-    // us; 20011 of 48 heads: 97 / 82 / 78 / 82 us; 20000 of 24 heads of 64: 59 / 36 / 27 / 24 us (16: 26);
-    // 1024 of 80 heads: 9.6 / 8.8 / 10.9 / 16.4 us.
+    // Tokens a block: up to 8, as many as leave a thread at most 8 heads to go through (fewer heads do
+    // not pay for the block's angles and start-up, more leave a ragged last wave), more than 8
+    // until a thread has two heads, and always at least three blocks an SM.  With 1 / 2 / 4 / 8 / 16
+    // tokens: 4096 tokens of 80 heads 30.8 / 29.1 / 28.9 / 29.3 / - us; 20011 of 48 heads 97 / 82 / 78 /
+    // 82 / -; 20000 of 24 heads of 64 59 / 36 / 27 / 24 / 27; 1024 of 80 heads 9.6 / 8.8 / 10.9 / 16.4 / -;
+    // 27892 of 6 heads of 64 with 8 tokens 16.2, with 32 13.2.
     constexpr int LANES = kRopeThreads * 2 * Vec<T>::N / D;
+    const long long heads = a.Hq + 2LL * a.Hkv;
     int tok = 1;
-    while (tok < 8 && (a.Hq + 2LL * a.Hkv) * 2 * tok <= 8 * LANES && a.T >= 3LL * num_sms * 2 * tok) tok *= 2;
+    while (2 * tok <= LANES && a.T >= 3LL * num_sms * 2 * tok && (tok < 8 ? heads * 2 * tok <= 8 * LANES : heads * tok < 2 * LANES))
+        tok *= 2;
     const dim3 grid(static_cast<unsigned>((a.T + tok - 1) / tok));
     const size_t smem = (size_t)tok * a.R * sizeof(float);
     return a.neighbours ? launch_pdl(rope_append_kernel<T, D, true>, grid, dim3(kRopeThreads), smem, stream, 1u, a, tok)

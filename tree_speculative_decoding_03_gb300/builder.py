@@ -29,12 +29,14 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 
 def _sources():
-    # CUDA translation units and the host-only C++ ones (tree construction)
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    # CUDA translation units (those of the serving operators in their own folder) and the
+    # host-only C++ ones (tree construction)
+    return sorted(p for pat in ("*.cu", "*.cpp", "serving/*.cu") for p in glob.glob(os.path.join(CSRC, pat)))
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = [p for pat in ("*.cuh", "serving/*.cuh") for p in glob.glob(os.path.join(CSRC, pat))]
+    return _sources() + headers + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 # Test builds of the same sources: "checked" adds device-side index checks

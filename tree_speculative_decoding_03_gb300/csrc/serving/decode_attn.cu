@@ -26,7 +26,7 @@
 // one of 100 keys 9.8 against 8.3.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "../common.cuh"
 #include "serving_args.cuh"
 
 namespace tsv {

@@ -18,7 +18,7 @@
 #include <climits>
 #include <cooperative_groups.h>
 
-#include "common.cuh"
+#include "../common.cuh"
 #include "serving_args.cuh"
 
 namespace tsv {

@@ -13,7 +13,7 @@
 // (i, i + R/2) vector c and its partner R/2 elements on, otherwise vectors 2c and 2c + 1.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "../common.cuh"
 #include "serving_args.cuh"
 
 namespace tsv {

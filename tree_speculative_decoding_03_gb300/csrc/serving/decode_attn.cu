@@ -4,12 +4,15 @@
 //   s_t = scale * q . k_t (t < L),  out = sum_t e^{s_t - m} v_t / l,  m = max s,  l = sum_t e^{s_t - m},
 //   lse = m + ln l.
 // Each K/V row is read once; the Hq / Hkv query rows of a kv head share it (about that many
-// multiply-adds per element), so the call is bound by the cache's bytes.
+// multiply-adds per element), so the call is bound by the cache's bytes: 64 sequences of 64/8 heads,
+// 1.06 M keys, 4.36 GB in 620 us (7.0 TB/s, 1.04 of the measured copy rate); 13 fp32 sequences, 480 MB in
+// 78 us (6.1 TB/s).  Calls of tens of MB spend as long on launch, schedule, first loads and the
+// join: 8 sequences of 2048 keys, 67 MB, 20 us.
 //
 // Work split: a unit is (sequence, kv head, group of query rows).  Its keys are cut into tiles
 // of 16 (bf16) or 8 (fp32) keys.  `team` warps take as many units of one sequence together, each
 // warp one unit and all of them the same keys, so neighbouring heads of a cache row, which are
-// neighbours in memory, are read at about the same time.  The tiles of all teams' units,
+// neighbours in memory, are read at about the same time (4.36 GB: 625 us, 660 without).  The tiles of all teams' units,
 // sequence-major, form one row that is divided evenly between `lanes` teams, so every warp
 // streams the same bytes whatever the mix of lengths.  A warp goes through its tiles as
 // segments, one per unit it touches.  A segment that is a whole unit writes the result; the
@@ -22,8 +25,9 @@
 // no block barrier anywhere.
 //
 // Joining inside the launch, through the shared memory of a cluster that owns a sequence's units,
-// was slower at every size tried: 8 sequences of 2048 keys 30.5 us (16 CTAs a cluster) against 20.1,
-// one of 100 keys 9.8 against 8.3.
+// does not pay: 8 sequences of 2048 keys 30.5 us (16 CTAs a cluster) against 20.1, one of 100 keys 9.8
+// against 8.3, one of 4096 18.2 against 10.4; it gained only where a sequence is short and there are
+// several (16 of 512 keys: 12.8 against 13.8).
 #include <cuda_bf16.h>
 
 #include "../common.cuh"
@@ -36,7 +40,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's share fill an SM's shared memory
 constexpr int kMaxTeam = 8;        // warps of a team
-constexpr int kMinTiles = 4;       // tiles of a lane, at least: fewer pieces to join when there is little work
+// tiles of a lane, at least: fewer pieces to join when there is little work, more latencies in a
+// row (one sequence of 4096 keys with 2 / 3 / 4 / 6 tiles: 11.4 / 12.5 / 10.4 / 14.7 us)
+constexpr int kMinTiles = 4;
 constexpr int kScratch = 72;       // floats of a warp beside its ring
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -376,8 +382,10 @@ struct F32Core {
 // ------------------------------------------------------------------ the schedule
 
 // Keys of sequence b that are attended to: 0 when its length does not fit the block table.
+// (AHEAD: read before the wait for the kernel before, past the L1 cache.)
+template <bool AHEAD = false>
 __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
-    const int L = __ldg(a.seq_lens + b);
+    const int L = AHEAD ? __ldcg(a.seq_lens + b) : __ldg(a.seq_lens + b);
     return (L < 0 || (long long)L > ((long long)a.max_blocks << a.bs_log2)) ? 0 : L;
 }
 
@@ -472,6 +480,33 @@ __device__ __forceinline__ Place locate(const DecodeArgs& a, int which, int memb
         base = __shfl_sync(0xffffffffu, end, 31);
     }
     return p;
+}
+
+// One warp: where the pieces of unit `record` (of all units) lie, as the main kernel leaves them:
+// sequence, unit, last lane (-1: in one piece, or no keys) and first slot.
+template <int TILE>
+__device__ __forceinline__ int4 unit_pieces(const DecodeArgs& a, int record) {
+    const int lane = threadIdx.x & 31, units = a.Hkv * a.groups, b = record / units, unit = record % units;
+    long long T = 0, first = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int tiles = (seq_keys<true>(a, i) + TILE - 1) / TILE;
+        T += tiles;
+        first += i < b ? tiles : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        T += __shfl_xor_sync(0xffffffffu, T, o);
+        first += __shfl_xor_sync(0xffffffffu, first, o);
+    }
+    const int tiles = (seq_keys<true>(a, b) + TILE - 1) / TILE, per_seq = units / a.team;
+    T *= per_seq;
+    first = first * per_seq + (long long)(unit / a.team) * tiles;
+    if (tiles == 0) return make_int4(b, unit, -1, 0);
+    const int lanes = lanes_of(T, a.lanes);
+    const int c0 = lane_of_tile(first, T, lanes), c1 = lane_of_tile(first + tiles - 1, T, lanes);
+    if (c0 == c1) return make_int4(b, unit, -1, 0);
+    // the piece is the lane's first segment if the lane starts with the unit
+    return make_int4(b, unit, c1, 2 * (c0 * a.team + unit % a.team) + (lane_start(c0, T, lanes) == first ? 0 : 1));
 }
 
 template <typename T>
@@ -615,7 +650,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
     float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
-    const int units = a.Hkv * a.groups;
     pdl_wait();
     pdl_launch_dependents();
     // sequences without keys: nothing to attend to (zeros), or a length that does not fit (NaN)
@@ -628,8 +662,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
         if (a.lse != nullptr)
             for (int h = tid; h < a.Hq; h += kThreads) a.lse[(long long)b * a.Hq + h] = empty ? -INFINITY : x;
         if (tid == 0) a.seq_err[b] = empty ? 0 : TSV_DERR_CAPACITY;
-        if (a.by_unit)
-            for (int u = tid; u < units; u += kThreads) a.split[(long long)b * units + u] = make_int4(b, u, -1, 0);
     }
     const int me = blockIdx.x * kWarps + warp;
     const int lane_me = me / a.team;
@@ -660,16 +692,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
             const long long h = first_head(a, p.b, p.unit);
             core.finish(nrows, ToResult<Elem, D>{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, seg_bad}, scratch);
             if (p.unit == 0 && lane == 0) a.seq_err[p.b] = seg_bad ? TSV_DERR_BLOCK : 0;
-            if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
         } else {
             const long long slot = 2LL * me + (seg == 0 ? 0 : 1);
             if (!TSV_IN_BOUNDS(slot, 2LL * a.lanes * a.team, a.seq_err + p.b)) return;
             core.finish(nrows, ToSlot<D>{a.part_o + slot * a.rows * D, a.part_m + slot * a.rows, a.part_l + slot * a.rows}, scratch);
             if (lane == 0) a.part_bad[slot] = seg_bad;
-            if (t_first == 0) {
-                left = make_int4(p.b, p.unit, lane_of_tile(x + i - p.t + p.tiles - 1, T, lanes_of(T, a.lanes)), me * 2 + (seg == 0 ? 0 : 1));
-                if (a.by_unit && lane == 0) a.split[(long long)p.b * units + p.unit] = left;
-            }
+            if (t_first == 0)
+                left = make_int4(p.b, p.unit, lane_of_tile(x + i - p.t + p.tiles - 1, T, lanes_of(T, a.lanes)), static_cast<int>(slot));
         }
         if (i + 1 < n) {
             p.next<KEYS>(a);
@@ -690,13 +719,18 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
 // CTAs go through all rows.  Time of a call with 1, 4 and 8 threads: 0.6 pieces a unit 32 / - / 46
 // us; 9.5 pieces 14.2 / - / 16.2; 11.7 pieces 85.6 / 77.7 / 79.4; 19 pieces 59.7 / 50.2 / 52.9; 64
 // pieces - / 12.5 / 10.4; 304 pieces - / - / 28.5, with 16 threads 22.2.
-template <typename Elem, int D, int GROUPS, int ROWS>
+template <typename Elem, int D, int KEYS, int GROUPS, int ROWS>
 __global__ void __launch_bounds__(ROWS* GROUPS* D / 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
     constexpr int kAhead = 8, VEC = D / 4;
     __shared__ float s_part[GROUPS > 1 ? GROUPS - 1 : 1][ROWS * VEC][6];
+    // With a record per unit the schedule is worked out here, from the lengths, which the kernel
+    // before this one has waited for before it let this one start: so the pieces are known when
+    // the wait ends.
+    int4 sp = make_int4(0, 0, -1, 0);
+    if (a.by_unit) sp = unit_pieces<KEYS>(a, blockIdx.x);
     pdl_wait();
     pdl_launch_dependents();
-    const int4 sp = a.split[blockIdx.x];
+    if (!a.by_unit) sp = a.split[blockIdx.x];
     if (sp.z < 0) return;
     const int first_warp = sp.w >> 1, member = first_warp % a.team, k = first_warp / a.team, last = sp.z;
     const int b = sp.x, unit = sp.y;
@@ -790,10 +824,10 @@ cudaError_t launch_core(const DecodeArgs& a, cudaStream_t stream) {
     const int all = a.B * a.Hkv * a.groups;  // units
     const unsigned records = static_cast<unsigned>(a.by_unit ? all : warps - a.team);
     const dim3 by_row(records, static_cast<unsigned>(min(a.rows, a.G)));
-    if (warps >= 96LL * all) return launch_pdl(decode_join_kernel<Elem, D, 16, 1>, by_row, dim3(16 * D / 4), 0, stream, 1u, a);
-    if (warps >= 32LL * all) return launch_pdl(decode_join_kernel<Elem, D, 8, 1>, by_row, dim3(8 * D / 4), 0, stream, 1u, a);
-    if (warps >= 10LL * all) return launch_pdl(decode_join_kernel<Elem, D, 4, 1>, by_row, dim3(4 * D / 4), 0, stream, 1u, a);
-    return launch_pdl(decode_join_kernel<Elem, D, 1, 4>, dim3(records), dim3(4 * D / 4), 0, stream, 1u, a);
+    if (warps >= 96LL * all) return launch_pdl(decode_join_kernel<Elem, D, Core::KEYS, 16, 1>, by_row, dim3(16 * D / 4), 0, stream, 1u, a);
+    if (warps >= 32LL * all) return launch_pdl(decode_join_kernel<Elem, D, Core::KEYS, 8, 1>, by_row, dim3(8 * D / 4), 0, stream, 1u, a);
+    if (warps >= 10LL * all) return launch_pdl(decode_join_kernel<Elem, D, Core::KEYS, 4, 1>, by_row, dim3(4 * D / 4), 0, stream, 1u, a);
+    return launch_pdl(decode_join_kernel<Elem, D, Core::KEYS, 1, 4>, dim3(records), dim3(4 * D / 4), 0, stream, 1u, a);
 }
 
 template <int D>

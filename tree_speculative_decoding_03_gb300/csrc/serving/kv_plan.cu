@@ -25,9 +25,13 @@ namespace tsv {
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int kPlanCluster = 8;
+// Launches by size, us in a stream (one CTA / a cluster of 16 / the cluster and a fill kernel): 8 trees
+// of 6 nodes 3.7 / 4.7 / 6.7; 32 of 16 4.2 / 4.6 / 8.2; 16 of 64 6.6 / 5.7 / 14.2; 512 of 64 - / 9.5 / 15.7; 1000
+// prompts of 60 tokens - / 8.3 / 10.0; 1000 trees of 64 - / 15.6 / 15.9; 1000 prompts of 255 tokens with a
+// cluster of 8 36.6, with the fill kernel 9.4.  Against 16 CTAs a cluster of 8 takes 15.2 for 512 x 64.
+constexpr int kPlanCluster = 16;
 constexpr int kPlanSmallSeqs = 64, kPlanSmallTokens = 512;  // one CTA up to here
-constexpr int kPlanClusterTokens = 32768;                  // tokens by the cluster up to here
+constexpr int kPlanClusterTokens = 65536;                  // tokens by the cluster up to here
 constexpr int kFillThreads = 256, kFillTokens = 4;  // the second kernel: threads, tokens of a thread
 
 // First i in [0, n) with end[i] > x (n when there is none): the sequence item x falls in.
@@ -336,19 +340,17 @@ __global__ void __launch_bounds__(kFillThreads) kv_plan_fill_kernel(const __grid
 template <int THREADS, int CLUSTER, bool TOKENS>
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.B * (5 * sizeof(int) + 1) + 16;
-    if (smem > 40 * 1024) {  // with the static part, past what a launch gets unasked
-        thread_local int smem_dev = -1;
-        thread_local size_t smem_set = 0;
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
+    // the kernel's limits, raised once per device and host thread
+    thread_local int set_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev != set_dev) {
+        const auto kernel = kv_plan_kernel<THREADS, CLUSTER, TOKENS>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxSeqs * (5 * (int)sizeof(int) + 1) + 16);
+        if (e == cudaSuccess && CLUSTER > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        if (dev != smem_dev || smem > smem_set) {
-            e = cudaFuncSetAttribute(kv_plan_kernel<THREADS, CLUSTER, TOKENS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            smem_dev = dev;
-            smem_set = smem;
-        }
+        set_dev = dev;
     }
     return launch_pdl(kv_plan_kernel<THREADS, CLUSTER, TOKENS>, dim3(CLUSTER), dim3(THREADS), smem, stream, CLUSTER, a);
 }

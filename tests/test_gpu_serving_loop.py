@@ -180,3 +180,28 @@ def test_single_token_attention_is_the_tree_attention_of_one_node():
                     workspace=ws, seq_err=e)
     # both are within 2^-7 sum p |v| of the exact result, |v| < 5
     assert not e.any() and np.abs(out.float().cpu().numpy().reshape(want.shape) - want).max() <= 2 * 2.0 ** -7 * 5
+
+
+def test_a_step_on_a_stream_of_its_own():
+    # all three operators on a side stream, against the same step on the default one
+    def step(stream):
+        c = Cache(B=3, Hq=4, Hkv=2, D=64, bs=8, nb=30, mb=8, seed=9)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        n, T = torch.tensor([5, 17, 0], **i32), 22
+        offs, slots, pos = torch.empty(4, **i32), torch.empty(T, dtype=torch.int64, device="cuda"), torch.empty(T, **i32)
+        err, terr, total, derr = (torch.empty(k, **i32) for k in (3, T, 3, 3))
+        x = torch.from_numpy(U.bf16_round(c.r.standard_normal((T, 8, 64)).astype(np.float32))).to(c.dtype).cuda()
+        q, out = torch.empty(T, 4, 64, dtype=c.dtype, device="cuda"), torch.empty(3, 4, 64, dtype=c.dtype, device="cuda")
+        inv, lse = torch.from_numpy(c.inv).cuda(), torch.empty(3, 4, device="cuda")
+        ws = torch.empty(tsv.decode_attn_workspace_size(3, 4, 2, 64, 8, 8, tsv.TSV_BF16), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        tsv.kv_plan_slots(c.lens, n, c.table, c.held, c.held, c.pool, c.count, c.count, total, offs, slots, pos, 8, err, stream=stream)
+        tsv.rope_kv_append(x[:, :4], x[:, 4:6], x[:, 6:], pos, inv, q, c.k, c.v, slots, terr, stream=stream)
+        tsv.decode_attn(q[:3], c.k, c.v, c.table, total, out, 0.125, workspace=ws, seq_err=derr, lse=lse, stream=stream)
+        torch.cuda.synchronize()
+        assert not err.any() and not terr.any() and not derr.any()
+        return [c.table, c.held, c.pool[:20], c.count, total, offs, slots, pos, q, out, lse]
+
+    for a, b in zip(step(None), step(torch.cuda.Stream())):
+        assert torch.equal(a, b)
+    assert torch.isfinite(a[:2]).all() and (a[2] == -float("inf")).all()

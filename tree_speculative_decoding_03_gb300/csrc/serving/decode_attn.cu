@@ -10,7 +10,7 @@
 // join: 8 sequences of 2048 keys, 67 MB, 20 us.
 //
 // Work split: a unit is (sequence, kv head, group of query rows).  Its keys are cut into tiles
-// of 16 (bf16) or 8 (fp32) keys.  `team` warps take as many units of one sequence together, each
+// of 8 KB (bf16, D = 128: 16 keys).  `team` warps take as many units of one sequence together, each
 // warp one unit and all of them the same keys, so neighbouring heads of a cache row, which are
 // neighbours in memory, are read at about the same time (4.36 GB: 625 us, 660 without).  The tiles of all teams' units,
 // sequence-major, form one row that is divided evenly between `lanes` teams, so every warp
@@ -43,7 +43,11 @@ constexpr int kMaxTeam = 8;        // warps of a team
 // tiles of a lane, at least: fewer pieces to join when there is little work, more latencies in a
 // row (one sequence of 4096 keys with 2 / 3 / 4 / 6 tiles: 11.4 / 12.5 / 10.4 / 14.7 us)
 constexpr int kMinTiles = 4;
-constexpr int kScratch = 72;       // floats of a warp beside its ring
+constexpr int kFewLanes = 64;  // up to here two tiles do (one sequence of 256 fp32 keys 7.9 -> 6.9 us, 16 of 1 to 60 11.6 -> 8.3)
+constexpr int kScratch = 136;      // floats of a warp beside its ring
+
+// Keys of a tile: its K and V rows are 8 KB.
+__host__ __device__ constexpr int tile_keys(bool bf16, int D) { return 4096 / (D * (bf16 ? 2 : 4)); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
@@ -87,7 +91,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ------------------------------------------------------------------ the two element types
-// Keys of a warp's chunk, the stage bytes, and the running state of ROWS query rows.
+// A warp's part of a tile, and the running state of its query rows.
 
 // bf16: products on the tensor cores, 16 rows a fragment (MT fragments).  With at most 16 rows
 // per K/V row the tensor rate is far from a limit (about 190 multiply-adds a clock and SM at
@@ -95,7 +99,7 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0
 // product (relative error 2^-9 of each weight, averaged over the keys; l sums the unrounded P).
 template <int D_, int MT>
 struct Bf16Core {
-    static constexpr int D = D_, KEYS = 16, ROWB = D * 2, CH = ROWB / 16;
+    static constexpr int D = D_, KEYS = tile_keys(true, D_), ROWB = D * 2, CH = ROWB / 16, NF = KEYS / 8;
     using Elem = __nv_bfloat16;
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4];
@@ -131,41 +135,47 @@ struct Bf16Core {
         }
     }
 
-    // `live` of the chunk's 16 keys exist
+    // `live` of the tile's keys exist
     __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, int live, float sl2, float*) {
         const int lane = threadIdx.x & 31;
-        float s[MT][2][4];
+        float s[MT][NF][4];  // 8 keys a fragment
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.0f;
+            for (int n = 0; n < NF; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.0f;
         {
             const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t b[4];
-                ldsm4(b, ks + place(row, 2 * kk + ((lane >> 3) & 1)));
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    mma16816(s[t][0], qf[t][kk], b[0], b[1]);
-                    mma16816(s[t][1], qf[t][kk], b[2], b[3]);
+                for (int n = 0; n < NF; n += 2) {
+                    uint32_t b[4];
+                    ldsm4(b, ks + place(8 * n + row, 2 * kk + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        mma16816(s[t][n], qf[t][kk], b[0], b[1]);
+                        mma16816(s[t][n + 1], qf[t][kk], b[2], b[3]);
+                    }
                 }
             }
         }
         const int k0 = (lane & 3) * 2;
-        uint32_t p[MT][4];
+        uint32_t p[MT][NF / 2][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if (live < KEYS) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NF; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (8 * n + k0 + (e & 1) >= live) s[t][n][e] = -INFINITY;
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float mx = fmaxf(fmaxf(s[t][0][2 * r], s[t][0][2 * r + 1]), fmaxf(s[t][1][2 * r], s[t][1][2 * r + 1])) * sl2;
+                float mx = fmaxf(s[t][0][2 * r], s[t][0][2 * r + 1]);
+#pragma unroll
+                for (int n = 1; n < NF; ++n) mx = fmaxf(mx, fmaxf(s[t][n][2 * r], s[t][n][2 * r + 1]));
+                mx *= sl2;
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float m_new = fmaxf(m[t][r], mx);
@@ -180,26 +190,29 @@ struct Bf16Core {
                     }
                 }
                 m[t][r] = m_new;
-                float w[2][2];
+                float sum = 0.0f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) w[n][e] = ex2(fmaf(s[t][n][2 * r + e], sl2, -ms));
-                l[t][r] += (w[0][0] + w[0][1]) + (w[1][0] + w[1][1]);
-                p[t][r] = pack_bf16(w[0][0], w[0][1]);
-                p[t][2 + r] = pack_bf16(w[1][0], w[1][1]);
+                for (int n = 0; n < NF; ++n) {
+                    const float w0 = ex2(fmaf(s[t][n][2 * r], sl2, -ms)), w1 = ex2(fmaf(s[t][n][2 * r + 1], sl2, -ms));
+                    sum += w0 + w1;
+                    p[t][n / 2][2 * (n & 1) + r] = pack_bf16(w0, w1);
+                }
+                l[t][r] += sum;
             }
         }
         {
             const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t b[4];
-                ldsm4_t(b, vs + place(row, 2 * i + (lane >> 4)));
+            for (int n = 0; n < NF / 2; ++n) {
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    mma16816(o[t][2 * i], p[t], b[0], b[1]);
-                    mma16816(o[t][2 * i + 1], p[t], b[2], b[3]);
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];
+                    ldsm4_t(b, vs + place(16 * n + row, 2 * i + (lane >> 4)));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        mma16816(o[t][2 * i], p[t][n], b[0], b[1]);
+                        mma16816(o[t][2 * i + 1], p[t][n], b[2], b[3]);
+                    }
                 }
             }
         }
@@ -235,7 +248,7 @@ struct Bf16Core {
 // shared memory.
 template <int D_, int RR>
 struct F32Core {
-    static constexpr int D = D_, KEYS = 8, ROWB = D * 4, CH = ROWB / 16;
+    static constexpr int D = D_, KEYS = tile_keys(false, D_), ROWB = D * 4, CH = ROWB / 16;
     static constexpr int LPK = D / 8, KPP = 32 / LPK, PASSES = KEYS / KPP, DV = D / 32;
     using Elem = float;
     float qr[RR][8];
@@ -395,8 +408,8 @@ __device__ __forceinline__ int lane_of_tile(long long x, long long T, int lanes)
 }
 
 // Lanes that share T tiles.
-__device__ __forceinline__ int lanes_of(long long T, int lanes) {
-    const long long n = T / kMinTiles;
+__host__ __device__ __forceinline__ int lanes_of(long long T, int lanes) {
+    const long long few = T / 2 < kFewLanes ? T / 2 : kFewLanes, n = T / kMinTiles > few ? T / kMinTiles : few;
     return n < 1 ? 1 : n < lanes ? static_cast<int>(n) : lanes;
 }
 
@@ -849,17 +862,16 @@ DecodePlan make_decode_plan(int B, int Hq, int Hkv, int D, int block_size, int m
     // a unit's rows: one or two 16-row fragments (bf16); a power of two up to 8 (fp32)
     p.rows = bf16 ? (G <= 16 ? 16 : 32) : (G >= 5 ? 8 : G >= 3 ? 4 : G);
     p.groups = (G + p.rows - 1) / p.rows;
-    const int tile = bf16 ? 16 : 8, units = Hkv * p.groups;
+    const int tile = tile_keys(bf16, D), units = Hkv * p.groups;
     const long long cap_tiles = ((long long)max_blocks * block_size + tile - 1) / tile;
     p.team = 1;
     for (int t = 2; t <= kMaxTeam; ++t)
         if (units % t == 0) p.team = t;
-    // eight warps an SM, as many as the shared memory takes; never more than the table's capacity
-    // gives kMinTiles each
+    // eight warps an SM, as many as the shared memory takes; never more than share the table's
+    // capacity
     const long long cap = (long long)B * (units / p.team) * cap_tiles;
     long long lanes = 2LL * kWarps * num_sms / p.team;
-    if (lanes > cap / kMinTiles) lanes = cap / kMinTiles;
-    p.lanes = lanes < 1 ? 1 : static_cast<int>(lanes);
+    p.lanes = lanes_of(cap, static_cast<int>(lanes < 1 ? 1 : lanes));
     const size_t warps = (size_t)p.lanes * p.team;
     p.by_unit = (long long)B * units <= static_cast<long long>(warps);
     p.ws_bytes = 2 * warps * ((size_t)p.rows * (D + 2) * sizeof(float) + sizeof(int)) + warps * sizeof(int4);

@@ -250,3 +250,28 @@ def test_workspace_of_another_size_is_refused():
         tsv.decode_attn(**d)
     with pytest.raises(ValueError, match="device"):
         tsv.decode_attn(**{**on_device(h), "lse": torch.zeros(1, 8)})
+
+
+def test_host_threads_at_once():
+    import threading
+    hs = [make(50 + i, [700 * i + 5, 33], 8, 2, 128 if i % 2 else 64, 16, torch.bfloat16 if i < 3 else torch.float32) for i in range(4)]
+    ds, failed = [on_device(h) for h in hs], []
+    torch.cuda.synchronize()
+
+    def work(d):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    tsv.decode_attn(**d)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 - reported by the test below
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in ds]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for h, d in zip(hs, ds):
+        check(h, d)

@@ -387,7 +387,8 @@ tsv_status tsv_rope_kv_append(const void *q, const void *k, const void *v, const
  * L_b = seq_lens[b] (the new token's own K/V row included, already written):
  *   out[b,h,:] = softmax_t(scale * q[b,h,:] . k[t,g,:]) @ v[t,g,:],
  *   lse[b,h] = ln sum_t exp(scale * q[b,h,:] . k[t,g,:])   (lse may be NULL).
- * q, out [B, Hq, D]; lse [B, Hq] fp32.  L_b = 0: out is zero and lse -infinity.
+ * q, out [B, Hq, D]; lse [B, Hq] fp32.  L_b = 0: out is zero and lse -infinity.  Sums and weights
+ * are fp32 (a bf16 call's weights within 2^-15 of themselves); out is rounded once to dtype.
  * Slots past L_b are never read into the result.  The keys of all sequences are divided
  * evenly between the GPU's SMs; pieces of a sequence are joined by log-sum-exp in a fixed order, so a
  * repeated call gives the same bits.  `workspace` as in tsv_tree_verify_attn, with

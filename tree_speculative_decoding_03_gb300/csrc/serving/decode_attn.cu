@@ -87,6 +87,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
+// Two weights (0 or normal numbers) as the sum of two bf16 each.  hi is the next bf16 below the
+// weight, so lo = w - hi is exact in fp32 and positive, and rounded to at most 2^-8 of itself; a
+// positive weight has two positive parts, which keep an infinite value infinite (0 or a sign change
+// would make it NaN).
+__device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h0 = max(__float_as_uint(w0), 1u) - 1u, h1 = max(__float_as_uint(w1), 1u) - 1u;
+    *hi = __byte_perm(h0, h1, 0x7632);
+    *lo = pack_bf16(w0 - __uint_as_float(h0 & 0xffff0000u), w1 - __uint_as_float(h1 & 0xffff0000u));
+}
 // the reference point of the exponentials; a row that has seen only -inf scores keeps P = 0
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -95,8 +104,11 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0
 
 // bf16: products on the tensor cores, 16 rows a fragment (MT fragments).  With at most 16 rows
 // per K/V row the tensor rate is far from a limit (about 190 multiply-adds a clock and SM at
-// full memory speed), so the warp-level product serves; P is rounded to bf16 for the second
-// product (relative error 2^-9 of each weight, averaged over the keys; l sums the unrounded P).
+// full memory speed), so the warp-level product serves.  The second product takes each weight as
+// two bf16 parts, hi + lo, so a weight is off by at most 2^-15 of itself and the result by little
+// but its own rounding.  (One part alone is off by up to 2^-8, an error as large as the result's
+// rounding at any number of keys.  The second part's products take: 64 sequences of 64/8 heads 620 -> 622
+// us, 8 of 32/8 heads 19.9 -> 20.3, 32 of 64/1 heads 43.9 -> 48.4.)
 template <int D_, int MT>
 struct Bf16Core {
     static constexpr int D = D_, KEYS = tile_keys(true, D_), ROWB = D * 2, CH = ROWB / 16, NF = KEYS / 8;
@@ -160,7 +172,7 @@ struct Bf16Core {
             }
         }
         const int k0 = (lane & 3) * 2;
-        uint32_t p[MT][NF / 2][4];
+        uint32_t p[MT][NF / 2][4], p_lo[MT][NF / 2][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if (live < KEYS) {
@@ -195,7 +207,7 @@ struct Bf16Core {
                 for (int n = 0; n < NF; ++n) {
                     const float w0 = ex2(fmaf(s[t][n][2 * r], sl2, -ms)), w1 = ex2(fmaf(s[t][n][2 * r + 1], sl2, -ms));
                     sum += w0 + w1;
-                    p[t][n / 2][2 * (n & 1) + r] = pack_bf16(w0, w1);
+                    split_bf16(w0, w1, &p[t][n / 2][2 * (n & 1) + r], &p_lo[t][n / 2][2 * (n & 1) + r]);
                 }
                 l[t][r] += sum;
             }
@@ -210,6 +222,8 @@ struct Bf16Core {
                     ldsm4_t(b, vs + place(16 * n + row, 2 * i + (lane >> 4)));
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
+                        mma16816(o[t][2 * i], p_lo[t][n], b[0], b[1]);
+                        mma16816(o[t][2 * i + 1], p_lo[t][n], b[2], b[3]);
                         mma16816(o[t][2 * i], p[t][n], b[0], b[1]);
                         mma16816(o[t][2 * i + 1], p[t][n], b[2], b[3]);
                     }

@@ -336,7 +336,9 @@ tsv_status tsv_tree_reject_sample_compact_ex(const void *target_logits, const fl
  * slots are -1; one given back goes onto the stack as it is) and TSV_DERR_PARENT for a
  * parent row that is not a tree (positions of the nodes below the fault are -1) leave
  * the rest of the sequence as planned.
- * Negative lengths count as no tokens.  An empty batch writes nothing.  B <= 8192; block_size a power of two in
+ * Negative lengths count as no tokens.  B = 0: slot_map and positions are -1 throughout, token_offsets[0]
+ * is 0 and *free_count_out = *free_count (arrays of B entries and free_blocks may be NULL; with
+ * these five NULL too the call writes nothing).  B <= 8192; block_size a power of two in
  * [8, 128]; max_blocks * block_size, max_tokens and num_blocks up to 2^30.
  * ------------------------------------------------------------------------- */
 tsv_status tsv_kv_plan_slots(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *parent,

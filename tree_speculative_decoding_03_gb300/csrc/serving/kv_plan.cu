@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_consta
     const int t0 = rank * THREADS + tid;
     constexpr int kAll = CLUSTER * THREADS;
     const int tokens = TOKENS ? a.max_tokens : 0, pushed = pool_ok ? max(left - count, 0) : 0;
-    const long long items = (long long)tokens + a.B + grown + pushed;
+    const int seqs = max(a.B, 1);  // an empty batch has the first item's single words too
+    const long long items = (long long)tokens + seqs + grown + pushed;
     for (long long item = t0; item < items; item += kAll) {
         if (item < tokens) {
             const int t = static_cast<int>(item);
@@ -236,19 +237,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_plan_kernel(const __grid_consta
             continue;
         }
         int k = static_cast<int>(item - tokens);
-        if (k < a.B) {
-            const bool ok = s_err[k] == 0;
-            const int end = s_tok[k];
-            a.token_offsets[k + 1] = end;
+        if (k < seqs) {
             if (k == 0) {
                 a.token_offsets[0] = 0;
                 *a.free_count_out = pool_ok ? left : count;
             }
+            if (k >= a.B) continue;
+            const bool ok = s_err[k] == 0;
+            const int end = s_tok[k];
+            a.token_offsets[k + 1] = end;
             a.held_out[k] = ok ? want_of(k) : s_held[k];
             a.total_lens[k] = s_len[k] + (ok ? end - begin(s_tok, k) : 0);
             continue;
         }
-        k -= a.B;
+        k -= seqs;
         if (k < grown) {
             const int b = first_above(s_grow, a.B, k);
             const int j = s_held[b] + (k - begin(s_grow, b));
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kFillThreads) kv_plan_fill_kernel(const __grid
     pdl_wait();
     pdl_launch_dependents();
     const int* end = a.token_offsets + 1;
-    const int total = min(end[a.B - 1], a.max_tokens);
+    const int total = min(end[a.B - 1], a.max_tokens);  // (an empty batch: token_offsets[0], 0)
     if (tid < 64) {
         // warp 0: the sequence of the CTA's first token, warp 1: of its last; 32 probes a step
         const int lane = tid & 31, x = tid < 32 ? t0 : min(t1, total) - 1;

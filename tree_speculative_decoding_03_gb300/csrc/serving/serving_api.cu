@@ -70,9 +70,10 @@ tsv_status tsv_kv_plan_slots(const int32_t* seq_lens, const int32_t* new_lens, c
         return report_error(TSV_ERR_UNSUPPORTED, "max_tokens=%d or num_blocks=%d exceeds 2^30", max_tokens, num_blocks);
     if (parent != nullptr && N < 1) return report_error(TSV_ERR_ARG, "bad size N=%d", N);
     if (parent != nullptr && N > tsv::kMaxNodes) return report_error(TSV_ERR_UNSUPPORTED, "N=%d exceeds %d tree nodes", N, tsv::kMaxNodes);
-    if (B == 0) return TSV_OK;
-    if (!seq_lens || !new_lens || !block_table || !blocks_held || !blocks_held_out || !free_blocks || !free_count ||
-        !free_count_out || !total_lens || !token_offsets || !seq_err || (max_tokens > 0 && (!slot_map || !positions)))
+    // an empty batch has no per-sequence arrays; with none of the others either there is nothing to write
+    if (B == 0 && !free_count && !free_count_out && !token_offsets && !slot_map && !positions) return TSV_OK;
+    const bool per_seq = seq_lens && new_lens && block_table && blocks_held && blocks_held_out && free_blocks && total_lens && seq_err;
+    if ((B > 0 && !per_seq) || !free_count || !free_count_out || !token_offsets || (max_tokens > 0 && (!slot_map || !positions)))
         return report_error(TSV_ERR_ARG, "null array argument");
     tsv::PlanArgs a{};
     a.seq_lens = seq_lens;

@@ -364,7 +364,7 @@ tsv_status tsv_kv_plan_slots(const int32_t *seq_lens, const int32_t *new_lens, c
  * and tok_err[t] = TSV_DERR_BLOCK (otherwise 0; one int32 per token, overwritten).
  * Slots that are not negative must differ; q, k, v and the caches must not overlap
  * (but for q_out = q).  D in {64, 128}; rotary_dim a multiple of 16; bases and strides
- * 16-byte aligned.  opts NULL: {D, 0, 1, 0, {D / 2}}.
+ * 16-byte aligned; Hq * D and Hkv * D up to 2^28.  opts NULL: {D, 0, 1, 0, {D / 2}}.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int rotary_dim;  /* elements of a head that turn */
@@ -399,7 +399,7 @@ tsv_status tsv_rope_kv_append(const void *q, const void *k, const void *v, const
  * seq_err[b]: TSV_DERR_CAPACITY (L_b < 0 or > max_blocks * block_size), TSV_DERR_BLOCK (a
  * block id covering [0, L_b) outside [0, num_blocks)); rows of a flagged sequence are NaN.
  * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128];
- * max_blocks * block_size and B * Hq up to 2^30.
+ * max_blocks * block_size and B * Hq up to 2^30; Hq * D up to 2^28; scale > 0, scale * log2(e) finite.
  * ------------------------------------------------------------------------- */
 size_t tsv_decode_attn_workspace_size(int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
                                       tsv_dtype dtype);

@@ -42,6 +42,12 @@ tsv_status check_cache_shape(int Hkv, int D, int block_size, int num_blocks, tsv
     return TSV_OK;
 }
 
+// The kernels hold the offsets within a token's row in 32 bits (and three rows of the caches on).
+tsv_status check_row(int heads, int D) {
+    if ((long long)heads * D > (1LL << 28)) return report_error(TSV_ERR_UNSUPPORTED, "a row of %d heads of %d exceeds 2^28 elements", heads, D);
+    return TSV_OK;
+}
+
 tsv_status check_decode_shapes(int B, int Hq, int Hkv, int D, int block_size, int max_blocks, int num_blocks, tsv_dtype dtype) {
     if (B < 0 || Hq < 1 || max_blocks < 1) return report_error(TSV_ERR_ARG, "bad sizes B=%d Hq=%d max_blocks=%d", B, Hq, max_blocks);
     const tsv_status st = check_cache_shape(Hkv, D, block_size, num_blocks, dtype);
@@ -49,7 +55,7 @@ tsv_status check_decode_shapes(int B, int Hq, int Hkv, int D, int block_size, in
     if (Hq % Hkv) return report_error(TSV_ERR_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
     if ((long long)max_blocks * block_size > (1LL << 30)) return report_error(TSV_ERR_UNSUPPORTED, "a table row covers more than 2^30 slots");
     if ((long long)B * Hq > (1LL << 30)) return report_error(TSV_ERR_UNSUPPORTED, "B * Hq exceeds 2^30 query rows");
-    return TSV_OK;
+    return check_row(Hq, D);
 }
 }  // namespace
 
@@ -106,7 +112,8 @@ tsv_status tsv_rope_kv_append(const void* q, const void* k, const void* v, const
                               int64_t k_stride, int64_t v_stride, int64_t q_out_stride, int block_size, int num_blocks,
                               tsv_dtype dtype, const tsv_rope_options* opts, int32_t* tok_err, void* stream) {
     if (T < 0 || Hq < 1) return report_error(TSV_ERR_ARG, "bad sizes T=%d Hq=%d", T, Hq);
-    const tsv_status st = check_cache_shape(Hkv, D, block_size, num_blocks, dtype);
+    tsv_status st = check_cache_shape(Hkv, D, block_size, num_blocks, dtype);
+    if (st == TSV_OK) st = check_row(Hq > Hkv ? Hq : Hkv, D);
     if (st != TSV_OK) return st;
     if (T > (1 << 30)) return report_error(TSV_ERR_UNSUPPORTED, "T=%d exceeds 2^30", T);
     const tsv_rope_options o = opts ? *opts : tsv_rope_options{D, 0, 1, 0, {D / 2, 0, 0, 0}};
@@ -179,7 +186,8 @@ tsv_status tsv_decode_attn(const void* q, const void* k_cache, const void* v_cac
                            void* workspace, size_t workspace_bytes, int32_t* seq_err, void* stream) {
     const tsv_status st = check_decode_shapes(B, Hq, Hkv, D, block_size, max_blocks, num_blocks, dtype);
     if (st != TSV_OK) return st;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return report_error(TSV_ERR_ARG, "scale must be positive and finite");
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!(scale > 0.0f) || !std::isfinite(scale_log2)) return report_error(TSV_ERR_ARG, "scale must be positive, and finite times log2(e)");
     if (B == 0) return TSV_OK;
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !seq_err)
         return report_error(TSV_ERR_ARG, "null array argument");
@@ -217,7 +225,7 @@ tsv_status tsv_decode_attn(const void* q, const void* k_cache, const void* v_cac
     a.bs_log2 = log2i(block_size);
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     const cudaError_t e = tsv::launch_decode_attn(a, dtype == TSV_BF16, static_cast<cudaStream_t>(stream));
     return launch_status(e, "decode_attn");
 }

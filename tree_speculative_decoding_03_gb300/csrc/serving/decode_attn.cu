@@ -409,10 +409,12 @@ struct F32Core {
 // ------------------------------------------------------------------ the schedule
 
 // Keys of sequence b that are attended to: 0 when its length does not fit the block table.
-// (AHEAD: read before the wait for the kernel before, past the L1 cache.)
+// (AHEAD: read before the wait for the kernel before, past the L1 cache.)  Lengths and block ids are
+// read with ordinary loads, here and below: an earlier kernel may write them while this one is
+// already resident, which the read-only path does not allow.
 template <bool AHEAD = false>
 __device__ __forceinline__ int seq_keys(const DecodeArgs& a, int b) {
-    const int L = AHEAD ? __ldcg(a.seq_lens + b) : __ldg(a.seq_lens + b);
+    const int L = AHEAD ? __ldcg(a.seq_lens + b) : a.seq_lens[b];
     return (L < 0 || (long long)L > ((long long)a.max_blocks << a.bs_log2)) ? 0 : L;
 }
 
@@ -604,7 +606,7 @@ struct Stream {
 #pragma unroll
         for (int u = 0; u < RUNS; ++u) {
             const int key = f.t * KEYS + 8 * u;
-            ids[u] = key < f.keys ? (TSV_IN_BOUNDS(key >> a.bs_log2, a.max_blocks, nullptr) ? __ldg(bt + (key >> a.bs_log2)) : -1) : 0;
+            ids[u] = key < f.keys ? (TSV_IN_BOUNDS(key >> a.bs_log2, a.max_blocks, nullptr) ? bt[key >> a.bs_log2] : -1) : 0;
         }
     }
     // sends tile f on its way into stage `fill`, then fetches the next tile's ids
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const __grid_c
     // sequences without keys: nothing to attend to (zeros), or a length that does not fit (NaN)
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (seq_keys(a, b) > 0) continue;
-        const bool empty = __ldg(a.seq_lens + b) == 0;
+        const bool empty = a.seq_lens[b] == 0;
         const float x = empty ? 0.0f : __int_as_float(0x7fc00000);
         Elem* out = static_cast<Elem*>(a.out) + (long long)b * a.Hq * D;
         for (int i = tid; i < a.Hq * D; i += kThreads) out[i] = to_elem<Elem>(x);

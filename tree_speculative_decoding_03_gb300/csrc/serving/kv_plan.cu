@@ -95,12 +95,12 @@ __device__ __forceinline__ Three block_scan(Three v, Three* s_warp, Three* carry
 __device__ __forceinline__ int depth_of(const int32_t* par, int j) {
     int depth = 0, x = j;
     while (x > 0) {
-        const int p = __ldg(par + x);
+        const int p = par[x];
         if (p < 0 || p >= x) return -1;
         x = p;
         ++depth;
     }
-    return __ldg(par) == -1 ? depth : -1;
+    return par[0] == -1 ? depth : -1;
 }
 
 template <int THREADS, int CLUSTER, bool TOKENS>

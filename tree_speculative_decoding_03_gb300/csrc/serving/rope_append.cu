@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     long long slot = -1;
     uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
     if (live) {
-        slot = __ldg(a.slot_map + t);
+        slot = a.slot_map[t];  // an ordinary load, as of the positions: the kernel before this one may have written them
         u0 = *reinterpret_cast<const uint4*>(source(h0) + e0);
         u1 = *reinterpret_cast<const uint4*>(source(h0) + e1);
     }
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     float* s_sin = s_turn + tok * half;
     for (int i = tid, ts = t0 + tid / half, p = tid % half; i < tok * half; i += kRopeThreads) {
         float2 cs = make_float2(1.0f, 0.0f);
-        if (ts < a.T) cs = turn_of(__ldg(a.positions + (long long)a.axis[p] * a.T + ts), __ldg(a.inv_freq + p));
+        if (ts < a.T) cs = turn_of(a.positions[(long long)a.axis[p] * a.T + ts], __ldg(a.inv_freq + p));
         s_cos[i] = cs.x;
         s_sin[i] = cs.y;
         ts += kRopeThreads / half;

@@ -357,8 +357,8 @@ tsv_status tsv_kv_plan_slots(const int32_t *seq_lens, const int32_t *new_lens, c
  * theta = positions[axis(i), t] * inv_freq[i] (positions [axes, T], inv_freq
  * [rotary_dim / 2]):  (x, y) <- (x cos - y sin, y cos + x sin); the rest passes through.
  * The turned q goes to q_out[t] (q_out_stride; q_out may be q with the same stride), the
- * turned k and v to cache slot slot_map[t].  The angle is formed to about 2^-22 of a turn for
- * |position| < 2^24.  Arithmetic is fp32, rounded once to dtype.
+ * turned k and v to cache slot slot_map[t].  The angle is formed to about 2^-22 of a turn while
+ * |position| and |position * inv_freq| are below 2^24.  Arithmetic is fp32, rounded once to dtype.
  * slot_map[t] < 0 (padding): nothing is written to the cache and q_out[t] is zero.
  * slot_map[t] >= num_blocks * block_size: nothing is written to the cache, q_out[t] is NaN
  * and tok_err[t] = TSV_DERR_BLOCK (otherwise 0; one int32 per token, overwritten).

@@ -28,10 +28,10 @@ constexpr int kRopeThreads = 256;
 __device__ __forceinline__ float2 turn_of(int pos, float f) {
     constexpr float kInvTwoPiHi = 0.15915494f;
     constexpr float kInvTwoPiLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(0.15915494f));
-    const float fh = f * kInvTwoPiHi;
+    const float fh = __fmul_rn(f, kInvTwoPiHi);  // (rounded products by name: contracted ones would lose what fl and lo hold)
     const float fl = fmaf(f, kInvTwoPiHi, -fh) + f * kInvTwoPiLo;
     const float ph = static_cast<float>(pos);  // exact up to 2^24; past that the rest is added below
-    const float hi = ph * fh;
+    const float hi = __fmul_rn(ph, fh);
     float lo = fmaf(ph, fl, fmaf(ph, fh, -hi));
     if (pos > (1 << 24) || pos < -(1 << 24))
         lo = fmaf(static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph)), fh, lo);

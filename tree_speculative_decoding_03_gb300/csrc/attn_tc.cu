@@ -1018,7 +1018,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merge of the units that straddle lanes (log-sum-exp over their pieces).  One CTA per
 // (unit, block of 32 rows); 8 threads per row, each owning D / 8 consecutive columns,
 // so a row's 8 threads read its partial rows as one coalesced run.  Runs after the
-// attention kernel (programmatic dependent launch: it waits for that kernel's writes).
+// attention kernel (programmatic dependent launch: it waits for that kernel's writes, and reads them
+// with ordinary loads: the read-only path is for data that nobody writes while the kernel is resident).
 template <int D>
 __global__ void __launch_bounds__(256) attn_tc_merge_kernel(const AttnArgs a) {
     constexpr int C = D / 8;  // columns per thread
@@ -1068,11 +1069,11 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(const AttnArgs a) {
                 TSV_IN_BOUNDS(((long long)((c_first + k) * nrg + rg) * 2 + (k == 0 ? sd0 : 0)) * a.rows_item + rr,
                               2LL * a.lanes * nrg * a.rows_item, a.seq_err + b)) {
                 const long long pr = ((long long)((c_first + k) * nrg + rg) * 2 + (k == 0 ? sd0 : 0)) * a.rows_item + rr;
-                lk[k] = __ldg(a.part_l + pr);
-                mk[k] = __ldg(a.part_m + pr);
+                lk[k] = a.part_l[pr];
+                mk[k] = a.part_m[pr];
                 const float4* src = reinterpret_cast<const float4*>(a.part_o + pr * D + c0);
 #pragma unroll
-                for (int q = 0; q < C / 4; ++q) o[k][q] = __ldg(src + q);
+                for (int q = 0; q < C / 4; ++q) o[k][q] = src[q];
             }
         }
 #pragma unroll
@@ -1096,7 +1097,7 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(const AttnArgs a) {
         for (int k = c_first; k <= c_last; ++k) {
             if (!dense && lane_start(k + 1, T_all, a.lanes) == lane_start(k, T_all, a.lanes)) continue;
             const long long pr = ((long long)(k * nrg + rg) * 2 + (k == c_first ? sd0 : 0)) * a.rows_item + rr;
-            const float lk = __ldg(a.part_l + pr), mk = __ldg(a.part_m + pr);
+            const float lk = a.part_l[pr], mk = a.part_m[pr];
             if (!(lk > 0.0f)) continue;
             if (mk > M) {
                 W = W * exp2f(M - mk) + lk;
@@ -1108,13 +1109,13 @@ __global__ void __launch_bounds__(256) attn_tc_merge_kernel(const AttnArgs a) {
         for (int k = c_first; k <= c_last; ++k) {
             if (!dense && lane_start(k + 1, T_all, a.lanes) == lane_start(k, T_all, a.lanes)) continue;
             const long long pr = ((long long)(k * nrg + rg) * 2 + (k == c_first ? sd0 : 0)) * a.rows_item + rr;
-            const float lk = __ldg(a.part_l + pr);
+            const float lk = a.part_l[pr];
             if (!(lk > 0.0f)) continue;
-            const float wk = lk * exp2f(__ldg(a.part_m + pr) - M);
+            const float wk = lk * exp2f(a.part_m[pr] - M);
             const float4* src = reinterpret_cast<const float4*>(a.part_o + pr * D + c0);
 #pragma unroll
             for (int q = 0; q < C / 4; ++q) {
-                const float4 o = __ldg(src + q);
+                const float4 o = src[q];
                 acc[4 * q] = fmaf(wk, o.x, acc[4 * q]);
                 acc[4 * q + 1] = fmaf(wk, o.y, acc[4 * q + 1]);
                 acc[4 * q + 2] = fmaf(wk, o.z, acc[4 * q + 2]);

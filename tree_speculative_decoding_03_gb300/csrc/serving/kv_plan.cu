@@ -339,30 +339,88 @@ __global__ void __launch_bounds__(kFillThreads) kv_plan_fill_kernel(const __grid
     }
 }
 
+constexpr size_t plan_smem(int B) { return (size_t)B * (5 * sizeof(int) + 1) + 16; }
+
+// The kernel's limits, raised once per device and host thread.
 template <int THREADS, int CLUSTER, bool TOKENS>
-cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream) {
-    const size_t smem = (size_t)a.B * (5 * sizeof(int) + 1) + 16;
-    // the kernel's limits, raised once per device and host thread
+cudaError_t raise_limits(int dev) {
     thread_local int set_dev = -1;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    if (dev == set_dev) return cudaSuccess;
+    const auto kernel = kv_plan_kernel<THREADS, CLUSTER, TOKENS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan_smem(kPlanMaxSeqs)));
+    if (e == cudaSuccess && CLUSTER > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) set_dev = dev;
+    return e;
+}
+
+#ifdef TSV_TEST_HOOKS
+int g_test_plan_cluster = kPlanCluster;  // test build: the largest cluster that counts as resident
+#endif
+
+// Whether a cluster of this size, with the largest batch's shared memory, can be resident.
+template <int CLUSTER>
+bool cluster_fits(int dev) {
+#ifdef TSV_TEST_HOOKS
+    if (CLUSTER > g_test_plan_cluster) return false;
+#endif
+    if (raise_limits<1024, CLUSTER, true>(dev) != cudaSuccess) return false;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CLUSTER;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(CLUSTER);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = plan_smem(kPlanMaxSeqs);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kv_plan_kernel<1024, CLUSTER, true>, &cfg) == cudaSuccess && n > 0;
+}
+
+template <int THREADS, int CLUSTER, bool TOKENS>
+cudaError_t launch_plan(const PlanArgs& a, int dev, cudaStream_t stream) {
+    const size_t smem = plan_smem(a.B);
+    const cudaError_t e = raise_limits<THREADS, CLUSTER, TOKENS>(dev);
     if (e != cudaSuccess) return e;
-    if (dev != set_dev) {
-        const auto kernel = kv_plan_kernel<THREADS, CLUSTER, TOKENS>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxSeqs * (5 * (int)sizeof(int) + 1) + 16);
-        if (e == cudaSuccess && CLUSTER > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        set_dev = dev;
-    }
     return launch_pdl(kv_plan_kernel<THREADS, CLUSTER, TOKENS>, dim3(CLUSTER), dim3(THREADS), smem, stream, CLUSTER, a);
+}
+
+// The cluster's size: a cluster of 16 needs as many SMs of one GPC, which a partitioned GPU may not
+// have; then 8, or one CTA.  Looked up once per device and host thread.
+template <bool TOKENS>
+cudaError_t launch_clustered(const PlanArgs& a, int dev, cudaStream_t stream) {
+    thread_local int of_dev = -1, size = 0;
+#ifdef TSV_TEST_HOOKS
+    of_dev = -1;
+#endif
+    if (dev != of_dev) {
+        size = cluster_fits<kPlanCluster>(dev) ? kPlanCluster : cluster_fits<8>(dev) ? 8 : 1;
+        of_dev = dev;
+    }
+    if (size == kPlanCluster) return launch_plan<1024, kPlanCluster, TOKENS>(a, dev, stream);
+    return size == 8 ? launch_plan<1024, 8, TOKENS>(a, dev, stream) : launch_plan<1024, 1, TOKENS>(a, dev, stream);
 }
 
 }  // namespace
 
+#ifdef TSV_TEST_HOOKS
+// test build only: clusters of more CTAs count as not resident
+extern "C" int tsv_test_set_plan_cluster(int most) {
+    const int before = g_test_plan_cluster;
+    g_test_plan_cluster = most;
+    return before;
+}
+#endif
+
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
-    if (a.B <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens) return launch_plan<512, 1, true>(a, stream);
-    if (a.max_tokens <= kPlanClusterTokens) return launch_plan<1024, kPlanCluster, true>(a, stream);
-    const cudaError_t e = launch_plan<1024, kPlanCluster, false>(a, stream);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (a.B <= kPlanSmallSeqs && a.max_tokens <= kPlanSmallTokens) return launch_plan<512, 1, true>(a, dev, stream);
+    if (a.max_tokens <= kPlanClusterTokens) return launch_clustered<true>(a, dev, stream);
+    e = launch_clustered<false>(a, dev, stream);
     if (e != cudaSuccess) return e;
     constexpr int kTok = kFillThreads * kFillTokens;
     return launch_pdl(kv_plan_fill_kernel, dim3(static_cast<unsigned>((a.max_tokens + kTok - 1) / kTok)), dim3(kFillThreads), 0,

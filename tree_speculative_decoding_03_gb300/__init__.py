@@ -275,10 +275,13 @@ def _marshal():
 
         import torch  # noqa: F401  (the module resolves against its libraries)
 
-        from .builder import MARSHAL
-        if not os.path.exists(MARSHAL):
-            raise RuntimeError(f"_marshal.so not built at {MARSHAL}; run build() first")
-        loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL)
+        from .builder import marshal_missing, marshal_path
+        path = marshal_path()
+        if not os.path.exists(path):
+            missing = marshal_missing()
+            raise RuntimeError(f"the serving operators' binding is not built at {path}; " +
+                               (f"building it needs {missing}" if missing else "run build() first"))
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
         _marshal_module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
         loader.exec_module(_marshal_module)
     return _marshal_module

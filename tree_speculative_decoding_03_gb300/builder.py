@@ -4,22 +4,25 @@ Each translation unit compiles in parallel into `_build/`, then the objects are
 linked into `_build/libtsv.so` (static CUDA runtime, so the library needs no
 runtime search path).  Rebuilds only when a source or header is newer than the
 library.  The serving operators' argument marshalling (`binding/marshal.cpp`, against torch's
-headers) is compiled beside it with the host compiler into `_build/_marshal.so`.
+headers) is compiled beside it with the host compiler into `_build/`, under a name that holds the
+Python ABI and the torch version it belongs to; without torch's or Python's headers it is left out.
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
+import warnings
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libtsv.so")
 MARSHAL_SRC = os.path.join(HERE, "binding", "marshal.cpp")
-MARSHAL = os.path.join(OUT_DIR, "_marshal.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -87,26 +90,61 @@ def build_library(verbose: bool = False, extra_flags=(), variant=None) -> str:
     return lib
 
 
-def build_marshal() -> str:
-    """Compiles the argument marshalling of the serving operators (host code)."""
-    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
-        return MARSHAL
+def marshal_path() -> str:
+    """Where the argument marshalling of this Python and this torch lies: one built against
+    another torch is never loaded, however new the file."""
     import sysconfig
+
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}"
+    return os.path.join(OUT_DIR, "_marshal." + re.sub(r"[^A-Za-z0-9_.-]", "_", tag) + ".so")
+
+
+def _marshal_includes() -> list:
+    import sysconfig
+
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
+    return [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+
+
+def marshal_missing() -> Optional[str]:
+    """What the argument marshalling needs and does not find (None: nothing)."""
+    try:
+        dirs = _marshal_includes()
+    except ImportError:
+        return "torch"
+    for name in ("Python.h", "torch/csrc/autograd/python_variable.h", "c10/cuda/CUDAStream.h", "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, name)) for d in dirs):
+            return name
+    return None
+
+
+def build_marshal() -> Optional[str]:
+    """Compiles the argument marshalling of the serving operators (host code).  Where torch or a
+    header is missing the rest of the package stands without it: a warning, and those operators
+    raise when they are called."""
+    missing = marshal_missing()
+    if missing is not None:
+        warnings.warn(f"{missing} not found: the serving operators' binding is not built", RuntimeWarning)
+        return None
+    import torch
+    out = marshal_path()
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     os.makedirs(OUT_DIR, exist_ok=True)
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-isystem{d}" for d in inc),
-           MARSHAL_SRC, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           *(f"-isystem{d}" for d in [*_marshal_includes(), INCLUDE]), MARSHAL_SRC, "-o", tmp,
+           f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling {os.path.basename(MARSHAL_SRC)} failed:\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":

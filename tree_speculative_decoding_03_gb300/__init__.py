@@ -42,7 +42,8 @@ def lib_path(variant=None) -> str:
 
 def build(verbose: bool = False, variant=None) -> str:
     """Builds the library: the product build, or a test build ("checked": device-side
-    index checks; "hooks": short bounded waits and a stall switch)."""
+    index checks; "hooks": short bounded waits, a stall switch and a limit on the
+    slot plan's cluster)."""
     from concurrent.futures import ThreadPoolExecutor
 
     from .builder import build_library, build_marshal
@@ -339,7 +340,8 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, out, scale: float, w
                 lse=None, stream=None):
     """Attention of one new token per sequence over the paged cache (see include/tsv.h).
     q/out [B,Hq,D]; caches [num_blocks,bs,Hkv,D]; seq_lens [B]: keys, the new token's
-    included; lse [B,Hq] float32, if given, takes the log-sum-exp of the scaled scores."""
+    included; seq_err [B] int32 and a workspace of decode_attn_workspace_size(...) bytes are needed
+    (None is refused); lse [B,Hq] float32, if given, takes the log-sum-exp of the scaled scores."""
     _check(_marshal().decode_attn(
         load().addresses["tsv_decode_attn"], q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, seq_err, lse,
         _raw_stream(stream, q)))

@@ -43,7 +43,7 @@ def _deps():
 
 
 # Test builds of the same sources: "checked" adds device-side index checks
-# (-DTSV_CHECKED), "hooks" shortens the bounded waits and adds a stall switch
+# (-DTSV_CHECKED), "hooks" shortens the bounded waits and adds a stall switch and a limit on the plan's cluster
 # (-DTSV_TEST_HOOKS).  Each is built into its own folder; the product library is the
 # default (no variant).
 VARIANT_FLAGS = {"checked": ["-DTSV_CHECKED"], "hooks": ["-DTSV_TEST_HOOKS"]}

@@ -5,7 +5,7 @@
 //   lse = m + ln l.
 // Each K/V row is read once; the Hq / Hkv query rows of a kv head share it (about that many
 // multiply-adds per element), so the call is bound by the cache's bytes: 64 sequences of 64/8 heads,
-// 1.06 M keys, 4.36 GB in 620 us (7.0 TB/s, 1.04 of the measured copy rate); 13 fp32 sequences, 480 MB in
+// 1.06 M keys, 4.36 GB in 622 us (7.0 TB/s, 1.03 of the measured copy rate); 13 fp32 sequences, 480 MB in
 // 78 us (6.1 TB/s).  Calls of tens of MB spend as long on launch, schedule, first loads and the
 // join: 8 sequences of 2048 keys, 67 MB, 20 us.
 //
@@ -103,7 +103,7 @@ __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0
 // A warp's part of a tile, and the running state of its query rows.
 
 // bf16: products on the tensor cores, 16 rows a fragment (MT fragments).  With at most 16 rows
-// per K/V row the tensor rate is far from a limit (about 190 multiply-adds a clock and SM at
+// per K/V row the tensor rate is far from a limit (about 280 multiply-adds a clock and SM at
 // full memory speed), so the warp-level product serves.  The second product takes each weight as
 // two bf16 parts, hi + lo, so a weight is off by at most 2^-15 of itself and the result by little
 // but its own rounding.  (One part alone is off by up to 2^-8, an error as large as the result's

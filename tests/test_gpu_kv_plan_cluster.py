@@ -31,3 +31,32 @@ def test_smaller_clusters(hooks_lib, most, B, bs, max_len, max_new, kw, past):
     if past:
         c["max_tokens"] = max(c["max_tokens"], edges.CLUSTER_TOKENS + past)
     edges.run_both(c)
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np, torch
+import serving_util as U, test_gpu_kv_plan as plan
+for B, pad in ((300, 0), (300, 70000), (8, 0)):
+    c = U.plan_case(np.random.default_rng(B + pad), B, 16, 200, 9, ended=0.2, pad=pad)
+    d = plan.device_plan(c)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.call(d)
+    g.replay()
+    plan.check(c, d)
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    # the look-up of the cluster's size and the kernels' limits happen inside the capture
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(here), tests=here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

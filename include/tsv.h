@@ -71,7 +71,9 @@ enum {
                                 sequence are not valid (never expected; reported, not trapped) */
     TSV_DERR_INTERNAL = 64,  /* checked builds only (-DTSV_CHECKED, a test build): a device-side
                                 index check failed and the access was skipped -- a library bug */
-    TSV_DERR_POOL = 128      /* the pool of free blocks is too small, or its count is wrong */
+    TSV_DERR_POOL = 128,     /* the pool of free blocks is too small, or its count is wrong */
+    TSV_DERR_SEQ = 256       /* a sequence index is outside the batch, named twice or not empty; groups
+                                that do not cover the batch in order */
 };
 
 /* Message for the calling thread's most recent failed call ("" if none). */
@@ -409,6 +411,142 @@ tsv_status tsv_decode_attn(const void *q, const void *k_cache, const void *v_cac
                            int B, int Hq, int Hkv, int D, int block_size, int max_blocks,
                            int num_blocks, float scale, tsv_dtype dtype, void *workspace,
                            size_t workspace_bytes, int32_t *seq_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Several continuations of one prompt (samples, beams) on the same paged cache: sequences forked on
+ * shared blocks, attention that reads a shared prefix once, log probabilities to rank them by.
+ *   tsv_kv_fork_seqs -> tsv_kv_copy_blocks (each layer) -> steps with tsv_prefix_decode_attn
+ *   -> tsv_token_logprobs -> tsv_kv_release_seqs, tsv_kv_fork_seqs, ...
+ *
+ * shares [num_blocks] holds, for each block, the table entries that refer to it beyond the first: 0 for
+ * a block of one sequence and for a free one, never negative.  It starts as zeros, and
+ * tsv_kv_plan_slots, which takes and gives back blocks of one sequence, needs nothing of it.  Blocks that may be
+ * shared go back with tsv_kv_release_seqs, before the plan sees the shorter length (blocks_held is then what is
+ * left).  Only full blocks are shared, so a sequence never writes into a shared block unless it is cut back
+ * into one; a sequence to be cut back there is forked and released instead.
+ *
+ * In these calls an output array may be its input array (seq_lens_out, blocks_held_out, shares_out,
+ * free_count_out, block_table_out); with separate outputs, and no change in between, a repeated call gives
+ * the same result.  Nothing else may overlap.  B <= 8192; block_size a power of two in [8, 128];
+ * max_blocks * block_size and num_blocks up to 2^30.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * Forks: sequence fork_dst[i], which holds no blocks, becomes a copy of fork_src[i] (batch rows;
+ * fork_src[i] < 0: padding).  With L = seq_lens[src]:
+ *   entries 0 .. L / bs - 1 of the source's table row go into the destination's, and each such block's
+ *   shares grow by one;
+ *   if L % bs > 0, a block is taken from the top of the stack free_blocks[0 .. free_count), in
+ *   order of i, into entry L / bs, and (copy_src, copy_dst, copy_rows)[i] = (the source's block, the
+ *   new one, L % bs); otherwise (-1, -1, 0).  tsv_kv_copy_blocks does the copy, in each layer's cache;
+ *   seq_lens_out[dst] = L, blocks_held_out[dst] = ceil(L / bs).  Other rows' entries are copied.
+ * Surplus blocks of the source are not shared.  A source may be forked many times.
+ * fork_err[i], overwritten: TSV_DERR_SEQ (an index outside the batch, a destination named twice or holding blocks),
+ * TSV_DERR_CAPACITY (the source's length negative or past its blocks, its blocks_held outside [0, max_blocks]),
+ * TSV_DERR_POOL (too few free blocks: no later fork that needs one gets one then; *free_count outside
+ * [0, num_blocks]): the fork is not done.  TSV_DERR_BLOCK (a block id outside [0, num_blocks)): the
+ * entry is copied as it is, and nothing is counted or copied for it.
+ * F <= 8192 forks.
+ * ------------------------------------------------------------------------- */
+tsv_status tsv_kv_fork_seqs(const int32_t *fork_src, const int32_t *fork_dst, const int32_t *seq_lens,
+                            int32_t *seq_lens_out, int32_t *block_table, const int32_t *blocks_held,
+                            int32_t *blocks_held_out, const int32_t *shares, int32_t *shares_out,
+                            const int32_t *free_blocks, const int32_t *free_count, int32_t *free_count_out,
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_rows, int F, int B,
+                            int block_size, int max_blocks, int num_blocks, int32_t *fork_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Blocks given back by reference: sequence b keeps the blocks of its first keep_lens[b] tokens (0: it has
+ * ended; its length or more: only surplus blocks go).  Each entry ceil(keep / bs) .. blocks_held[b] - 1 takes
+ * one from its block's shares; a block with no reference left goes onto the stack free_blocks, in
+ * ascending order of ids after all entries of the batch are counted.  blocks_held_out[b] = entries kept; the
+ * table keeps its values.
+ * seq_err[b], overwritten: TSV_DERR_CAPACITY (keep_lens[b] < 0, blocks_held[b] outside [0, max_blocks]) and
+ * TSV_DERR_POOL for *free_count outside [0, num_blocks]: nothing is given back.  TSV_DERR_BLOCK (a block id
+ * outside [0, num_blocks)): that entry is dropped.  TSV_DERR_POOL also where more references of a block
+ * come back than there were, or more blocks than the pool has places for (the rest is lost): the others are served.
+ * ------------------------------------------------------------------------- */
+tsv_status tsv_kv_release_seqs(const int32_t *keep_lens, const int32_t *block_table, const int32_t *blocks_held,
+                               int32_t *blocks_held_out, const int32_t *shares, int32_t *shares_out,
+                               int32_t *free_blocks, const int32_t *free_count, int32_t *free_count_out, int B,
+                               int block_size, int max_blocks, int num_blocks, int32_t *seq_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The blocks in use put together at the low end of the cache.  The n distinct blocks of the held
+ * table entries are live -- so every block in use must be in this table --; the k-th live block with an id of
+ * n or more moves to the k-th free id below n: copy_src[k] -> copy_dst[k] for k < *copy_count, and -1 from there
+ * to num_blocks / 2, the places of both lists.  block_table_out and shares_out follow the moves (shares_out is 0
+ * for free blocks); free_blocks[0 .. num_blocks - n) = num_blocks - 1 .. n, *free_count_out = num_blocks - n, so the
+ * lowest free id is taken first.  tsv_kv_copy_blocks(..., copy_count) moves the rows, in each layer's cache; no
+ * block is both source and destination.
+ * seq_err[b], overwritten: TSV_DERR_CAPACITY (blocks_held[b] outside [0, max_blocks]: the row is copied as it is and
+ * its blocks do not count as live), TSV_DERR_BLOCK (a block id outside [0, num_blocks): the entry stays).
+ * `workspace` holds tsv_kv_compact_workspace_size(num_blocks) bytes, 4-byte aligned.  max_blocks up to 2^27.
+ * ------------------------------------------------------------------------- */
+size_t tsv_kv_compact_workspace_size(int num_blocks);
+
+tsv_status tsv_kv_compact_blocks(const int32_t *block_table, int32_t *block_table_out, const int32_t *blocks_held,
+                                 const int32_t *shares, int32_t *shares_out, int32_t *free_blocks,
+                                 int32_t *free_count_out, int32_t *copy_src, int32_t *copy_dst,
+                                 int32_t *copy_count, int B, int max_blocks, int num_blocks, void *workspace,
+                                 size_t workspace_bytes, int32_t *seq_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Block contents copied within a cache: the first copy_rows[i] slots (NULL: all; held to [0, block_size]) of
+ * block copy_src[i] of k_cache and v_cache go to block copy_dst[i], for i < n, or i < *copy_count if that
+ * is not NULL (held to [0, n]).  copy_src[i] < 0: nothing.  Destinations must differ, and no
+ * destination may be a source of another copy.  copy_err[i], overwritten: TSV_DERR_BLOCK for a source
+ * >= num_blocks or a destination outside [0, num_blocks) (nothing is copied).  D in {64, 128}; caches
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+tsv_status tsv_kv_copy_blocks(void *k_cache, void *v_cache, const int32_t *copy_src, const int32_t *copy_dst,
+                              const int32_t *copy_rows, const int32_t *copy_count, int n, int Hkv, int D,
+                              int block_size, int num_blocks, tsv_dtype dtype, int32_t *copy_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token per sequence where groups of sequences share the first keys.
+ *
+ * Group g is the sequences group_offsets[g] .. group_offsets[g+1] - 1 (group_offsets[0] = 0, ascending,
+ * group_offsets[G] = B; a group may be empty).  Its sequences attend to the same first P_g = prefix_lens[g]
+ * keys, 0 <= P_g <= seq_lens[b], which are read from the table row of the group's first sequence, once for all
+ * of them; keys P_g .. L_b - 1 come from each sequence's own row.  P_g need not be a multiple of the block size.
+ * out and lse are those of tsv_decode_attn for tables with these keys, with the same precision: fp32 sums and weights (a bf16 call's
+ * weights within 2^-15 of themselves), out rounded once.  A repeated call gives the same bits.
+ * L_b = 0: out is zero and lse -infinity.  Slots outside a sequence's keys are never read into the result.
+ * `workspace` as in tsv_tree_verify_attn, with tsv_prefix_decode_attn_workspace_size(...) bytes, 16-byte aligned; calls
+ * that may overlap on the GPU need one each.  out and lse must not overlap the inputs.
+ * seq_err[b]: TSV_DERR_SEQ (all sequences: the offsets are not as above), TSV_DERR_CAPACITY (L_b < 0 or
+ * > max_blocks * block_size, P_g < 0 or > L_b), TSV_DERR_BLOCK (a block id that covers one of the sequence's keys,
+ * the shared ones included, outside [0, num_blocks)); rows of a flagged sequence are NaN.
+ * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128]; B and G up to 8192;
+ * max_blocks * block_size up to 2^30, B * Hq up to 2^24; scale > 0, scale * log2(e) finite.
+ * ------------------------------------------------------------------------- */
+size_t tsv_prefix_decode_attn_workspace_size(int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks,
+                                             tsv_dtype dtype);
+
+tsv_status tsv_prefix_decode_attn(const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_table, const int32_t *seq_lens,
+                                  const int32_t *group_offsets, const int32_t *prefix_lens, void *out, float *lse,
+                                  int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks,
+                                  int num_blocks, float scale, tsv_dtype dtype, void *workspace,
+                                  size_t workspace_bytes, int32_t *seq_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, with entropy and top alternatives.
+ *
+ * Row t of logits (row_stride elements after the one before, its V elements contiguous) gives
+ * p = softmax(logits[t] / temperature):  logprobs[t] = ln p(tokens[t]);  entropy[t] = -sum p ln p (entropy may be
+ * NULL);  top_ids, top_logprobs [T, top]: the `top` entries of largest logit, ties to the lower index, and
+ * their ln p (both may be NULL if top = 0).  A logit of -infinity is an entry of probability 0.  Sums are fp32.
+ * tokens[t] < 0 (padding): the row is not read; logprobs, entropy and top_logprobs are 0, top_ids -1.
+ * tok_err[t], overwritten: TSV_DERR_TOKEN (tokens[t] >= V), TSV_DERR_NONFINITE (a NaN or +infinity, or no finite logit):
+ * the row's floats are NaN and its ids -1.
+ * logits fp32 or bf16, aligned to their elements; 0 <= top <= min(32, V); T up to 2^27, V up to 2^30;
+ * temperature > 0, it and its inverse finite.
+ * ------------------------------------------------------------------------- */
+tsv_status tsv_token_logprobs(const void *logits, int64_t row_stride, const int32_t *tokens, int T, int V,
+                              float temperature, int top, tsv_dtype logits_dtype, float *logprobs,
+                              float *entropy, int32_t *top_ids, float *top_logprobs, int32_t *tok_err, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Tree construction (host side).  Sequoia summary, sections "Scalable Speculative

@@ -1,7 +1,8 @@
 """Python binding of libtsv: the GB300 target-side verification step of tree-based
 speculative decoding (tree-masked paged attention, rejection-sampling tree walk,
 KV-cache compaction of the accepted path) and the operators around it on the same paged
-cache (slot plan, rotary K/V append, single-token attention).
+cache (slot plan, rotary K/V append, single-token attention; for several continuations of one
+prompt blocks by reference, attention over shared prefixes, token log probabilities).
 
 Argument marshalling only: every step runs in the library's CUDA kernels.  Torch
 tensors supply device memory and the current CUDA stream.  There is no CPU
@@ -23,6 +24,7 @@ TSV_BF16, TSV_F32 = 0, 1
 TSV_DERR_PARENT, TSV_DERR_BLOCK, TSV_DERR_CAPACITY, TSV_DERR_TOKEN, TSV_DERR_NONFINITE, TSV_DERR_TIMEOUT = 1, 2, 4, 8, 16, 32
 TSV_DERR_INTERNAL = 64  # checked test build only
 TSV_DERR_POOL = 128
+TSV_DERR_SEQ = 256
 DERR_PARENT, DERR_BLOCK, DERR_CAPACITY, DERR_TOKEN, DERR_NONFINITE = 1, 2, 4, 8, 16
 
 _libs = {}           # loaded libraries by build variant (None = the product build)
@@ -104,6 +106,22 @@ def load(variant=None):
     lib.tsv_decode_attn_workspace_size.argtypes = [i32] * 7
     lib.tsv_decode_attn.restype = i32
     lib.tsv_decode_attn.argtypes = [P] * 7 + [i32] * 7 + [f32, i32, P, sz, P, P]
+    lib.tsv_kv_fork_seqs.restype = i32
+    lib.tsv_kv_fork_seqs.argtypes = [P] * 15 + [i32] * 5 + [P, P]
+    lib.tsv_kv_release_seqs.restype = i32
+    lib.tsv_kv_release_seqs.argtypes = [P] * 9 + [i32] * 4 + [P, P]
+    lib.tsv_kv_compact_workspace_size.restype = sz
+    lib.tsv_kv_compact_workspace_size.argtypes = [i32]
+    lib.tsv_kv_compact_blocks.restype = i32
+    lib.tsv_kv_compact_blocks.argtypes = [P] * 10 + [i32] * 3 + [P, sz, P, P]
+    lib.tsv_kv_copy_blocks.restype = i32
+    lib.tsv_kv_copy_blocks.argtypes = [P] * 6 + [i32] * 6 + [P, P]
+    lib.tsv_prefix_decode_attn_workspace_size.restype = sz
+    lib.tsv_prefix_decode_attn_workspace_size.argtypes = [i32] * 8
+    lib.tsv_prefix_decode_attn.restype = i32
+    lib.tsv_prefix_decode_attn.argtypes = [P] * 9 + [i32] * 8 + [f32, i32, P, sz, P, P]
+    lib.tsv_token_logprobs.restype = i32
+    lib.tsv_token_logprobs.argtypes = [P, i64, P, i32, i32, f32, i32, i32] + [P] * 6
     f64 = ctypes.c_double
     lib.tsv_sequoia_values.restype = i32
     lib.tsv_sequoia_values.argtypes = [P, i32, i32, i32, P]
@@ -118,7 +136,8 @@ def load(variant=None):
         lib.tsv_test_set_stall.argtypes = [i32]
     # entry points that the compiled marshalling calls
     lib.addresses = {n: ctypes.cast(getattr(lib, n), P).value
-                     for n in ("tsv_kv_plan_slots", "tsv_rope_kv_append", "tsv_decode_attn")}
+                     for n in ("tsv_kv_plan_slots", "tsv_rope_kv_append", "tsv_decode_attn", "tsv_kv_fork_seqs", "tsv_kv_release_seqs",
+                               "tsv_kv_compact_blocks", "tsv_kv_copy_blocks", "tsv_prefix_decode_attn", "tsv_token_logprobs")}
     _libs[v] = lib
     return lib
 
@@ -345,6 +364,77 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_lens, out, scale: float, w
     _check(_marshal().decode_attn(
         load().addresses["tsv_decode_attn"], q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, seq_err, lse,
         _raw_stream(stream, q)))
+
+
+# ----------------------------------------------------------------------------- several continuations of one prompt
+
+def kv_fork_seqs(fork_src, fork_dst, seq_lens, seq_lens_out, block_table, blocks_held, blocks_held_out, shares, shares_out, free_blocks,
+                 free_count, free_count_out, copy_src, copy_dst, copy_rows, block_size: int, fork_err, stream=None):
+    """Makes sequence fork_dst[i] a copy of fork_src[i] on shared blocks (see include/tsv.h).  fork_src,
+    fork_dst, copy_src, copy_dst, copy_rows, fork_err [F]; seq_lens, blocks_held and their outputs [B];
+    block_table [B,max_blocks]; shares, shares_out, free_blocks [num_blocks]; free_count, free_count_out [1]; all int32.
+    The copy lists, a partly filled last block each, are for kv_copy_blocks.  Outputs may be their inputs."""
+    _check(_marshal().kv_fork_seqs(
+        load().addresses["tsv_kv_fork_seqs"], fork_src, fork_dst, seq_lens, seq_lens_out, block_table, blocks_held, blocks_held_out,
+        shares, shares_out, free_blocks, free_count, free_count_out, copy_src, copy_dst, copy_rows, block_size, fork_err,
+        _raw_stream(stream, block_table)))
+
+
+def kv_release_seqs(keep_lens, block_table, blocks_held, blocks_held_out, shares, shares_out, free_blocks, free_count, free_count_out,
+                    block_size: int, seq_err, stream=None):
+    """Gives back the blocks past the first keep_lens[b] tokens, those without a reference left to the pool
+    (see include/tsv.h).  keep_lens, blocks_held, blocks_held_out, seq_err [B]; the others as in kv_fork_seqs."""
+    _check(_marshal().kv_release_seqs(
+        load().addresses["tsv_kv_release_seqs"], keep_lens, block_table, blocks_held, blocks_held_out, shares, shares_out, free_blocks,
+        free_count, free_count_out, block_size, seq_err, _raw_stream(stream, block_table)))
+
+
+def kv_compact_workspace_size(num_blocks) -> int:
+    return int(load().tsv_kv_compact_workspace_size(num_blocks))
+
+
+def kv_compact_blocks(block_table, block_table_out, blocks_held, shares, shares_out, free_blocks, free_count_out, copy_src, copy_dst,
+                      copy_count, seq_err, workspace, stream=None):
+    """Moves the blocks in use to the low end of the cache: tables, shares, the pool, and the copies for
+    kv_copy_blocks (see include/tsv.h).  block_table, block_table_out [B,max_blocks]; shares, shares_out, free_blocks
+    [num_blocks]; free_count_out, copy_count [1]; copy_src, copy_dst [num_blocks // 2]; all int32; a workspace of
+    kv_compact_workspace_size(num_blocks) bytes."""
+    _check(_marshal().kv_compact_blocks(
+        load().addresses["tsv_kv_compact_blocks"], block_table, block_table_out, blocks_held, shares, shares_out, free_blocks,
+        free_count_out, copy_src, copy_dst, copy_count, seq_err, workspace, _raw_stream(stream, block_table)))
+
+
+def kv_copy_blocks(k_cache, v_cache, copy_src, copy_dst, copy_err, copy_rows=None, copy_count=None, stream=None):
+    """Copies the first copy_rows[i] slots (None: all) of block copy_src[i] to block copy_dst[i] in both caches
+    [num_blocks,bs,Hkv,D] (see include/tsv.h).  copy_src, copy_dst, copy_rows, copy_err [n] int32; copy_count [1]
+    int32: how many of them count (None: all)."""
+    _check(_marshal().kv_copy_blocks(
+        load().addresses["tsv_kv_copy_blocks"], k_cache, v_cache, copy_src, copy_dst, copy_rows, copy_count, copy_err,
+        _raw_stream(stream, k_cache)))
+
+
+def prefix_decode_attn_workspace_size(B, G, Hq, Hkv, D, block_size, max_blocks, dtype_code) -> int:
+    return int(load().tsv_prefix_decode_attn_workspace_size(B, G, Hq, Hkv, D, block_size, max_blocks, dtype_code))
+
+
+def prefix_decode_attn(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out, scale: float, workspace=None,
+                       seq_err=None, lse=None, stream=None):
+    """Attention of one new token per sequence where groups of neighbouring sequences share their first keys,
+    which are read once for the group (see include/tsv.h).  group_offsets [G+1], prefix_lens [G] int32; the others as in
+    decode_attn; seq_err and a workspace of prefix_decode_attn_workspace_size(...) bytes are needed."""
+    _check(_marshal().prefix_decode_attn(
+        load().addresses["tsv_prefix_decode_attn"], q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out, scale,
+        workspace, seq_err, lse, _raw_stream(stream, q)))
+
+
+def token_logprobs(logits, tokens, logprobs, tok_err, temperature: float = 1.0, entropy=None, top_ids=None, top_logprobs=None,
+                   stream=None):
+    """Log probabilities of tokens [T] int32 under softmax(logits / temperature), logits [T,V] float32 or bfloat16
+    with contiguous rows (see include/tsv.h).  logprobs [T] float32, tok_err [T] int32; entropy [T] float32, and
+    top_ids [T,n] int32 with top_logprobs [T,n] float32 (n <= 32, the largest first), if given."""
+    _check(_marshal().token_logprobs(
+        load().addresses["tsv_token_logprobs"], logits, tokens, logprobs, tok_err, temperature, entropy, top_ids, top_logprobs,
+        _raw_stream(stream, logits)))
 
 
 # ----------------------------------------------------------------------------- tree construction

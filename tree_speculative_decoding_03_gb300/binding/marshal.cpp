@@ -1,6 +1,6 @@
 // marshal.cpp -- argument marshalling of the serving operators: torch tensors to the C ABI.
 //
-// A decoding step calls these three operators once per layer or step, each on up to fifteen
+// A decoding step calls these operators once per layer or step, each on up to sixteen
 // tensors whose types, shapes and devices have to be checked; in Python that costs more than the
 // launch (13 - 16 us a call on a Grace core, of which 5 - 8 us the launches).  Each function takes
 // the address of the library's entry point, the tensors and the raw stream (None: torch's current
@@ -225,7 +225,153 @@ PyObject* decode_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+int32_t* ints(const at::Tensor& t, const char* name, int64_t n) { return static_cast<int32_t*>(need(t, name, at::kInt, {n})); }
+
+// (entry, fork_src, fork_dst, seq_lens, seq_lens_out, block_table, blocks_held, blocks_held_out, shares, shares_out, free_blocks,
+//  free_count, free_count_out, copy_src, copy_dst, copy_rows, block_size, fork_err, stream)
+PyObject* kv_fork_seqs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 19, [&] {
+        const at::Tensor &fs = ranked(a[1], "fork_src", 1), &fd = tensor(a[2], "fork_dst"), &lens = tensor(a[3], "seq_lens"),
+                         &lo = tensor(a[4], "seq_lens_out"), &bt = ranked(a[5], "block_table", 2), &held = tensor(a[6], "blocks_held"),
+                         &ho = tensor(a[7], "blocks_held_out"), &sh = ranked(a[8], "shares", 1), &so = tensor(a[9], "shares_out"),
+                         &pool = tensor(a[10], "free_blocks"), &fc = tensor(a[11], "free_count"), &fo = tensor(a[12], "free_count_out"),
+                         &cs = tensor(a[13], "copy_src"), &cd = tensor(a[14], "copy_dst"), &cr = tensor(a[15], "copy_rows"),
+                         &err = tensor(a[17], "fork_err");
+        const int64_t F = fs.size(0), B = bt.size(0), mb = bt.size(1), nb = sh.size(0);
+        auto* p_bt = static_cast<int32_t*>(need(bt, "block_table", at::kInt, {B, mb}));
+        int32_t *p_fs = ints(fs, "fork_src", F), *p_fd = ints(fd, "fork_dst", F), *p_lens = ints(lens, "seq_lens", B),
+                *p_lo = ints(lo, "seq_lens_out", B), *p_held = ints(held, "blocks_held", B), *p_ho = ints(ho, "blocks_held_out", B),
+                *p_sh = ints(sh, "shares", nb), *p_so = ints(so, "shares_out", nb), *p_pool = ints(pool, "free_blocks", nb),
+                *p_fc = ints(fc, "free_count", 1), *p_fo = ints(fo, "free_count_out", 1), *p_cs = ints(cs, "copy_src", F),
+                *p_cd = ints(cd, "copy_dst", F), *p_cr = ints(cr, "copy_rows", F), *p_err = ints(err, "fork_err", F);
+        const long bs = PyLong_AsLong(a[16]);
+        if (bs == -1 && PyErr_Occurred()) return 0;
+        void* s = stream_for(a[18], {&bt, &fs, &fd, &lens, &lo, &held, &ho, &sh, &so, &pool, &fc, &fo, &cs, &cd, &cr, &err});
+        return call(entry<decltype(&tsv_kv_fork_seqs)>(a[0]), p_fs, p_fd, p_lens, p_lo, p_bt, p_held, p_ho, p_sh, p_so, p_pool, p_fc, p_fo,
+                    p_cs, p_cd, p_cr, small(F, "F"), small(B, "B"), small(bs, "block_size"), small(mb, "max_blocks"),
+                    small(nb, "num_blocks"), p_err, s);
+    });
+}
+
+// (entry, keep_lens, block_table, blocks_held, blocks_held_out, shares, shares_out, free_blocks, free_count, free_count_out, block_size,
+//  seq_err, stream)
+PyObject* kv_release_seqs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 13, [&] {
+        const at::Tensor &keep = tensor(a[1], "keep_lens"), &bt = ranked(a[2], "block_table", 2), &held = tensor(a[3], "blocks_held"),
+                         &ho = tensor(a[4], "blocks_held_out"), &sh = ranked(a[5], "shares", 1), &so = tensor(a[6], "shares_out"),
+                         &pool = tensor(a[7], "free_blocks"), &fc = tensor(a[8], "free_count"), &fo = tensor(a[9], "free_count_out"),
+                         &err = tensor(a[11], "seq_err");
+        const int64_t B = bt.size(0), mb = bt.size(1), nb = sh.size(0);
+        auto* p_bt = static_cast<int32_t*>(need(bt, "block_table", at::kInt, {B, mb}));
+        int32_t *p_keep = ints(keep, "keep_lens", B), *p_held = ints(held, "blocks_held", B), *p_ho = ints(ho, "blocks_held_out", B),
+                *p_sh = ints(sh, "shares", nb), *p_so = ints(so, "shares_out", nb), *p_pool = ints(pool, "free_blocks", nb),
+                *p_fc = ints(fc, "free_count", 1), *p_fo = ints(fo, "free_count_out", 1), *p_err = ints(err, "seq_err", B);
+        const long bs = PyLong_AsLong(a[10]);
+        if (bs == -1 && PyErr_Occurred()) return 0;
+        void* s = stream_for(a[12], {&bt, &keep, &held, &ho, &sh, &so, &pool, &fc, &fo, &err});
+        return call(entry<decltype(&tsv_kv_release_seqs)>(a[0]), p_keep, p_bt, p_held, p_ho, p_sh, p_so, p_pool, p_fc, p_fo, small(B, "B"),
+                    small(bs, "block_size"), small(mb, "max_blocks"), small(nb, "num_blocks"), p_err, s);
+    });
+}
+
+// (entry, block_table, block_table_out, blocks_held, shares, shares_out, free_blocks, free_count_out, copy_src, copy_dst, copy_count,
+//  seq_err, workspace, stream)
+PyObject* kv_compact_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const at::Tensor &bt = ranked(a[1], "block_table", 2), &bo = tensor(a[2], "block_table_out"), &held = tensor(a[3], "blocks_held"),
+                         &sh = ranked(a[4], "shares", 1), &so = tensor(a[5], "shares_out"), &pool = tensor(a[6], "free_blocks"),
+                         &fo = tensor(a[7], "free_count_out"), &cs = tensor(a[8], "copy_src"), &cd = tensor(a[9], "copy_dst"),
+                         &cc = tensor(a[10], "copy_count"), &err = tensor(a[11], "seq_err"), &ws = tensor(a[12], "workspace");
+        const int64_t B = bt.size(0), mb = bt.size(1), nb = sh.size(0);
+        auto* p_bt = static_cast<int32_t*>(need(bt, "block_table", at::kInt, {B, mb}));
+        auto* p_bo = static_cast<int32_t*>(need(bo, "block_table_out", at::kInt, {B, mb}));
+        int32_t *p_held = ints(held, "blocks_held", B), *p_sh = ints(sh, "shares", nb), *p_so = ints(so, "shares_out", nb),
+                *p_pool = ints(pool, "free_blocks", nb), *p_fo = ints(fo, "free_count_out", 1), *p_cs = ints(cs, "copy_src", nb / 2),
+                *p_cd = ints(cd, "copy_dst", nb / 2), *p_cc = ints(cc, "copy_count", 1), *p_err = ints(err, "seq_err", B);
+        if (!ws.is_contiguous()) throw Refused("workspace must be contiguous");
+        void* s = stream_for(a[13], {&bt, &bo, &held, &sh, &so, &pool, &fo, &cs, &cd, &cc, &err, &ws});
+        return call(entry<decltype(&tsv_kv_compact_blocks)>(a[0]), p_bt, p_bo, p_held, p_sh, p_so, p_pool, p_fo, p_cs, p_cd, p_cc,
+                    small(B, "B"), small(mb, "max_blocks"), small(nb, "num_blocks"), ws.data_ptr(), ws.nbytes(), p_err, s);
+    });
+}
+
+// (entry, k_cache, v_cache, copy_src, copy_dst, copy_rows, copy_count, copy_err, stream)
+PyObject* kv_copy_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        const at::Tensor &kc = ranked(a[1], "k_cache", 4), &vc = tensor(a[2], "v_cache"), &cs = ranked(a[3], "copy_src", 1),
+                         &cd = tensor(a[4], "copy_dst"), &err = tensor(a[7], "copy_err");
+        const at::Tensor *rows = a[5] == Py_None ? nullptr : &tensor(a[5], "copy_rows"), *count = a[6] == Py_None ? nullptr : &tensor(a[6], "copy_count");
+        const int64_t m = cs.size(0), nb = kc.size(0), bs = kc.size(1), Hkv = kc.size(2), D = kc.size(3);
+        const tsv_dtype dt = dtype_of(kc);
+        void* p_kc = need(kc, "k_cache", kc.scalar_type(), {nb, bs, Hkv, D});
+        void* p_vc = need(vc, "v_cache", kc.scalar_type(), {nb, bs, Hkv, D});
+        int32_t *p_cs = ints(cs, "copy_src", m), *p_cd = ints(cd, "copy_dst", m), *p_err = ints(err, "copy_err", m),
+                *p_rows = rows ? ints(*rows, "copy_rows", m) : nullptr, *p_count = count ? ints(*count, "copy_count", 1) : nullptr;
+        void* s = stream_for(a[8], {&kc, &vc, &cs, &cd, rows, count, &err});
+        return call(entry<decltype(&tsv_kv_copy_blocks)>(a[0]), p_kc, p_vc, p_cs, p_cd, p_rows, p_count, small(m, "n"), small(Hkv, "Hkv"),
+                    small(D, "D"), small(bs, "block_size"), small(nb, "num_blocks"), dt, p_err, s);
+    });
+}
+
+// (entry, q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out, scale, workspace, seq_err, lse, stream)
+PyObject* prefix_decode_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 14, [&] {
+        const at::Tensor &q = ranked(a[1], "q", 3), &kc = ranked(a[2], "k_cache", 4), &vc = tensor(a[3], "v_cache"),
+                         &bt = ranked(a[4], "block_table", 2), &lens = tensor(a[5], "seq_lens"), &off = tensor(a[6], "group_offsets"),
+                         &pre = ranked(a[7], "prefix_lens", 1), &out = tensor(a[8], "out"), &err = tensor(a[11], "seq_err");
+        const at::Tensor *ws = a[10] == Py_None ? nullptr : &tensor(a[10], "workspace"), *lse = a[12] == Py_None ? nullptr : &tensor(a[12], "lse");
+        const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2), nb = kc.size(0), bs = kc.size(1), Hkv = kc.size(2), mb = bt.size(1),
+                      G = pre.size(0);
+        const at::ScalarType type = q.scalar_type();
+        const tsv_dtype dt = dtype_of(q);
+        void* p_q = need(q, "q", type, {B, Hq, D});
+        void* p_out = need(out, "out", type, {B, Hq, D});
+        void* p_kc = need(kc, "k_cache", type, {nb, bs, Hkv, D});
+        void* p_vc = need(vc, "v_cache", type, {nb, bs, Hkv, D});
+        auto* p_bt = static_cast<int32_t*>(need(bt, "block_table", at::kInt, {B, mb}));
+        int32_t *p_lens = ints(lens, "seq_lens", B), *p_off = ints(off, "group_offsets", G + 1), *p_pre = ints(pre, "prefix_lens", G),
+                *p_err = ints(err, "seq_err", B);
+        auto* p_lse = lse ? static_cast<float*>(need(*lse, "lse", at::kFloat, {B, Hq})) : nullptr;
+        if (ws && !ws->is_contiguous()) throw Refused("workspace must be contiguous");
+        const double scale = PyFloat_AsDouble(a[9]);
+        if (scale == -1.0 && PyErr_Occurred()) return 0;
+        void* s = stream_for(a[13], {&q, &kc, &vc, &bt, &lens, &off, &pre, &out, ws, &err, lse});
+        return call(entry<decltype(&tsv_prefix_decode_attn)>(a[0]), p_q, p_kc, p_vc, p_bt, p_lens, p_off, p_pre, p_out, p_lse, small(B, "B"),
+                    small(G, "G"), small(Hq, "Hq"), small(Hkv, "Hkv"), small(D, "D"), small(bs, "block_size"), small(mb, "max_blocks"),
+                    small(nb, "num_blocks"), static_cast<float>(scale), dt, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : size_t(0), p_err, s);
+    });
+}
+
+// (entry, logits, tokens, logprobs, tok_err, temperature, entropy, top_ids, top_logprobs, stream)
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor &x = ranked(a[1], "logits", 2), &tok = tensor(a[2], "tokens"), &lp = tensor(a[3], "logprobs"), &err = tensor(a[4], "tok_err");
+        const at::Tensor *ent = a[6] == Py_None ? nullptr : &tensor(a[6], "entropy"), *ids = a[7] == Py_None ? nullptr : &ranked(a[7], "top_ids", 2),
+                         *tops = a[8] == Py_None ? nullptr : &tensor(a[8], "top_logprobs");
+        const int64_t T = x.size(0), V = x.size(1), top = ids ? ids->size(1) : 0;
+        const tsv_dtype dt = dtype_of(x);
+        if (V > 1 && x.stride(1) != 1) throw Refused("logits must have contiguous rows");
+        if ((ids == nullptr) != (tops == nullptr)) throw Refused("top_ids and top_logprobs go together");
+        int32_t *p_tok = ints(tok, "tokens", T), *p_err = ints(err, "tok_err", T);
+        auto* p_lp = static_cast<float*>(need(lp, "logprobs", at::kFloat, {T}));
+        auto* p_ent = ent ? static_cast<float*>(need(*ent, "entropy", at::kFloat, {T})) : nullptr;
+        auto* p_ids = ids ? static_cast<int32_t*>(need(*ids, "top_ids", at::kInt, {T, top})) : nullptr;
+        auto* p_tops = tops ? static_cast<float*>(need(*tops, "top_logprobs", at::kFloat, {T, top})) : nullptr;
+        const double temp = PyFloat_AsDouble(a[5]);
+        if (temp == -1.0 && PyErr_Occurred()) return 0;
+        void* s = stream_for(a[9], {&x, &tok, &lp, &err, ent, ids, tops});
+        return call(entry<decltype(&tsv_token_logprobs)>(a[0]), x.data_ptr(), T > 1 ? x.stride(0) : V, p_tok, small(T, "T"), small(V, "V"),
+                    static_cast<float>(temp), small(top, "top"), dt, p_lp, p_ent, p_ids, p_tops, p_err, s);
+    });
+}
+
 PyMethodDef methods[] = {
+    {"kv_fork_seqs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_fork_seqs)), METH_FASTCALL, nullptr},
+    {"kv_release_seqs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_release_seqs)), METH_FASTCALL, nullptr},
+    {"kv_compact_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_compact_blocks)), METH_FASTCALL, nullptr},
+    {"kv_copy_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_copy_blocks)), METH_FASTCALL, nullptr},
+    {"prefix_decode_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_decode_attn)), METH_FASTCALL, nullptr},
+    {"token_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(token_logprobs)), METH_FASTCALL, nullptr},
     {"kv_plan_slots", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_plan_slots)), METH_FASTCALL, nullptr},
     {"rope_kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_kv_append)), METH_FASTCALL, nullptr},
     {"decode_attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_attn)), METH_FASTCALL, nullptr},

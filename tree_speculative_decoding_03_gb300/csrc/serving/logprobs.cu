@@ -1,0 +1,396 @@
+// logprobs.cu -- log probabilities of given tokens, entropy and top alternatives of logits rows.
+//
+// With z = x / T, m = max z, s = sum e^{z - m}, w = sum e^{z - m} (z - m):
+//   log p(t) = z_t - m - ln s,   H = -sum p ln p = ln s - w / s.
+// One pass: every thread keeps a running m, s and w of its slice in fp32 and rescales them when m
+// grows (s' = f s, w' = f (w + s (m_old - m)), f = e^{m_old - m}).  Bound by the logits' bytes.
+//
+// The alternatives come from the same pass: a thread's running maximum is the largest of its
+// slice.  Of 64 groups of threads the n-th largest group maximum is a bound that at least n
+// entries reach, so only slices whose maximum reaches it hold alternatives -- some n of 512 --
+// and those few are read again, from L2, by whole warps, each of which keeps its n best in order,
+// one a lane.  Nothing depends on the values but the time: a row of equal logits is read twice.
+// Order: value descending (-0 and 0 are equal), then index ascending, as one 64-bit key.
+//
+// A row is taken by one CTA, or by a cluster of up to eight where there are too few rows to fill the GPU.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "../common.cuh"
+#include "continue_args.cuh"
+
+namespace tsv {
+namespace {
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kGroups = 64, kGroupThreads = kThreads / kGroups;
+constexpr int kAhead = 4;  // vectors of a thread on their way together
+constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
+// z - m in units of log2 is held above this, where e^{z - m} is 0 in fp32: a logit of -inf then adds
+// 0 * -200 to w and not 0 * -inf
+constexpr float kFloor = -200.0f;
+static_assert(kGroups >= kMaxTop && kMaxTop <= 32, "a group for each alternative, a lane for each");
+
+typedef unsigned long long Key;  // 0: none
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+// larger value, then lower index, is the larger key; finite and -inf values give keys above 0
+__device__ __forceinline__ Key make_key(float x, uint32_t index) {
+    const uint32_t u = __float_as_uint(x + 0.0f), ord = u & 0x80000000u ? ~u : u | 0x80000000u;
+    return (static_cast<Key>(ord) << 32) | (0xffffffffu - index);
+}
+__device__ __forceinline__ float key_value(Key k) {
+    const uint32_t o = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int key_index(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+
+// A 16-byte vector of logits as floats.
+template <typename Elem>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    uint4 r;
+    __device__ __forceinline__ void load(const void* p) { r = __ldcs(static_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void none() { r = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    __device__ __forceinline__ void set(int i, const float* p) {
+        const uint32_t u = __float_as_uint(*p);
+        if (i == 0) r.x = u;
+        if (i == 1) r.y = u;
+        if (i == 2) r.z = u;
+        if (i == 3) r.w = u;
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w); }
+    __device__ __forceinline__ float top() const { return max_nan(max_nan(get(0), get(1)), max_nan(get(2), get(3))); }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    uint4 r;
+    __device__ __forceinline__ void load(const void* p) { r = __ldcs(static_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void none() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    __device__ __forceinline__ void set(int i, const __nv_bfloat16* p) {
+        const uint32_t u = *reinterpret_cast<const unsigned short*>(p), keep = i & 1 ? 0x0000ffffu : 0xffff0000u, put = i & 1 ? u << 16 : u;
+        if (i >> 1 == 0) r.x = (r.x & keep) | put;
+        if (i >> 1 == 1) r.y = (r.y & keep) | put;
+        if (i >> 1 == 2) r.z = (r.z & keep) | put;
+        if (i >> 1 == 3) r.w = (r.w & keep) | put;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t u = i >> 1 == 0 ? r.x : i >> 1 == 1 ? r.y : i >> 1 == 2 ? r.z : r.w;
+        return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+    }
+    __device__ __forceinline__ float top() const {
+        const uint32_t u = max_nan2(max_nan2(r.x, r.y), max_nan2(r.z, r.w));
+        return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+};
+
+// A row as aligned vectors: the first may begin before the row and the last end behind it, and of
+// those only the row's own elements are read.
+template <typename Elem>
+struct Row {
+    static constexpr int N = Vec<Elem>::N;
+    const Elem* x;
+    int head, V, vecs;  // elements of the first vector before the row
+    __device__ __forceinline__ Row(const Elem* row, int V_)
+        : x(row), head(static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(Elem))), V(V_) {
+        vecs = static_cast<int>(((long long)head + V + N - 1) / N);
+    }
+    __device__ __forceinline__ int index(int v) const { return v * N - head; }  // of the vector's first element
+    __device__ __forceinline__ Vec<Elem> load(int v) const {
+        Vec<Elem> y;
+        const int i0 = index(v);
+        if (i0 >= 0 && i0 <= V - N) {
+            y.load(x + i0);
+        } else {
+            y.none();
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i0 + i >= 0 && i0 + i < V) y.set(i, x + i0 + i);
+        }
+        return y;
+    }
+};
+
+// Running sums of a slice, m in units of x.
+struct Stats {
+    float m, s, w;
+    // c = log2(e) / T
+    __device__ __forceinline__ void rise(float to, float c) {
+        const float d = fmaxf((m - to) * c, kFloor), f = ex2(d);
+        w = f * fmaf(s, d, w);
+        s *= f;
+        m = to;
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float w2, float c) {
+        Stats o{m2, s2, w2};
+        if (o.m > m) rise(o.m, c);
+        if (m > o.m) o.rise(m, c);
+        s += o.s;
+        w += o.w;
+    }
+};
+
+// The best keys of a warp, in order: lane i holds the i-th (0: none).
+struct Best {
+    Key key = 0;
+    // the lanes' candidates (0: none); `top` are kept
+    __device__ __forceinline__ void add(Key k, int top) {
+        const int lane = threadIdx.x & 31;
+        Key least = __shfl_sync(0xffffffffu, key, top - 1);
+        unsigned todo = __ballot_sync(0xffffffffu, k > least);
+        while (todo) {
+            const Key n = __shfl_sync(0xffffffffu, k, __ffs(todo) - 1);
+            const int pos = __popc(__ballot_sync(0xffffffffu, key > n));
+            const Key up = __shfl_up_sync(0xffffffffu, key, 1);
+            if (lane == pos) key = n;
+            if (lane > pos) key = up;
+            least = __shfl_sync(0xffffffffu, key, top - 1);
+            todo &= todo - 1;
+            todo &= __ballot_sync(0xffffffffu, k > least);
+        }
+    }
+};
+
+// Ranks the `n` keys of `keys` (distinct): the thread of rank r < top gives out[r].
+__device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* out) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const Key k = keys[i];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += keys[j] > k;
+        if (r < top) out[r] = k;
+    }
+}
+
+template <typename Elem, int CLUSTER, bool ENTROPY>
+__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+    constexpr int N = Vec<Elem>::N;
+    __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps], s_group[kGroups];
+    __shared__ Stats s_stats;   // of the CTA
+    __shared__ int s_bad, s_n;
+    __shared__ float s_bound;
+    __shared__ Key s_keys[kWarps * 32], s_best[32];
+    __shared__ Key s_all[CLUSTER > 1 ? CLUSTER * 32 : 1];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CLUSTER == 1 ? 0 : static_cast<int>(blockIdx.x % CLUSTER);
+    const int t = static_cast<int>(blockIdx.x / CLUSTER);
+    const int token = a.tokens[t];
+    if (token < 0 || token >= a.V) {  // padding, or a wrong token: the same in every CTA of the cluster
+        if (rank == 0) {
+            const float x = token < 0 ? 0.0f : __int_as_float(0x7fc00000);
+            if (tid == 0) {
+                a.logprob[t] = x;
+                if (ENTROPY) a.entropy[t] = x;
+                a.tok_err[t] = token < 0 ? 0 : TSV_DERR_TOKEN;
+            }
+            if (tid < a.top) {
+                a.top_ids[(long long)t * a.top + tid] = -1;
+                a.top_logprobs[(long long)t * a.top + tid] = x;
+            }
+        }
+        return;
+    }
+    const Elem* x = static_cast<const Elem*>(a.logits) + (long long)t * a.stride;
+    const Row<Elem> row(x, a.V);
+    const int begin = static_cast<int>((long long)row.vecs * rank / CLUSTER), end = static_cast<int>((long long)row.vecs * (rank + 1) / CLUSTER);
+    const float c = a.inv_t * kLog2e;
+    Stats st{-INFINITY, 0.0f, 0.0f};
+    bool bad = false;
+    for (int v = begin + tid; v < end; v += kAhead * kThreads) {
+        Vec<Elem> y[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (v + u * kThreads < end)
+                y[u] = row.load(v + u * kThreads);
+            else
+                y[u].none();
+        }
+        float top = y[0].top();
+#pragma unroll
+        for (int u = 1; u < kAhead; ++u) top = max_nan(top, y[u].top());
+        if (!(top <= st.m)) {
+            bad |= !(top < INFINITY);  // +inf or NaN
+            st.rise(top, c);
+        }
+        if (st.m == -INFINITY) continue;
+        float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float d = (y[u].get(i) - st.m) * c;
+                if (ENTROPY) d = fmaxf(d, kFloor);
+                const float p = ex2(d);
+                s[i & 1] += p;
+                if (ENTROPY) w[i & 1] = fmaf(p, d, w[i & 1]);
+            }
+        st.s += s[0] + s[1];
+        st.w += w[0] + w[1];
+    }
+    const float slice_max = st.m;
+    if (tid == 0) s_n = 0;
+    // the CTA's sums, in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        st.join(__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o), __shfl_xor_sync(0xffffffffu, st.w, o), c);
+    if (lane == 0) {
+        s_m[warp] = st.m;
+        s_s[warp] = st.s;
+        s_w[warp] = st.w;
+    }
+    if (a.top > 0) {
+        float g = slice_max;
+#pragma unroll
+        for (int o = 1; o < kGroupThreads; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (tid % kGroupThreads == 0) s_group[tid / kGroupThreads] = g;
+    }
+    bad = __syncthreads_or(bad);
+    if (warp == 0) {
+        Stats all{lane < kWarps ? s_m[lane] : -INFINITY, lane < kWarps ? s_s[lane] : 0.0f, lane < kWarps ? s_w[lane] : 0.0f};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            all.join(__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.s, o), __shfl_xor_sync(0xffffffffu, all.w, o), c);
+        if (lane == 0) {
+            s_stats = all;
+            s_bad = bad;
+        }
+    }
+    if (a.top > 0) {
+        // the bound: the top-th largest of the group maxima (in a bad row, none may be found)
+        if (tid == 0) s_bound = -INFINITY;
+        __syncthreads();
+        if (tid < kGroups) {
+            const float g = s_group[tid];
+            int r = 0;
+#pragma unroll 8
+            for (int j = 0; j < kGroups; ++j) {
+                const float o = s_group[j];
+                r += o > g || (o == g && j < tid);
+            }
+            if (r == a.top - 1) s_bound = g;
+        }
+        __syncthreads();
+        const float bound = s_bound;
+        Best best;
+        unsigned slices = bad ? 0u : __ballot_sync(0xffffffffu, slice_max >= bound);
+        while (slices) {
+            const int owner = warp * 32 + __ffs(slices) - 1;
+            slices &= slices - 1;
+            for (int v0 = begin + owner; v0 < end; v0 += 32 * kThreads) {
+                const int v = v0 + lane * kThreads;
+                Vec<Elem> y;
+                y.none();
+                if (v < end) y = row.load(v);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int at = row.index(v) + i;
+                    const float z = y.get(i);
+                    const bool in = v < end && at >= 0 && at < a.V && z >= bound;
+                    if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
+                }
+            }
+        }
+        // the warps' lists together
+        const unsigned have = __ballot_sync(0xffffffffu, best.key != 0 && lane < a.top);
+        int at = 0;
+        if (lane == 0 && have) at = atomicAdd(&s_n, __popc(have));
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if ((have >> lane) & 1u) s_keys[at + lane] = best.key;
+        if (tid < 32) s_best[tid] = 0;
+        __syncthreads();
+        rank_keys(s_keys, s_n, a.top, s_best);
+    }
+    __syncthreads();
+    Stats all = s_stats;
+    bad = s_bad != 0;
+    if (CLUSTER > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        if (rank == 0) {
+            all = Stats{-INFINITY, 0.0f, 0.0f};
+            bad = false;
+            Key least = 0;  // the largest of the CTAs' last keys: at least `top` keys reach it
+            for (int r = 0; r < CLUSTER; ++r) {
+                const Stats o = *cl.map_shared_rank(&s_stats, r);
+                all.join(o.m, o.s, o.w, c);
+                bad |= *cl.map_shared_rank(&s_bad, r) != 0;
+                if (a.top > 0) least = max(least, cl.map_shared_rank(s_best, r)[a.top - 1]);
+            }
+            if (a.top > 0) {
+                if (tid == 0) s_n = 0;
+                __syncthreads();
+                for (int i = tid; i < CLUSTER * a.top; i += kThreads) {
+                    const Key k = cl.map_shared_rank(s_best, i / a.top)[i % a.top];
+                    if (k != 0 && k >= least) s_all[atomicAdd(&s_n, 1)] = k;
+                }
+                __syncthreads();
+                rank_keys(s_all, s_n, a.top, s_keys);  // (s_keys is this CTA's own, no longer read)
+                __syncthreads();
+                if (tid < a.top) s_best[tid] = s_keys[tid];
+            }
+        }
+        cl.sync();  // no CTA leaves while its sums and keys are read
+        if (rank != 0) return;
+    }
+    // a row without a finite logit has no distribution
+    bad |= !(all.m > -INFINITY);
+    const float nan = __int_as_float(0x7fc00000), log_s = logf(all.s);
+    if (tid == 0) {
+        const float xt = static_cast<float>(x[token]);
+        a.logprob[t] = bad ? nan : (xt - all.m) * a.inv_t - log_s;
+        if (ENTROPY) a.entropy[t] = bad ? nan : log_s - kLn2 * (all.w / all.s);
+        a.tok_err[t] = bad ? TSV_DERR_NONFINITE : 0;
+    }
+    if (tid < a.top) {
+        const Key k = s_best[tid];
+        a.top_ids[(long long)t * a.top + tid] = bad ? -1 : key_index(k);
+        a.top_logprobs[(long long)t * a.top + tid] = bad ? nan : (key_value(k) - all.m) * a.inv_t - log_s;
+    }
+}
+
+template <typename Elem, int CLUSTER>
+cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t stream) {
+    const auto kernel = a.entropy ? token_logprobs_kernel<Elem, CLUSTER, true> : token_logprobs_kernel<Elem, CLUSTER, false>;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.T) * CLUSTER), dim3(kThreads), 0, stream, static_cast<unsigned>(CLUSTER), a);
+}
+
+template <typename Elem>
+cudaError_t launch_type(const LogprobArgs& a, int num_sms, cudaStream_t stream) {
+    // CTAs a row: as many as still find a place (two an SM) and have a vector for each thread
+    const long long vecs = ((long long)a.V + Vec<Elem>::N - 1) / Vec<Elem>::N;
+    int n = 1;
+    while (n < 8 && 2LL * n * a.T <= 2LL * num_sms && vecs >= 2LL * n * kThreads) n *= 2;
+    switch (n) {
+        case 8: return launch_rows<Elem, 8>(a, stream);
+        case 4: return launch_rows<Elem, 4>(a, stream);
+        case 2: return launch_rows<Elem, 2>(a, stream);
+        default: return launch_rows<Elem, 1>(a, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+    return bf16 ? launch_type<__nv_bfloat16>(a, num_sms, stream) : launch_type<float>(a, num_sms, stream);
+}
+
+}  // namespace tsv

@@ -1,0 +1,604 @@
+// pages.cu -- cache blocks that several sequences share: sequences forked, blocks released by
+// reference, the cache put together at its low end, block contents copied.
+//
+// shares[i] counts the table entries of block i beyond its first: 0 for a block of one sequence and
+// for a free one.  (A count of all entries would have to be set where blocks are taken, in the
+// slot plan too; this one is right for every block that the plan takes or gives back.)
+//
+// All but the copy are integers: chains of latencies (launch, lengths, scan, ids) over a few hundred
+// KB of tables, not bytes.  Places in the pool and in the copy lists are prefix sums in an order that
+// the arguments fix (forks in order, ids ascending), and the only atomics are counts and error
+// bits, whose result does not depend on their order.
+#include <cooperative_groups.h>
+
+#include "../common.cuh"
+#include "continue_args.cuh"
+
+namespace tsv {
+namespace {
+namespace cg = cooperative_groups;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kRowThreads = 256;
+constexpr int kFatal = TSV_DERR_SEQ | TSV_DERR_CAPACITY | TSV_DERR_POOL;  // errors that leave a fork undone
+
+__device__ __forceinline__ int cdiv_shift(int x, int s) { return (x >> s) + ((x & ((1 << s) - 1)) != 0); }
+
+// The sum over the block's threads before this one; *total: over all.  1024 threads.
+__device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // s_warp of the last scan has been read
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return incl - x + (warp ? before : 0);
+}
+
+// ------------------------------------------------------------------ fork
+
+// CTA 0 checks the forks, gives each its fresh block and writes the lists; the others copy the
+// shares when the result is another array.
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ ForkArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int step = (gridDim.x - 1) * kPlanThreads;
+        for (int i = (blockIdx.x - 1) * kPlanThreads + tid; i < a.num_blocks; i += step) a.shares_out[i] = a.shares[i];
+        return;
+    }
+    extern __shared__ int s_claims[];  // [B]: forks to the sequence
+    __shared__ int s_warp[32];
+    for (int b = tid; b < a.B; b += kPlanThreads) {
+        s_claims[b] = 0;
+        if (a.held_out != a.held) a.held_out[b] = a.held[b];
+        if (a.seq_lens_out != a.seq_lens) a.seq_lens_out[b] = a.seq_lens[b];
+    }
+    const int count = *a.free_count;
+    const bool count_ok = count >= 0 && count <= a.num_blocks;
+    __syncthreads();
+    for (int i = tid; i < a.F; i += kPlanThreads) {
+        const int d = a.fork_dst[i];
+        if (a.fork_src[i] >= 0 && d >= 0 && d < a.B) atomicAdd(&s_claims[d], 1);
+    }
+    __syncthreads();
+    constexpr int kPer = kPagesMaxForks / kPlanThreads;
+    const int per = (a.F + kPlanThreads - 1) / kPlanThreads;  // consecutive forks of a thread, at most kPer
+    int src[kPer], dst[kPer], len[kPer], err[kPer], part[kPer];
+    int needs = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        src[u] = -1;
+        const int i = tid * per + u;
+        if (u >= per || i >= a.F) continue;
+        src[u] = a.fork_src[i];
+        if (src[u] < 0) continue;
+        dst[u] = a.fork_dst[i];
+        err[u] = 0;
+        part[u] = -1;
+        len[u] = 0;
+        if (src[u] >= a.B || dst[u] < 0 || dst[u] >= a.B || s_claims[dst[u]] > 1 || a.held[dst[u]] != 0) {
+            err[u] = TSV_DERR_SEQ;
+            continue;
+        }
+        const int L = a.seq_lens[src[u]], h = a.held[src[u]];
+        if (L < 0 || h < 0 || h > a.max_blocks || cdiv_shift(L, a.bs_log2) > h) {
+            err[u] = TSV_DERR_CAPACITY;
+            continue;
+        }
+        if (!count_ok) {
+            err[u] = TSV_DERR_POOL;
+            continue;
+        }
+        len[u] = L;
+        if (L & ((1 << a.bs_log2) - 1)) {
+            part[u] = a.block_table[(long long)src[u] * a.max_blocks + (L >> a.bs_log2)];
+            ++needs;
+            err[u] = -1;  // takes a block
+        }
+    }
+    int total;
+    int taken = block_scan(needs, s_warp, &total);  // (its barriers: every input has been read by now)
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int i = tid * per + u;
+        if (u >= per || i >= a.F) continue;
+        int from = -1, to = -1, rows = 0, e = 0;
+        if (src[u] >= 0) {
+            e = err[u];
+            const int full = len[u] >> a.bs_log2;
+            if (e == -1) {
+                e = 0;
+                if (++taken > count) {
+                    e = TSV_DERR_POOL;
+                } else {
+                    const int fresh = a.free_blocks[count - taken];
+                    a.block_table[(long long)dst[u] * a.max_blocks + full] = fresh;
+                    if (part[u] < 0 || part[u] >= a.num_blocks || fresh < 0 || fresh >= a.num_blocks) {
+                        e = TSV_DERR_BLOCK;
+                    } else {
+                        from = part[u];
+                        to = fresh;
+                        rows = len[u] & ((1 << a.bs_log2) - 1);
+                    }
+                }
+            }
+            if (!(e & kFatal)) {
+                a.held_out[dst[u]] = cdiv_shift(len[u], a.bs_log2);
+                a.seq_lens_out[dst[u]] = len[u];
+            }
+        }
+        a.copy_src[i] = from;
+        a.copy_dst[i] = to;
+        a.copy_rows[i] = rows;
+        a.fork_err[i] = e;
+    }
+    if (tid == 0) *a.free_count_out = count_ok ? count - min(total, count) : count;
+}
+
+// One fork a CTA (blockIdx.y divides long rows): the source's full blocks go into the destination's
+// row, a reference each.
+__global__ void __launch_bounds__(kRowThreads) kv_fork_rows_kernel(const __grid_constant__ ForkArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int i = blockIdx.x, src = a.fork_src[i];
+    if (src < 0 || (a.fork_err[i] & kFatal)) return;
+    const int dst = a.fork_dst[i], full = a.seq_lens_out[dst] >> a.bs_log2;
+    const int32_t* from = a.block_table + (long long)src * a.max_blocks;
+    int32_t* to = a.block_table + (long long)dst * a.max_blocks;
+    constexpr int U = 4;
+    bool bad = false;
+    for (int j0 = (blockIdx.y * U) * kRowThreads + threadIdx.x; j0 < full; j0 += gridDim.y * U * kRowThreads) {
+        int id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = j0 + u * kRowThreads < full ? from[j0 + u * kRowThreads] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * kRowThreads;
+            if (j >= full || !TSV_IN_BOUNDS(j, a.max_blocks, a.fork_err + i)) continue;
+            to[j] = id[u];
+            if (id[u] >= 0 && id[u] < a.num_blocks)
+                atomicAdd(a.shares_out + id[u], 1);
+            else
+                bad = true;
+        }
+    }
+    if (bad) atomicOr(a.fork_err + i, TSV_DERR_BLOCK);
+}
+
+// ------------------------------------------------------------------ scans over the block ids
+
+// CTA `rank` of `ctas` takes a run of ids, in tiles of 4096: a warp 128 neighbours, 32 at a time.
+constexpr int kTileIds = 4 * kPlanThreads;
+struct IdRun {
+    int first, end;
+    __device__ __forceinline__ IdRun(int num_blocks, int rank, int ctas) {
+        const int chunk = (num_blocks + ctas - 1) / ctas;
+        first = min(rank * chunk, num_blocks);
+        end = min(first + chunk, num_blocks);
+    }
+    __device__ __forceinline__ static int id(int tile, int u) {
+        return tile + (threadIdx.x >> 5) * 128 + u * 32 + (threadIdx.x & 31);
+    }
+};
+
+// Ranks within a tile: rank[u] = marked ids of the tile before id(tile, u); returns their number.
+__device__ __forceinline__ int tile_ranks(const bool (&mark)[4], int (&rank)[4], int* s_warp) {
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const unsigned m = __ballot_sync(0xffffffffu, mark[u]);
+        rank[u] = sum + __popc(m & ((1u << lane) - 1));
+        sum += __popc(m);
+    }
+    int total;
+    // every lane holds the warp's sum: one lane hands it to the scan, the others nothing
+    const int before = block_scan(lane == 0 ? sum : 0, s_warp, &total);
+    const int base = __shfl_sync(0xffffffffu, before, 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) rank[u] += base;
+    return total;
+}
+
+// Sum of `mine` over the cluster's CTAs before this one; *all: over all CTAs.
+template <int CLUSTER>
+__device__ __forceinline__ int cluster_before(int mine, int* s_slot, int* all) {
+    if (CLUSTER == 1) {
+        *all = mine;
+        return 0;
+    }
+    cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) *s_slot = mine;
+    cl.sync();
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) {
+        const int x = *cl.map_shared_rank(s_slot, r);
+        before += r < static_cast<int>(cl.block_rank()) ? x : 0;
+        sum += x;
+    }
+    *all = sum;
+    return before;
+}
+template <int CLUSTER>
+__device__ __forceinline__ void cluster_barrier() {
+    if (CLUSTER == 1)
+        __syncthreads();
+    else
+        cg::this_cluster().sync();
+}
+template <int CLUSTER>
+__device__ __forceinline__ int cluster_rank() {
+    return CLUSTER == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+}
+
+// ------------------------------------------------------------------ release
+
+// Entries a sequence keeps; *err: what is wrong with it (then it keeps all).
+__device__ __forceinline__ int kept_blocks(const ReleaseArgs& a, int held, int keep, bool count_ok, int* err) {
+    *err = 0;
+    if (held < 0 || held > a.max_blocks || keep < 0)
+        *err = TSV_DERR_CAPACITY;
+    else if (!count_ok)
+        *err = TSV_DERR_POOL;
+    return *err ? held : min(held, cdiv_shift(keep, a.bs_log2));
+}
+
+__global__ void __launch_bounds__(256) copy_ints_kernel(int32_t* to, const int32_t* from, int n) {
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) to[i] = from[i];
+}
+
+// One sequence a CTA: each released entry takes one reference off its block; -1 is none left.
+__global__ void __launch_bounds__(kPlanThreads) kv_release_count_kernel(const __grid_constant__ ReleaseArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, count = *a.free_count, held = a.held[b];
+    int err;
+    const int stay = kept_blocks(a, held, a.keep_lens[b], count >= 0 && count <= a.num_blocks, &err);
+    const int32_t* row = a.block_table + (long long)b * a.max_blocks;
+    bool bad = false;
+    constexpr int U = 4;
+    const int n = blockDim.x;
+    if (err == 0)
+        for (int j0 = stay + threadIdx.x; j0 < held; j0 += U * n) {
+            int id[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) id[u] = j0 + u * n < held ? row[j0 + u * n] : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j0 + u * n >= held) continue;
+                if (id[u] >= 0 && id[u] < a.num_blocks)
+                    atomicSub(a.shares_out + id[u], 1);
+                else
+                    bad = true;
+            }
+        }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : err;
+}
+
+// One cluster: blocks without a reference go onto the pool in order of their ids.
+template <int CLUSTER>
+__global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __grid_constant__ ReleaseArgs a) {
+    __shared__ int s_warp[32], s_slot[2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, rank = cluster_rank<CLUSTER>();
+    const IdRun run(a.num_blocks, rank, CLUSTER);
+    const int count = *a.free_count;
+    const bool count_ok = count >= 0 && count <= a.num_blocks;
+    int mine = 0;
+    bool over = false;
+    for (int id = run.first + tid; id < run.end; id += kPlanThreads) {
+        const int s = a.shares_out[id];
+        mine += s < 0;
+        over |= s < -1;
+    }
+    int sum;
+    block_scan(mine, s_warp, &sum);
+    int all, any;
+    const int before = cluster_before<CLUSTER>(count_ok ? sum : 0, &s_slot[0], &all);
+    cluster_before<CLUSTER>(__syncthreads_or(over), &s_slot[1], &any);
+    const bool full = count_ok && all > a.num_blocks - count;
+    if (any || full) {
+        // more references given back than there were, or more blocks than the pool has places: the
+        // sequences that took part are told
+        for (int b = rank; b < a.B; b += CLUSTER) {
+            const int held = a.held[b];
+            int err;
+            const int stay = kept_blocks(a, held, a.keep_lens[b], count_ok, &err);
+            bool hit = full && err == 0 && stay < held;
+            if (err == 0)
+                for (int j = stay + tid; j < held; j += kPlanThreads) {
+                    const int id = a.block_table[(long long)b * a.max_blocks + j];
+                    hit |= id >= 0 && id < a.num_blocks && a.shares_out[id] < -1;
+                }
+            if (__syncthreads_or(hit) && tid == 0) a.seq_err[b] |= TSV_DERR_POOL;
+        }
+    }
+    cluster_barrier<CLUSTER>();  // counts and shares have been read
+    int place = count + before;
+    for (int tile = run.first; tile < run.end; tile += kTileIds) {
+        bool mark[4];
+        int r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int id = IdRun::id(tile, u);
+            mark[u] = count_ok && id < run.end && a.shares_out[id] < 0;
+        }
+        const int n = tile_ranks(mark, r, s_warp);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (!mark[u]) continue;
+            const int id = IdRun::id(tile, u);
+            a.shares_out[id] = 0;
+            if (place + r[u] < a.num_blocks) a.free_blocks[place + r[u]] = id;
+        }
+        place += n;
+    }
+    for (int b = rank * kPlanThreads + tid; b < a.B; b += CLUSTER * kPlanThreads) {
+        int err;
+        a.held_out[b] = kept_blocks(a, a.held[b], a.keep_lens[b], count_ok, &err);
+    }
+    if (rank == 0 && tid == 0) *a.free_count_out = count_ok ? min(count + all, a.num_blocks) : count;
+}
+
+// ------------------------------------------------------------------ compaction
+
+__global__ void __launch_bounds__(256) kv_compact_clear_kernel(const __grid_constant__ CompactBlocksArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < a.num_blocks; i += gridDim.x * 256) {
+        a.remap[i] = 0;
+        if (i < a.num_blocks / 2) {
+            a.copy_src[i] = -1;
+            a.copy_dst[i] = -1;
+        }
+    }
+}
+
+// One sequence a CTA: its blocks are live.
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_mark_kernel(const __grid_constant__ CompactBlocksArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, held = a.held[b];
+    const bool ok = held >= 0 && held <= a.max_blocks;
+    const int32_t* row = a.block_table + (long long)b * a.max_blocks;
+    bool bad = false;
+    if (ok)
+        for (int j = threadIdx.x; j < held; j += blockDim.x) {
+            const int id = row[j];
+            if (id >= 0 && id < a.num_blocks)
+                a.remap[id] = 1;
+            else
+                bad = true;
+        }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) a.seq_err[b] = !ok ? TSV_DERR_CAPACITY : bad ? TSV_DERR_BLOCK : 0;
+}
+
+// One cluster: with n live blocks, the k-th live id from n on moves to the k-th free id below n.
+template <int CLUSTER>
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __grid_constant__ CompactBlocksArgs a) {
+    __shared__ int s_warp[32], s_slot[2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, rank = cluster_rank<CLUSTER>();
+    const IdRun run(a.num_blocks, rank, CLUSTER);
+    int mine = 0;
+    for (int id = run.first + tid; id < run.end; id += kPlanThreads) mine += a.remap[id];
+    int sum, n, moves;
+    block_scan(mine, s_warp, &sum);
+    const int before = cluster_before<CLUSTER>(sum, &s_slot[0], &n);
+    mine = 0;
+    for (int id = max(run.first, n) + tid; id < run.end; id += kPlanThreads) mine += a.remap[id];
+    block_scan(mine, s_warp, &sum);
+    cluster_before<CLUSTER>(sum, &s_slot[1], &moves);
+    cluster_barrier<CLUSTER>();
+    int place = before;  // live ids before the tile
+    for (int tile = run.first; tile < run.end; tile += kTileIds) {
+        bool mark[4];
+        int r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int id = IdRun::id(tile, u);
+            mark[u] = id < run.end && a.remap[id] != 0;
+        }
+        const int live = tile_ranks(mark, r, s_warp);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int id = IdRun::id(tile, u);
+            if (id >= run.end) continue;
+            const int rk = place + r[u];
+            if (mark[u] && id < n) {
+                a.remap[id] = id;
+                if (a.shares_out != a.shares) a.shares_out[id] = a.shares[id];
+            } else if (mark[u]) {
+                // its share moves with it, below
+                if (TSV_IN_BOUNDS(rk - (n - moves), a.num_blocks / 2, nullptr)) a.copy_src[rk - (n - moves)] = id;
+            } else {
+                if (id < n && TSV_IN_BOUNDS(id - rk, a.num_blocks / 2, nullptr)) a.copy_dst[id - rk] = id;
+                a.shares_out[id] = 0;
+            }
+            if (id < a.num_blocks - n) a.free_blocks[id] = a.num_blocks - 1 - id;
+        }
+        place += live;
+    }
+    __threadfence();
+    cluster_barrier<CLUSTER>();
+    for (int k = rank * kPlanThreads + tid; k < moves; k += CLUSTER * kPlanThreads) {
+        const int from = __ldcg(a.copy_src + k), to = __ldcg(a.copy_dst + k);
+        a.remap[from] = to;
+        const int s = __ldcg(a.shares + from);
+        a.shares_out[to] = s;
+        a.shares_out[from] = 0;
+    }
+    if (rank == 0 && tid == 0) {
+        *a.free_count_out = a.num_blocks - n;
+        *a.copy_count = moves;
+    }
+}
+
+// One sequence a CTA: its row under the new ids; entries that are not held stay.
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_rows_kernel(const __grid_constant__ CompactBlocksArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, held = a.held[b];
+    const int mine = held <= a.max_blocks ? held : 0;
+    const int end = a.block_table_out == a.block_table ? mine : a.max_blocks;
+    const int32_t* row = a.block_table + (long long)b * a.max_blocks;
+    int32_t* out = a.block_table_out + (long long)b * a.max_blocks;
+    constexpr int U = 4;
+    const int step = blockDim.x;
+    for (int j0 = threadIdx.x; j0 < end; j0 += U * step) {
+        int id[U], to[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = j0 + u * step < end ? row[j0 + u * step] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) to[u] = j0 + u * step < mine && id[u] >= 0 && id[u] < a.num_blocks ? a.remap[id[u]] : id[u];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j0 + u * step < end) out[j0 + u * step] = to[u];
+    }
+}
+
+// ------------------------------------------------------------------ copy
+
+// A piece is 16 KB of one block of one cache: 4 vectors a thread, all on their way before one is
+// written.
+constexpr int kCopyThreads = 256, kCopyVecs = 4, kPieceVecs = kCopyThreads * kCopyVecs;
+
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ CopyArgs a, int pieces) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int n = a.copy_count ? min(max(*a.copy_count, 0), a.n) : a.n;
+    for (int i = blockIdx.x * kCopyThreads + threadIdx.x; i < a.n; i += gridDim.x * kCopyThreads) {
+        int e = 0;
+        if (i < n && a.copy_src[i] >= 0) {
+            const int d = a.copy_dst[i];
+            if (a.copy_src[i] >= a.num_blocks || d < 0 || d >= a.num_blocks) e = TSV_DERR_BLOCK;
+        }
+        a.copy_err[i] = e;
+    }
+    const long long all = (long long)n * 2 * pieces, block_vecs = (long long)a.bs * a.row_vecs;
+    for (long long w = blockIdx.x; w < all; w += gridDim.x) {
+        const int i = static_cast<int>(w / (2 * pieces)), rest = static_cast<int>(w % (2 * pieces));
+        const int s = a.copy_src[i], d = a.copy_dst[i];
+        if (s < 0 || s >= a.num_blocks || d < 0 || d >= a.num_blocks || s == d) continue;
+        const int rows = a.copy_rows ? min(max(a.copy_rows[i], 0), a.bs) : a.bs;
+        const long long vecs = (long long)rows * a.row_vecs, first = (long long)(rest >> 1) * kPieceVecs + threadIdx.x;
+        uint4* cache = static_cast<uint4*>((rest & 1) ? a.v_cache : a.k_cache);
+        const uint4* from = cache + s * block_vecs;
+        uint4* to = cache + d * block_vecs;
+        uint4 x[kCopyVecs];
+#pragma unroll
+        for (int u = 0; u < kCopyVecs; ++u)
+            if (first + u * kCopyThreads < vecs) x[u] = from[first + u * kCopyThreads];
+#pragma unroll
+        for (int u = 0; u < kCopyVecs; ++u)
+            if (first + u * kCopyThreads < vecs) to[first + u * kCopyThreads] = x[u];
+    }
+}
+
+// Whether a cluster of eight CTAs of the kernel can be resident (a partitioned GPU may not have as
+// many SMs in one group); looked up once per device and host thread.
+template <typename K>
+bool cluster8_fits(K kernel, int& of_dev, bool& fits) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev != of_dev) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 8;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(8);
+        cfg.blockDim = dim3(kPlanThreads);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        fits = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+        of_dev = dev;
+    }
+    return fits;
+}
+
+// Threads for a row of the table, a CTA a row.
+unsigned row_threads(int max_blocks) {
+    unsigned t = 128;
+    while (t < kPlanThreads && static_cast<int>(4 * t) < max_blocks) t *= 2;
+    return t;
+}
+unsigned int_ctas(int n, int num_sms) {
+    const int c = (n + 1023) / 1024;
+    return static_cast<unsigned>(c < 1 ? 1 : c < num_sms ? c : num_sms);
+}
+
+// Block ids up to which one CTA scans them; beyond, a cluster of eight.
+constexpr int kOneCtaIds = 8192;
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const ForkArgs& a, int num_sms, cudaStream_t stream) {
+    const unsigned copiers = a.shares_out == a.shares ? 0u : int_ctas(a.num_blocks, num_sms);
+    cudaError_t e = launch_pdl(kv_fork_plan_kernel, dim3(1 + copiers), dim3(kPlanThreads), a.B * sizeof(int), stream, 1u, a);
+    if (e != cudaSuccess || a.F == 0) return e;
+    const int split = (a.max_blocks + 4 * kRowThreads - 1) / (4 * kRowThreads);
+    return launch_pdl(kv_fork_rows_kernel, dim3(static_cast<unsigned>(a.F), static_cast<unsigned>(split < 16 ? split : 16)), dim3(kRowThreads),
+                      0, stream, 1u, a);
+}
+
+cudaError_t launch_kv_release(const ReleaseArgs& a, int num_sms, cudaStream_t stream) {
+    thread_local int of_dev = -1;
+    thread_local bool fits = false;
+    cudaError_t e = cudaSuccess;
+    if (a.shares_out != a.shares)
+        e = launch_pdl(copy_ints_kernel, dim3(int_ctas(a.num_blocks, num_sms)), dim3(256), 0, stream, 1u, a.shares_out, a.shares, a.num_blocks);
+    if (e == cudaSuccess && a.B > 0)
+        e = launch_pdl(kv_release_count_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
+    if (e != cudaSuccess) return e;
+    if (a.num_blocks > kOneCtaIds && cluster8_fits(kv_release_push_kernel<8>, of_dev, fits))
+        return launch_pdl(kv_release_push_kernel<8>, dim3(8), dim3(kPlanThreads), 0, stream, 8u, a);
+    return launch_pdl(kv_release_push_kernel<1>, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
+}
+
+cudaError_t launch_kv_compact_blocks(const CompactBlocksArgs& a, int num_sms, cudaStream_t stream) {
+    thread_local int of_dev = -1;
+    thread_local bool fits = false;
+    cudaError_t e = launch_pdl(kv_compact_clear_kernel, dim3(int_ctas(a.num_blocks, num_sms)), dim3(256), 0, stream, 1u, a);
+    if (e == cudaSuccess && a.B > 0)
+        e = launch_pdl(kv_compact_mark_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
+    if (e != cudaSuccess) return e;
+    if (a.num_blocks > kOneCtaIds && cluster8_fits(kv_compact_plan_kernel<8>, of_dev, fits))
+        e = launch_pdl(kv_compact_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, stream, 8u, a);
+    else
+        e = launch_pdl(kv_compact_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
+    if (e != cudaSuccess || a.B == 0) return e;
+    return launch_pdl(kv_compact_rows_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
+}
+
+cudaError_t launch_kv_copy(const CopyArgs& a, int num_sms, cudaStream_t stream) {
+    const long long block_vecs = (long long)a.bs * a.row_vecs;
+    const int pieces = static_cast<int>((block_vecs + kPieceVecs - 1) / kPieceVecs);
+    const long long all = (long long)a.n * 2 * pieces, most = 8LL * num_sms;
+    return launch_pdl(kv_copy_kernel, dim3(static_cast<unsigned>(all < most ? all : most)), dim3(kCopyThreads), 0, stream, 1u, a, pieces);
+}
+
+}  // namespace tsv

@@ -1,0 +1,556 @@
+// prefix_attn.cu -- attention of one new token per sequence where groups of sequences share the first
+// keys of their caches: the shared keys are read once for all rows of the group.
+//
+//   s_t = scale * q . k_t over t in [0, P) of the group's first sequence and t in [P, L) of the
+//   sequence itself;  out = sum_t e^{s_t - m} v_t / l,  m = max s,  l = sum_t e^{s_t - m},  lse = m + ln l.
+//
+// A softmax over two runs of keys is the join of the two runs' (m, l, O): M = max m_i, O = sum e^{m_i - M}
+// O_i, l likewise.  So the prefix of a group, with the rows of all its sequences, and each sequence's own
+// keys, with its own rows, are items of one schedule, and the last kernel joins what the pieces of
+// both leave.
+//
+// Kernels: a plan (one CTA: checks, items, running sums of their tiles), the stream of tiles, the join.
+// Lengths stay on the device.  An item's units are (group of query rows, kv head); `team` warps take
+// neighbouring kv heads of the same rows and keys together.  The tiles of all units, item after item,
+// form one row that is divided evenly between `lanes` teams.  A segment that is a whole unit leaves its
+// (m, l, O) at its rows' places, a piece in one of its warp's two slots.
+#include <cuda_bf16.h>
+
+#include "../common.cuh"
+#include "continue_args.cuh"
+#include "decode_core.cuh"
+
+namespace tsv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's share fill an SM's shared memory
+constexpr int kMaxTeam = 8;
+constexpr int kScratch = 136;  // floats of a warp beside its ring
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxItems = 2 * kPagesMaxSeqs;
+
+// ------------------------------------------------------------------ plan
+
+// Tiles of an item: from the tile that holds its first key.
+template <int TILE>
+__device__ __forceinline__ int item_tiles(const int4& it) {
+    return it.z > it.y ? (it.z + TILE - 1) / TILE - it.y / TILE : 0;
+}
+// Units of an item, a team at a time.
+__device__ __forceinline__ int item_units(const PrefixArgs& a, const int4& it) {
+    return ((it.w + a.rows - 1) / a.rows) * (a.Hkv / a.team);
+}
+
+template <int TILE>
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
+    extern __shared__ int s_off[];  // [G + 1]
+    __shared__ long long s_warp[32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool wrong = false;
+    for (int g = tid; g <= a.G; g += kPlanThreads) {
+        const int x = a.group_offsets[g];
+        s_off[g] = x;
+        wrong |= x < 0 || x > a.B || (g == 0 && x != 0) || (g == a.G && x != a.B);
+    }
+    __syncthreads();
+    for (int g = tid; g < a.G; g += kPlanThreads) wrong |= s_off[g] > s_off[g + 1];
+    wrong = __syncthreads_or(wrong);
+    const long long cap = (long long)a.max_blocks << a.bs_log2;
+    const int n = a.G + a.B, per = (n + kPlanThreads - 1) / kPlanThreads;
+    long long mine = 0;
+    for (int u = 0; u < per; ++u) {
+        const int i = tid * per + u;
+        if (i >= n) break;
+        int4 it = make_int4(0, 0, 0, 0);
+        if (i < a.G) {
+            const int P = a.prefix_lens[i];
+            if (!wrong && s_off[i + 1] > s_off[i])
+                it = make_int4(s_off[i], 0, P > 0 && P <= cap ? P : 0, (s_off[i + 1] - s_off[i]) * a.gq);
+        } else {
+            const int b = i - a.G, L = a.seq_lens[b];
+            int g = 0, e = 0, P = 0;
+            if (wrong) {
+                e = TSV_DERR_SEQ;
+            } else {
+                // the last group that begins at or before b and is not empty
+                int lo = 0, hi = a.G;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_off[mid] <= b)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                g = lo;
+                P = a.prefix_lens[g];
+                if (L < 0 || L > cap || P < 0 || P > L) e = TSV_DERR_CAPACITY;
+            }
+            it = make_int4(b, e ? 0 : P, e ? 0 : L, a.gq);
+            a.group[b] = g;
+            a.seq_err[b] = e;
+        }
+        a.item[i] = it;
+        mine += (long long)item_tiles<TILE>(it) * item_units(a, it);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    long long w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    long long at = incl - mine + (warp ? before : 0);
+    for (int u = 0; u < per; ++u) {
+        const int i = tid * per + u;
+        if (i >= n) break;
+        a.start[i] = at;
+        const int4 it = a.item[i];  // (this thread's own)
+        at += (long long)item_tiles<TILE>(it) * item_units(a, it);
+        if (i == n - 1) a.start[n] = at;
+    }
+}
+
+// ------------------------------------------------------------------ the schedule
+
+// A position in the row of tiles: tile t of the `tiles` of the team's unit `unit` of item i.
+struct Place {
+    int i, unit, t, tiles, units;
+    int4 it;  // first sequence, first key, end, rows
+    template <int TILE>
+    __device__ __forceinline__ void set(const PrefixArgs& a, int item) {
+        i = item;
+        it = a.item[i];
+        tiles = item_tiles<TILE>(it);
+        units = item_units(a, it);
+    }
+    template <int TILE>
+    __device__ __forceinline__ void next(const PrefixArgs& a) {
+        if (++t < tiles) return;
+        t = 0;
+        if (++unit < units) return;
+        unit = 0;
+        do {
+            set<TILE>(a, i + 1);
+        } while (tiles * units == 0 && i + 1 < a.G + a.B);
+    }
+    __device__ __forceinline__ int chunk(const PrefixArgs& a) const { return unit / (a.Hkv / a.team); }
+    __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return unit % (a.Hkv / a.team) * a.team + member; }
+    __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk(a) * a.rows); }
+};
+
+// One warp: the position of tile x (x < start[n]).
+template <int TILE>
+__device__ __forceinline__ Place locate(const PrefixArgs& a, long long x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = a.G + a.B;  // the item lies in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) >> 5, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < len && a.start[at] <= x);
+        const int hit = 31 - __clz(below);  // start[lo] <= x
+        lo += hit * step;
+        len = min(step, len - hit * step);
+    }
+    Place p;
+    p.set<TILE>(a, lo);
+    const long long off = x - a.start[lo];
+    p.unit = static_cast<int>(off / p.tiles);
+    p.t = static_cast<int>(off - (long long)p.unit * p.tiles);
+    return p;
+}
+
+// ------------------------------------------------------------------ the stream of tiles
+
+template <typename Core>
+__host__ __device__ constexpr int stages_of() { return kRingBytes / (2 * Core::KEYS * Core::ROWB); }
+constexpr size_t kSmem = (size_t)kWarps * (kRingBytes + kScratch * sizeof(float));
+
+// A warp's stream of tiles: the copies run STAGES - 1 tiles ahead and the block ids one more.
+template <typename Core>
+struct Stream {
+    using Elem = typename Core::Elem;
+    static constexpr int D = Core::D, KEYS = Core::KEYS, STAGES = stages_of<Core>(), RUNS = KEYS / 8;
+    static constexpr uint32_t HALF = KEYS * Core::ROWB, STAGE = 2 * HALF;
+    static constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
+    const PrefixArgs& a;
+    const uint32_t ring;
+    const int member, row_elems, lrow, lane_elems, lch;
+    Place f;           // the tile whose ids were fetched last
+    int ids[RUNS];     // its blocks (8 keys lie in one block); all lanes hold the same
+    uint32_t bad = 0;  // stages holding a tile with a block id outside the cache
+    int left;          // tiles not yet on their way
+    int fill = 0, stage = 0;
+
+    __device__ __forceinline__ Stream(const PrefixArgs& args, uint32_t ring_, int member_, const Place& p, int n)
+        : a(args), ring(ring_), member(member_), row_elems(args.Hkv * D), lrow((threadIdx.x & 31) / LANES_ROW),
+          lane_elems(lrow * row_elems + ((threadIdx.x & 31) % LANES_ROW) * (16 / (int)sizeof(Elem))), lch((threadIdx.x & 31) % LANES_ROW),
+          f(p), left(n) {}
+
+    // the tile's first key; the item's first key may lie behind it
+    __device__ __forceinline__ static int first_key(const Place& p) { return (p.it.y / KEYS + p.t) * KEYS; }
+    __device__ __forceinline__ bool holds(int key) const { return key < f.it.z && key + 8 > f.it.y; }
+    __device__ __forceinline__ void fetch() {
+        const int32_t* bt = a.block_table + (long long)f.it.x * a.max_blocks;
+#pragma unroll
+        for (int u = 0; u < RUNS; ++u) {
+            const int key = first_key(f) + 8 * u;
+            ids[u] = holds(key) ? (TSV_IN_BOUNDS(key >> a.bs_log2, a.max_blocks, nullptr) ? bt[key >> a.bs_log2] : -1) : 0;
+        }
+    }
+    // sends tile f on its way into stage `fill`, then fetches the next tile's ids
+    __device__ __forceinline__ void load() {
+        if (left > 0) {
+            const uint32_t dst = ring + fill * STAGE;
+            const Elem* kc = static_cast<const Elem*>(a.k_cache);
+            const Elem* vc = static_cast<const Elem*>(a.v_cache);
+            const long long head = (long long)f.head(a, member) * D + lane_elems;
+            bool wrong = false;
+#pragma unroll
+            for (int u = 0; u < RUNS; ++u) {
+                const int key = first_key(f) + 8 * u;
+                const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
+                wrong |= !in && holds(key);
+                const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
+#pragma unroll
+                for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
+                    // rows outside the item's keys are zeros: they may hold anything, and 0 * NaN is NaN
+                    const int row = key + r0 + lrow;
+                    bool take = in && row >= f.it.y && row < f.it.z;
+                    const long long off = take ? at + (long long)r0 * row_elems : 0;
+                    // (an index check that fails is reported as a bad block)
+                    if (!TSV_IN_BOUNDS(off + 16 / (int)sizeof(Elem) - 1, ((long long)a.num_blocks << a.bs_log2) * row_elems, nullptr))
+                        wrong = true, take = false;
+                    cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
+                    cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
+                }
+            }
+            bad = (bad & ~(1u << fill)) | (wrong ? 1u << fill : 0u);
+            if (--left > 0) {
+                f.next<KEYS>(a);
+                fetch();
+            }
+        }
+        cp_commit();
+        if (++fill == STAGES) fill = 0;
+    }
+    __device__ __forceinline__ void begin() {
+        if (left > 0) fetch();
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) load();
+    }
+    // the next tile, p: waits for it, keeps the copies ahead, adds it to the core's state
+    __device__ __forceinline__ bool step(Core& core, const Place& p, float* scratch) {
+        cp_wait<STAGES - 2>();
+        __syncwarp();
+        load();
+        const uint32_t src = ring + stage * STAGE;
+        const bool wrong = ((bad >> stage) & 1u) != 0;
+        const int first = first_key(p);
+        core.step(src, src + HALF, p.it.y - first, p.it.z - first, a.scale_log2, scratch);
+        __syncwarp();
+        if (++stage == STAGES) stage = 0;
+        return wrong;
+    }
+};
+
+// Query rows from row `row` of the item on: row r is head r % gq (of the kv head) of its sequence r / gq.
+template <typename Elem, int D>
+struct ItemRows {
+    const Elem* q;  // the kv head's first row of the item's first sequence
+    int row, gq, seq;  // seq: elements from a sequence to the next
+    __device__ __forceinline__ const Elem* operator()(int r) const {
+        const int x = row + r, s = x / gq;
+        return q + (long long)s * seq + (x - s * gq) * D;
+    }
+};
+template <typename Core>
+__device__ __forceinline__ void load_rows(const PrefixArgs& a, const Place& p, int member, Core& core) {
+    using Elem = typename Core::Elem;
+    const Elem* q = static_cast<const Elem*>(a.q) + ((long long)p.it.x * a.Hq + p.head(a, member) * a.gq) * Core::D;
+    core.load_q(ItemRows<Elem, Core::D>{q, p.chunk(a) * a.rows, a.gq, a.Hq * Core::D}, p.rows(a));
+}
+
+// Where the rows of a whole unit go: each to its own place.
+template <int D>
+struct ToPlaces {
+    float *o, *m, *l;
+    int row, gq, Hq;
+    long long first;  // the place of the item's row 0
+    __device__ __forceinline__ long long place(int r) const {
+        const int x = row + r, s = x / gq;
+        return first + (long long)s * Hq + (x - s * gq);
+    }
+    __device__ __forceinline__ void row_(int r, float m_, float l_) const {
+        m[place(r)] = m_;
+        l[place(r)] = l_;
+    }
+};
+template <int D>
+struct Leave {
+    ToPlaces<D> whole;
+    ToSlot<D> slot;
+    bool in_slot;
+    __device__ __forceinline__ void row(int r, float m, float l) const {
+        if (in_slot)
+            slot.row(r, m, l);
+        else
+            whole.row_(r, m, l);
+    }
+    __device__ __forceinline__ float factor(float) const { return 1.0f; }
+    __device__ __forceinline__ void two(int r, int d, float x, float y) const {
+        float* o = in_slot ? slot.o + r * D : whole.o + whole.place(r) * D;
+        *reinterpret_cast<float2*>(o + d) = make_float2(x, y);
+    }
+};
+
+template <typename Core>
+__global__ void __launch_bounds__(kThreads, 2) prefix_stream_kernel(const __grid_constant__ PrefixArgs a) {
+    constexpr int D = Core::D, KEYS = Core::KEYS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
+    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int me = blockIdx.x * kWarps + warp, which = me / a.team, member = me % a.team;
+    const long long T = a.start[a.G + a.B];
+    const int lanes = lanes_of(T, a.lanes);
+    if (which >= lanes || T == 0) return;
+    const long long x = lane_start(which, T, lanes), x_end = lane_start(which + 1, T, lanes);
+    const int n = static_cast<int>(x_end - x);
+    if (n <= 0) return;
+    Place p = locate<KEYS>(a, x);
+    Stream<Core> stream(a, ring, member, p, n);
+    stream.begin();
+    Core core;
+    load_rows(a, p, member, core);
+    core.reset();
+    bool seg_bad = false;
+    int seg = 0, t_first = p.t;
+    for (int i = 0; i < n; ++i) {
+        seg_bad |= stream.step(core, p, scratch);
+        if (p.t + 1 < p.tiles && i + 1 < n) {
+            ++p.t;
+            continue;
+        }
+        // the segment's end
+        const bool prefix = p.i < a.G, piece = t_first > 0 || p.t + 1 < p.tiles;
+        const long long rows = (long long)a.B * a.Hq, slot = 2LL * me + (seg == 0 ? 0 : 1);
+        const int row0 = p.chunk(a) * a.rows;
+        if (!TSV_IN_BOUNDS(slot, 2LL * a.lanes * a.team, a.seq_err + p.it.x)) return;
+        const Leave<D> to{
+            {a.whole_o, a.whole_m, a.whole_l, row0, a.gq, a.Hq, (prefix ? 0 : rows) + (long long)p.it.x * a.Hq + p.head(a, member) * a.gq},
+            {a.part_o + slot * a.rows * D, a.part_m + slot * a.rows, a.part_l + slot * a.rows},
+            piece};
+        core.finish(p.rows(a), to, scratch);
+        if (seg_bad)  // the sequences of the unit's rows are told
+            for (int s = row0 / a.gq + lane; s <= (row0 + p.rows(a) - 1) / a.gq; s += 32) atomicOr(a.seq_err + p.it.x + s, TSV_DERR_BLOCK);
+        if (i + 1 < n) {
+            p.next<KEYS>(a);
+            t_first = 0;
+            seg_bad = false;
+            ++seg;
+            load_rows(a, p, member, core);
+            core.reset();
+        }
+    }
+}
+
+// ------------------------------------------------------------------ join
+
+// Where the pieces of one row of an item lie.
+struct Pieces {
+    int n = 0;          // pieces
+    long long at = 0;   // row of the first piece, in the whole units' places or in the slots
+    long long next = 0; // row of the second piece; the others follow at `step`
+    long long step = 0;
+    bool whole = false;
+};
+template <int TILE>
+__device__ __forceinline__ Pieces find_pieces(const PrefixArgs& a, int i, int b, int kvh, int j, long long T, int lanes) {
+    Pieces p;
+    const int4 it = a.item[i];
+    const int tiles = item_tiles<TILE>(it);
+    if (tiles == 0 || it.w == 0) return p;
+    const int x = (b - it.x) * a.gq + j, chunk = x / a.rows, member = kvh % a.team;
+    const long long first = a.start[i] + ((long long)chunk * (a.Hkv / a.team) + kvh / a.team) * tiles;
+    const int c0 = lane_of_tile(first, T, lanes), c1 = lane_of_tile(first + tiles - 1, T, lanes);
+    p.n = c1 - c0 + 1;
+    p.whole = c0 == c1;
+    if (p.whole) {
+        p.at = (i < a.G ? 0 : (long long)a.B * a.Hq) + (long long)b * a.Hq + kvh * a.gq + j;
+    } else {
+        const int r = x - chunk * a.rows;
+        p.step = 2LL * a.team * a.rows;
+        // the piece is the lane's first segment if the lane starts with the unit
+        p.at = (2LL * (c0 * a.team + member) + (lane_start(c0, T, lanes) == first ? 0 : 1)) * a.rows + r;
+        p.next = 2LL * ((c0 + 1) * a.team + member) * a.rows + r;
+    }
+    return p;
+}
+
+// One CTA: kJoinRows query rows of a (sequence, kv head), kJoinGroups threads to four output elements,
+// each with kJoinAhead pieces in flight.  The pieces are joined in a fixed order.
+constexpr int kJoinGroups = 4, kJoinRows = 2, kJoinAhead = 4;
+
+template <typename Elem, int D, int TILE>
+__global__ void __launch_bounds__(kJoinGroups* kJoinRows* D / 4) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+    constexpr int VEC = D / 4, EL = kJoinRows * VEC;
+    __shared__ float s_part[kJoinGroups - 1][EL][6];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
+    const int e = threadIdx.x % EL, grp = threadIdx.x / EL, d = (e % VEC) * 4, j = blockIdx.y * kJoinRows + e / VEC;
+    const long long T = a.start[a.G + a.B];
+    const int lanes = lanes_of(T, a.lanes), err = a.seq_err[b];
+    float M = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (err == 0 && j < a.gq && T > 0) {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const Pieces p = find_pieces<TILE>(a, part == 0 ? a.group[b] : a.G + b, b, kvh, j, T, lanes);
+            const float *pm = p.whole ? a.whole_m : a.part_m, *pl = p.whole ? a.whole_l : a.part_l, *po = p.whole ? a.whole_o : a.part_o;
+            for (int c = grp * kJoinAhead; c < p.n; c += kJoinAhead * kJoinGroups) {
+                float m[kJoinAhead], l[kJoinAhead];
+                float4 o[kJoinAhead];
+#pragma unroll
+                for (int i = 0; i < kJoinAhead; ++i) {
+                    m[i] = -INFINITY;
+                    l[i] = 0.0f;
+                    o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (c + i < p.n) {
+                        const long long row = c + i == 0 ? p.at : p.next + (c + i - 1) * p.step;
+                        if (!TSV_IN_BOUNDS(row, p.whole ? 2LL * a.B * a.Hq : 2LL * a.lanes * a.team * a.rows, a.seq_err + b)) continue;
+                        m[i] = pm[row];
+                        l[i] = pl[row];
+                        o[i] = *reinterpret_cast<const float4*>(po + row * D + d);
+                    }
+                }
+                float m_new = M;
+#pragma unroll
+                for (int i = 0; i < kJoinAhead; ++i) m_new = fmaxf(m_new, m[i]);
+                const float ms = safe_max(m_new), f0 = ex2(M - ms);
+                M = m_new;
+                sum *= f0;
+                acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+                for (int i = 0; i < kJoinAhead; ++i) {
+                    const float f = ex2(m[i] - ms);
+                    sum = fmaf(f, l[i], sum);
+                    acc = make_float4(fmaf(f, o[i].x, acc.x), fmaf(f, o[i].y, acc.y), fmaf(f, o[i].z, acc.z), fmaf(f, o[i].w, acc.w));
+                }
+            }
+        }
+    }
+    if (grp > 0) {
+        float* s = s_part[grp - 1][e];
+        s[0] = M;
+        s[1] = sum;
+        s[2] = acc.x;
+        s[3] = acc.y;
+        s[4] = acc.z;
+        s[5] = acc.w;
+    }
+    __syncthreads();
+    if (grp > 0 || j >= a.gq) return;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups - 1; ++i) {
+        const float* s = s_part[i][e];
+        const float m_new = fmaxf(M, s[0]), ms = safe_max(m_new);
+        const float f0 = ex2(M - ms), f1 = ex2(s[0] - ms);
+        M = m_new;
+        sum = sum * f0 + s[1] * f1;
+        acc = make_float4(acc.x * f0 + s[2] * f1, acc.y * f0 + s[3] * f1, acc.z * f0 + s[4] * f1, acc.w * f0 + s[5] * f1);
+    }
+    const long long h = (long long)b * a.Hq + kvh * a.gq + j;
+    const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, err != 0};
+    // no keys at all: zeros (and an lse of -infinity)
+    const float inv = err == 0 && a.seq_lens[b] == 0 ? 0.0f : to.factor(sum);
+    to.two(0, d, acc.x * inv, acc.y * inv);
+    to.two(0, d + 2, acc.z * inv, acc.w * inv);
+    if (d == 0) to.row(0, M, sum);
+}
+
+template <typename Core>
+cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
+    using Elem = typename Core::Elem;
+    thread_local int smem_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev != smem_dev) {
+        e = cudaFuncSetAttribute(prefix_stream_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        if (e != cudaSuccess) return e;
+        smem_dev = dev;
+    }
+    e = launch_pdl(prefix_plan_kernel<Core::KEYS>, dim3(1), dim3(kPlanThreads), (a.G + 1) * sizeof(int), stream, 1u, a);
+    if (e != cudaSuccess) return e;
+    const int warps = a.lanes * a.team;
+    e = launch_pdl(prefix_stream_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), kSmem, stream, 1u, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefix_join_kernel<Elem, Core::D, Core::KEYS>,
+                      dim3(static_cast<unsigned>(a.B * a.Hkv), static_cast<unsigned>((a.gq + kJoinRows - 1) / kJoinRows)),
+                      dim3(kJoinGroups * kJoinRows * Core::D / 4), 0, stream, 1u, a);
+}
+
+template <int D>
+cudaError_t launch_dim(const PrefixArgs& a, bool bf16, cudaStream_t stream) {
+    if (bf16) return a.rows <= 16 ? launch_core<Bf16Core<D, 1>>(a, stream) : launch_core<Bf16Core<D, 2>>(a, stream);
+    return a.rows <= 4 ? launch_core<F32Core<D, 4>>(a, stream) : launch_core<F32Core<D, 8>>(a, stream);
+}
+
+size_t aligned(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks, bool bf16, int num_sms) {
+    PrefixPlan p{};
+    const int gq = Hq / Hkv;
+    // a unit's rows: one or two 16-row fragments (bf16), 4 or 8 (fp32)
+    const long long rows = (long long)B * gq;
+    p.rows = bf16 ? (rows <= 16 ? 16 : 32) : (rows <= 4 ? 4 : 8);
+    p.team = 1;
+    for (int t = 2; t <= kMaxTeam; ++t)
+        if (Hkv % t == 0) p.team = t;
+    // eight warps an SM, as many as the shared memory takes; never more than share the most tiles
+    // that the tables can hold
+    const int tile = tile_keys(bf16, D);
+    const long long cap_tiles = ((long long)max_blocks * block_size + tile - 1) / tile + 1;
+    const long long units = (rows / p.rows + G) + (long long)B * ((gq + p.rows - 1) / p.rows);
+    long long lanes = 2LL * kWarps * num_sms / p.team;
+    p.lanes = lanes_of(units * (Hkv / p.team) * cap_tiles, static_cast<int>(lanes < 1 ? 1 : lanes));
+    const size_t slots = 2 * (size_t)p.lanes * p.team * p.rows, whole = 2 * (size_t)B * Hq;
+    size_t at = aligned(((size_t)G + B + 1) * sizeof(long long));
+    auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += aligned(bytes);
+        return o;
+    };
+    p.item = take(((size_t)G + B) * sizeof(int4));
+    p.group = take((size_t)B * sizeof(int));
+    p.part_o = take(slots * D * sizeof(float));
+    p.part_m = take(slots * sizeof(float));
+    p.part_l = take(slots * sizeof(float));
+    p.whole_o = take(whole * D * sizeof(float));
+    p.whole_m = take(whole * sizeof(float));
+    p.whole_l = take(whole * sizeof(float));
+    p.ws_bytes = at;
+    return p;
+}
+
+cudaError_t launch_prefix_attn(const PrefixArgs& a, bool bf16, cudaStream_t stream) {
+    return a.D == 64 ? launch_dim<64>(a, bf16, stream) : launch_dim<128>(a, bf16, stream);
+}
+
+}  // namespace tsv

@@ -519,7 +519,8 @@ tsv_status tsv_kv_copy_blocks(void *k_cache, void *v_cache, const int32_t *copy_
  * > max_blocks * block_size, P_g < 0 or > L_b), TSV_DERR_BLOCK (a block id that covers one of the sequence's keys,
  * the shared ones included, outside [0, num_blocks)); rows of a flagged sequence are NaN.
  * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128]; B and G up to 8192;
- * max_blocks * block_size up to 2^30, B * Hq up to 2^24; scale > 0, scale * log2(e) finite.
+ * max_blocks * block_size and num_blocks * block_size up to 2^30, B * Hq up to 2^24; scale > 0, scale * log2(e)
+ * finite.
  * ------------------------------------------------------------------------- */
 size_t tsv_prefix_decode_attn_workspace_size(int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks,
                                              tsv_dtype dtype);

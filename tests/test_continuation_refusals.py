@@ -92,7 +92,7 @@ def _prefix(lib, q=A, kc=A, vc=A, bt=A, sl=A, off=A, pre=A, out=A, lse=P, B=2, G
 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), 1), (dict(G=-1), 1), (dict(G=0), 1), (dict(B=8193), 2), (dict(G=8193), 2), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=9), 1),
-    (dict(B=8192, Hq=4096), 2), (dict(D=96), 2), (dict(bs=48), 2), (dict(mb=0), 1), (dict(nb=0), 1), (dict(mb=1 << 27), 2), (dict(dt=2), 1),
+    (dict(B=8192, Hq=4096), 2), (dict(nb=(1 << 26) + 1), 2), (dict(D=96), 2), (dict(bs=48), 2), (dict(mb=0), 1), (dict(nb=0), 1), (dict(mb=1 << 27), 2), (dict(dt=2), 1),
     (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=3e38), 1),
     (dict(q=M), 1), (dict(out=M), 1), (dict(kc=M), 1), (dict(vc=M), 1), (dict(q=P), 1), (dict(bt=P), 1), (dict(sl=P), 1), (dict(off=P), 1),
     (dict(pre=P), 1), (dict(out=P), 1), (dict(err=P), 1), (dict(ws=P), 1), (dict(wsb=16), 1), (dict(ws=M), 1)])

@@ -28,6 +28,8 @@ tsv_status check_prefix_shapes(int B, int G, int Hq, int Hkv, int D, int block_s
         return report_error(TSV_ERR_UNSUPPORTED, "B=%d or G=%d exceeds %d", B, G, tsv::kPagesMaxSeqs);
     if (B > 0 && G == 0) return report_error(TSV_ERR_ARG, "%d sequences in no group", B);
     if ((long long)max_blocks * block_size > (1LL << 30)) return report_error(TSV_ERR_UNSUPPORTED, "a table row covers more than 2^30 slots");
+    // (rows of the cache are 32-bit coordinates of its tensor map)
+    if ((long long)num_blocks * block_size > (1LL << 30)) return report_error(TSV_ERR_UNSUPPORTED, "the cache has more than 2^30 slots");
     if ((long long)B * Hq > (1LL << 24)) return report_error(TSV_ERR_UNSUPPORTED, "B * Hq exceeds 2^24 query rows");
     return check_row(Hq, D);
 }
@@ -205,6 +207,11 @@ tsv_status tsv_prefix_decode_attn(const void* q, const void* k_cache, const void
     a.whole_o = reinterpret_cast<float*>(ws + p.whole_o);
     a.whole_m = reinterpret_cast<float*>(ws + p.whole_m);
     a.whole_l = reinterpret_cast<float*>(ws + p.whole_l);
+    a.tc_start = reinterpret_cast<long long*>(ws + p.tc_start);
+    a.tc_o = reinterpret_cast<float*>(ws + p.tc_o);
+    a.tc_m = reinterpret_cast<float*>(ws + p.tc_m);
+    a.tc_l = reinterpret_cast<float*>(ws + p.tc_l);
+    a.tc_lanes = p.tc_lanes;
     a.B = B;
     a.G = G;
     a.Hq = Hq;

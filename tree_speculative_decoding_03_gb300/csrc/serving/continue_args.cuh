@@ -77,13 +77,17 @@ struct CopyArgs {
 };
 cudaError_t launch_kv_copy(const CopyArgs& a, int num_sms, cudaStream_t stream);
 
+constexpr int kPrefixTcKeys = 128;  // keys of a tile of the tensor-core kernel
+constexpr int kPrefixTcRows = 256;  // query rows of a unit there
+
 // Attention over shared prefixes.  Plan: a deterministic function of the shapes and the SM count.
 struct PrefixPlan {
     int rows;   // query rows of a unit
     int team;   // warps that go through the same keys, each with a kv head of its own
     int lanes;  // teams the key tiles are divided between
+    int tc_lanes;  // CTAs that the prefixes' tiles are divided between on the tensor cores (0: not there)
     // byte offsets of the workspace's parts, and its size
-    size_t item, group, part_o, part_m, part_l, whole_o, whole_m, whole_l, ws_bytes;
+    size_t item, group, part_o, part_m, part_l, whole_o, whole_m, whole_l, tc_start, tc_o, tc_m, tc_l, ws_bytes;
 };
 PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks, bool bf16, int num_sms);
 
@@ -106,13 +110,18 @@ struct PrefixArgs {
     float* part_o;     // [2 * warps][rows][D]: pieces of units, two slots a warp (warp = lane * team + member)
     float* part_m;
     float* part_l;
-    float* whole_o;  // [2][B * Hq][D]: units in one piece, those of prefixes first
+    float* whole_o;  // [3][B * Hq][D]: units in one piece: prefixes, the sequences' own keys, prefixes' odd tiles
     float* whole_m;
     float* whole_l;
-    int B, G, Hq, Hkv, D, gq, rows, team, lanes;  // gq = Hq / Hkv
+    long long* tc_start;  // [G + 1]: running sums of the prefixes' tiles on the tensor cores
+    float* tc_o;          // [4 * tc_lanes][128][D]: pieces there; a CTA's first and last unit, two streams each
+    float* tc_m;
+    float* tc_l;
+    int B, G, Hq, Hkv, D, gq, rows, team, lanes, tc_lanes;  // gq = Hq / Hkv
     int bs_log2, max_blocks, num_blocks;
     float scale_log2;  // scale * log2(e)
 };
+cudaError_t launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attn(const PrefixArgs& a, bool bf16, cudaStream_t stream);
 
 constexpr int kMaxTop = 32;  // alternatives of a row

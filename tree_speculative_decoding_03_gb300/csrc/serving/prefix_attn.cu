@@ -9,8 +9,8 @@
 // keys, with its own rows, are items of one schedule, and the last kernel joins what the pieces of
 // both leave.
 //
-// Kernels: a plan (one CTA: checks, items, running sums of their tiles), the stream of tiles, the join.
-// Lengths stay on the device.  An item's units are (group of query rows, kv head); `team` warps take
+// Kernels: a plan (one CTA: checks, items, running sums of their tiles), for bf16 the prefixes on the tensor
+// cores (prefix_tc.cu), the stream of the other tiles, the join.  Lengths stay on the device.  An item's units are (group of query rows, kv head); `team` warps take
 // neighbouring kv heads of the same rows and keys together.  The tiles of all units, item after item,
 // form one row that is divided evenly between `lanes` teams.  A segment that is a whole unit leaves its
 // (m, l, O) at its rows' places, a piece in one of its warp's two slots.
@@ -29,7 +29,6 @@ constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's sha
 constexpr int kMaxTeam = 8;
 constexpr int kScratch = 136;  // floats of a warp beside its ring
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanMaxItems = 2 * kPagesMaxSeqs;
 
 // ------------------------------------------------------------------ plan
 
@@ -38,18 +37,43 @@ template <int TILE>
 __device__ __forceinline__ int item_tiles(const int4& it) {
     return it.z > it.y ? (it.z + TILE - 1) / TILE - it.y / TILE : 0;
 }
-// Units of an item, a team at a time.
-__device__ __forceinline__ int item_units(const PrefixArgs& a, const int4& it) {
-    return ((it.w + a.rows - 1) / a.rows) * (a.Hkv / a.team);
+// Units of item i, a team at a time; those of the tensor cores are not in the stream.
+__device__ __forceinline__ int item_units(const PrefixArgs& a, int i, const int4& it) {
+    return i < a.G && a.tc_lanes > 0 ? 0 : ((it.w + a.rows - 1) / a.rows) * (a.Hkv / a.team);
+}
+// Tiles of a prefix on the tensor cores, over all its units.
+__device__ __forceinline__ long long tc_tiles(const PrefixArgs& a, const int4& it) {
+    return (long long)((it.z + kPrefixTcKeys - 1) / kPrefixTcKeys) * ((it.w + kPrefixTcRows - 1) / kPrefixTcRows) * a.Hkv;
+}
+
+// The sum over the block's threads before this one.
+__device__ __forceinline__ long long block_before(long long mine, long long* s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    long long w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return incl - mine + (warp ? before : 0);
 }
 
 template <int TILE>
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ int s_off[];  // [G + 1]
-    __shared__ long long s_warp[32];
+    __shared__ long long s_warp[32], s_tc_warp[32];
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     bool wrong = false;
     for (int g = tid; g <= a.G; g += kPlanThreads) {
         const int x = a.group_offsets[g];
@@ -61,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     wrong = __syncthreads_or(wrong);
     const long long cap = (long long)a.max_blocks << a.bs_log2;
     const int n = a.G + a.B, per = (n + kPlanThreads - 1) / kPlanThreads;
-    long long mine = 0;
+    long long mine = 0, tc_mine = 0;
     for (int u = 0; u < per; ++u) {
         const int i = tid * per + u;
         if (i >= n) break;
@@ -94,31 +118,19 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             a.seq_err[b] = e;
         }
         a.item[i] = it;
-        mine += (long long)item_tiles<TILE>(it) * item_units(a, it);
+        mine += (long long)item_tiles<TILE>(it) * item_units(a, i, it);
+        if (i < a.G) tc_mine += tc_tiles(a, it);
     }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    long long w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-    }
-    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    long long at = incl - mine + (warp ? before : 0);
+    long long at = block_before(mine, s_warp), tc_at = block_before(tc_mine, s_tc_warp);
     for (int u = 0; u < per; ++u) {
         const int i = tid * per + u;
         if (i >= n) break;
         a.start[i] = at;
         const int4 it = a.item[i];  // (this thread's own)
-        at += (long long)item_tiles<TILE>(it) * item_units(a, it);
+        at += (long long)item_tiles<TILE>(it) * item_units(a, i, it);
         if (i == n - 1) a.start[n] = at;
+        if (i <= a.G) a.tc_start[i] = tc_at;
+        if (i < a.G) tc_at += tc_tiles(a, it);
     }
 }
 
@@ -133,7 +145,7 @@ struct Place {
         i = item;
         it = a.item[i];
         tiles = item_tiles<TILE>(it);
-        units = item_units(a, it);
+        units = item_units(a, i, it);
     }
     template <int TILE>
     __device__ __forceinline__ void next(const PrefixArgs& a) {
@@ -162,7 +174,7 @@ __device__ __forceinline__ Place locate(const PrefixArgs& a, long long x) {
         lo += hit * step;
         len = min(step, len - hit * step);
     }
-    Place p;
+    Place p{};
     p.set<TILE>(a, lo);
     const long long off = x - a.start[lo];
     p.unit = static_cast<int>(off / p.tiles);
@@ -314,15 +326,11 @@ struct Leave {
     }
 };
 
+// One warp: its tiles.
 template <typename Core>
-__global__ void __launch_bounds__(kThreads, 2) prefix_stream_kernel(const __grid_constant__ PrefixArgs a) {
+__device__ __forceinline__ void stream_tiles(const PrefixArgs& a, uint32_t ring, float* scratch) {
     constexpr int D = Core::D, KEYS = Core::KEYS;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
-    pdl_wait();
-    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int me = blockIdx.x * kWarps + warp, which = me / a.team, member = me % a.team;
     const long long T = a.start[a.G + a.B];
     const int lanes = lanes_of(T, a.lanes);
@@ -367,6 +375,20 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_stream_kernel(const __grid
     }
 }
 
+template <typename Core>
+__global__ void __launch_bounds__(kThreads, 2) prefix_stream_kernel(const __grid_constant__ PrefixArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5;
+    float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
+    // After the tensor-core kernel this one starts as that one's CTAs end: it needs only the plan, which that
+    // kernel had waited for before it let this one start, and waits for that kernel itself at its end (so
+    // that the join, which waits for this one, has both).
+    if (a.tc_lanes == 0) pdl_wait();
+    pdl_launch_dependents();
+    stream_tiles<Core>(a, smem_u32(smem) + warp * kRingBytes, scratch);
+    if (a.tc_lanes > 0) pdl_wait();
+}
+
 // ------------------------------------------------------------------ join
 
 // Where the pieces of one row of an item lie.
@@ -375,8 +397,15 @@ struct Pieces {
     long long at = 0;   // row of the first piece, in the whole units' places or in the slots
     long long next = 0; // row of the second piece; the others follow at `step`
     long long step = 0;
-    bool whole = false;
+    const float *o, *m, *l;  // the array they lie in, and its rows
+    long long rows = 0;
 };
+__device__ __forceinline__ void in_places(const PrefixArgs& a, Pieces& p) {
+    p.o = a.whole_o;
+    p.m = a.whole_m;
+    p.l = a.whole_l;
+    p.rows = 3LL * a.B * a.Hq;
+}
 template <int TILE>
 __device__ __forceinline__ Pieces find_pieces(const PrefixArgs& a, int i, int b, int kvh, int j, long long T, int lanes) {
     Pieces p;
@@ -387,8 +416,8 @@ __device__ __forceinline__ Pieces find_pieces(const PrefixArgs& a, int i, int b,
     const long long first = a.start[i] + ((long long)chunk * (a.Hkv / a.team) + kvh / a.team) * tiles;
     const int c0 = lane_of_tile(first, T, lanes), c1 = lane_of_tile(first + tiles - 1, T, lanes);
     p.n = c1 - c0 + 1;
-    p.whole = c0 == c1;
-    if (p.whole) {
+    if (c0 == c1) {
+        in_places(a, p);
         p.at = (i < a.G ? 0 : (long long)a.B * a.Hq) + (long long)b * a.Hq + kvh * a.gq + j;
     } else {
         const int r = x - chunk * a.rows;
@@ -396,6 +425,40 @@ __device__ __forceinline__ Pieces find_pieces(const PrefixArgs& a, int i, int b,
         // the piece is the lane's first segment if the lane starts with the unit
         p.at = (2LL * (c0 * a.team + member) + (lane_start(c0, T, lanes) == first ? 0 : 1)) * a.rows + r;
         p.next = 2LL * ((c0 + 1) * a.team + member) * a.rows + r;
+        p.o = a.part_o;
+        p.m = a.part_m;
+        p.l = a.part_l;
+        p.rows = 2LL * a.lanes * a.team * a.rows;
+    }
+    return p;
+}
+// The pieces of a prefix's row that the tensor-core kernel leaves.  Units of up to 128 rows have two from
+// each CTA, one of every other tile; the odd ones are a search of their own (`odd`).
+__device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int b, int kvh, int j, bool odd) {
+    Pieces p;
+    const int4 it = a.item[g];
+    const int tiles = (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys, groups = (it.w + kPrefixTcRows - 1) / kPrefixTcRows;
+    if (tiles == 0 || it.w == 0) return p;
+    const long long T = a.tc_start[a.G];
+    const int lanes = static_cast<int>(min(T, (long long)a.tc_lanes));
+    const int x = (b - it.x) * a.gq + j, grp = x / kPrefixTcRows, r = x - grp * kPrefixTcRows;
+    const bool by_tile = it.w - grp * kPrefixTcRows <= 128;
+    if (odd && !by_tile) return p;
+    const long long first = a.tc_start[g] + ((long long)kvh * groups + grp) * tiles;
+    const int c0 = lane_of_tile(first, T, lanes), c1 = lane_of_tile(first + tiles - 1, T, lanes);
+    p.n = c1 - c0 + 1;
+    if (c0 == c1) {
+        in_places(a, p);
+        p.at = (odd ? 2LL * a.B * a.Hq : 0LL) + (long long)b * a.Hq + kvh * a.gq + j;
+    } else {
+        const int half = by_tile ? (odd ? 1 : 0) : r >> 7, rl = r & 127;
+        p.step = 4 * 128;
+        p.at = (4LL * c0 + (lane_start(c0, T, lanes) == first ? 0 : 2) + half) * 128 + rl;
+        p.next = (4LL * (c0 + 1) + half) * 128 + rl;
+        p.o = a.tc_o;
+        p.m = a.tc_m;
+        p.l = a.tc_l;
+        p.rows = 512LL * a.tc_lanes;
     }
     return p;
 }
@@ -416,11 +479,13 @@ __global__ void __launch_bounds__(kJoinGroups* kJoinRows* D / 4) prefix_join_ker
     const int lanes = lanes_of(T, a.lanes), err = a.seq_err[b];
     float M = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (err == 0 && j < a.gq && T > 0) {
+    if (err == 0 && j < a.gq) {
+        const int g = a.group[b];
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-            const Pieces p = find_pieces<TILE>(a, part == 0 ? a.group[b] : a.G + b, b, kvh, j, T, lanes);
-            const float *pm = p.whole ? a.whole_m : a.part_m, *pl = p.whole ? a.whole_l : a.part_l, *po = p.whole ? a.whole_o : a.part_o;
+        for (int part = 0; part < (a.tc_lanes > 0 ? 3 : 2); ++part) {
+            const Pieces p = part == 0 ? find_pieces<TILE>(a, a.G + b, b, kvh, j, T, lanes)
+                             : a.tc_lanes > 0 ? find_tc_pieces(a, g, b, kvh, j, part == 2)
+                                              : find_pieces<TILE>(a, g, b, kvh, j, T, lanes);
             for (int c = grp * kJoinAhead; c < p.n; c += kJoinAhead * kJoinGroups) {
                 float m[kJoinAhead], l[kJoinAhead];
                 float4 o[kJoinAhead];
@@ -431,10 +496,12 @@ __global__ void __launch_bounds__(kJoinGroups* kJoinRows* D / 4) prefix_join_ker
                     o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (c + i < p.n) {
                         const long long row = c + i == 0 ? p.at : p.next + (c + i - 1) * p.step;
-                        if (!TSV_IN_BOUNDS(row, p.whole ? 2LL * a.B * a.Hq : 2LL * a.lanes * a.team * a.rows, a.seq_err + b)) continue;
-                        m[i] = pm[row];
-                        l[i] = pl[row];
-                        o[i] = *reinterpret_cast<const float4*>(po + row * D + d);
+                        if (!TSV_IN_BOUNDS(row, p.rows, a.seq_err + b)) continue;
+                        m[i] = p.m[row];
+                        l[i] = p.l[row];
+                        // (a piece without tiles, l = 0, leaves no O)
+                        const float4 x = *reinterpret_cast<const float4*>(p.o + row * D + d);
+                        if (l[i] != 0.0f) o[i] = x;
                     }
                 }
                 float m_new = M;
@@ -496,6 +563,8 @@ cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
     }
     e = launch_pdl(prefix_plan_kernel<Core::KEYS>, dim3(1), dim3(kPlanThreads), (a.G + 1) * sizeof(int), stream, 1u, a);
     if (e != cudaSuccess) return e;
+    if (a.tc_lanes > 0) e = launch_prefix_tc(a, stream);
+    if (e != cudaSuccess) return e;
     const int warps = a.lanes * a.team;
     e = launch_pdl(prefix_stream_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), kSmem, stream, 1u, a);
     if (e != cudaSuccess) return e;
@@ -518,8 +587,10 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     PrefixPlan p{};
     const int gq = Hq / Hkv;
     // a unit's rows: one or two 16-row fragments (bf16), 4 or 8 (fp32)
+    // (the prefixes of a bf16 call are units of 256 rows on the tensor cores)
+    p.tc_lanes = bf16 ? num_sms : 0;
     const long long rows = (long long)B * gq;
-    p.rows = bf16 ? (rows <= 16 ? 16 : 32) : (rows <= 4 ? 4 : 8);
+    p.rows = bf16 ? (gq <= 16 ? 16 : 32) : (rows <= 4 ? 4 : 8);
     p.team = 1;
     for (int t = 2; t <= kMaxTeam; ++t)
         if (Hkv % t == 0) p.team = t;
@@ -530,7 +601,7 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     const long long units = (rows / p.rows + G) + (long long)B * ((gq + p.rows - 1) / p.rows);
     long long lanes = 2LL * kWarps * num_sms / p.team;
     p.lanes = lanes_of(units * (Hkv / p.team) * cap_tiles, static_cast<int>(lanes < 1 ? 1 : lanes));
-    const size_t slots = 2 * (size_t)p.lanes * p.team * p.rows, whole = 2 * (size_t)B * Hq;
+    const size_t slots = 2 * (size_t)p.lanes * p.team * p.rows, whole = 3 * (size_t)B * Hq;
     size_t at = aligned(((size_t)G + B + 1) * sizeof(long long));
     auto take = [&at](size_t bytes) {
         const size_t o = at;
@@ -545,6 +616,10 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     p.whole_o = take(whole * D * sizeof(float));
     p.whole_m = take(whole * sizeof(float));
     p.whole_l = take(whole * sizeof(float));
+    p.tc_start = take(((size_t)G + 1) * sizeof(long long));
+    p.tc_o = take((size_t)p.tc_lanes * 512 * D * sizeof(float));
+    p.tc_m = take((size_t)p.tc_lanes * 512 * sizeof(float));
+    p.tc_l = take((size_t)p.tc_lanes * 512 * sizeof(float));
     p.ws_bytes = at;
     return p;
 }

@@ -1,0 +1,550 @@
+// prefix_tc.cu -- the shared prefixes of prefix_attn.cu on the 5th-generation tensor cores (tcgen05,
+// accumulators in TMEM, K/V tiles by TMA), bf16.
+//
+// The rows of a group and kv head -- the group's sequences times the heads of the kv head -- against the
+// group's P keys are a dense product: 4 R P D multiply-adds on 4 P D bytes, so from some 300 rows on the
+// tensor cores are the bound, and below the cache's bytes.
+//
+// Work split: a unit is (group, kv head, 256 rows).  Its keys are cut into 128-key tiles, the tiles of
+// all units form one row, divided evenly between persistent CTAs.  A CTA's segment of a unit ends in
+// (m, l, O) of its rows, at the rows' own places if it is the whole unit, else in a slot of the CTA; the
+// join of prefix_attn.cu adds them up.
+//
+// Two streams of softmax, a warpgroup each.  With more than 128 rows they take the two halves of
+// the rows, on the same tiles; with fewer they take the same rows, on every other tile, so that one's
+// products run during the other's softmax in both cases.
+//
+// Warp roles (384 threads): warp 0 loads K and V tiles by TMA into a ring of slots, ahead across segments; warp 1
+// issues the products, S = Q K^T into TMEM and O += P V with P in TMEM; warps 4 - 11 are the softmax, a thread
+// a row: all 128 scores of a tile in registers, O rescaled only when the maximum has grown by more than 2^8.
+//
+// Precision: a weight goes into the second product as two bf16 parts, as in the single-token attention
+// (the second part's products take half as long again as the others together; with one part alone the result is off by
+// another rounding of bf16).  Both lie in the columns of S that the weights came from.
+//
+// Every wait is bounded; a wait that gives up sets TSV_DERR_TIMEOUT for the group's sequences.
+#include <cuda_bf16.h>
+
+#include "../common.cuh"
+#include "../tc_ptx.cuh"
+#include "continue_args.cuh"
+
+namespace tsv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileKeys = kPrefixTcKeys;
+constexpr int kUnitRows = kPrefixTcRows;
+constexpr uint32_t kHalfBytes = 128 * 128;  // 128 rows x 64 bf16 (one 128B-swizzled half)
+constexpr int kMaxSlots = 12;
+constexpr uint32_t kRegsProducer = 96, kRegsSoftmax = 200;
+static_assert(128 * kRegsProducer + 256 * kRegsSoftmax <= 384 * 168, "register split exceeds the launch");
+
+// Shared memory: Q tiles | ring of K/V slots | barriers | schedule.
+struct Layout {
+    uint32_t ring, bars, misc, total;
+    int slots;
+};
+template <int D>
+__host__ __device__ inline Layout layout(int q_tiles) {
+    Layout l{};
+    const uint32_t tile = 128u * D * 2u;
+    l.ring = q_tiles * tile;
+    const uint32_t budget = 232448u - 1024u - 1024u;  // max dynamic smem - alignment slack - barriers and schedule
+    const int slots = static_cast<int>((budget - l.ring) / tile);
+    l.slots = slots > kMaxSlots ? kMaxSlots : slots;
+    l.bars = l.ring + l.slots * tile;
+    l.misc = l.bars + 512;
+    l.total = l.misc + 512 + 1024;
+    return l;
+}
+
+struct Bars {
+    static constexpr int kFull = 0;           // [slots]
+    static constexpr int kEmpty = kMaxSlots;  // [slots]
+    static constexpr int kS = 2 * kMaxSlots;  // [2] scores of a stream's tile are in TMEM
+    static constexpr int kP = kS + 2;         // [2] its weights are
+    static constexpr int kO = kP + 2;         // [2] its product with V is done
+    static constexpr int kQ = kO + 2;         // a segment's Q rows are in shared memory
+    static constexpr int kDone = kQ + 1;
+    static constexpr int kCount = kDone + 1;
+};
+
+// A position in the row of tiles: tile t of the `tiles` of unit `unit` of group g.
+struct Tile {
+    int g, unit, t, tiles, groups;  // groups: of 256 rows
+    int4 it;                        // first sequence, first key (0), end, rows
+    __device__ __forceinline__ void set(const PrefixArgs& a, int group) {
+        g = group;
+        it = a.item[group];
+        tiles = (it.z + kTileKeys - 1) / kTileKeys;
+        groups = (it.w + kUnitRows - 1) / kUnitRows;
+    }
+    __device__ __forceinline__ void next_unit(const PrefixArgs& a) {
+        t = 0;
+        if (++unit < groups * a.Hkv) return;
+        unit = 0;
+        do {
+            set(a, g + 1);
+        } while (tiles * groups == 0 && g + 1 < a.G);
+    }
+    __device__ __forceinline__ int head() const { return unit / groups; }
+    __device__ __forceinline__ int row0() const { return unit % groups * kUnitRows; }
+    __device__ __forceinline__ int rows() const { return min(kUnitRows, it.w - row0()); }
+    // both streams on the same rows, each with every other tile
+    __device__ __forceinline__ bool by_tile() const { return rows() <= 128; }
+};
+
+// One warp: the position of tile x (x < tc_start[G]).
+__device__ __forceinline__ Tile locate(const PrefixArgs& a, long long x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = a.G;
+    while (len > 1) {
+        const int step = (len + 31) >> 5, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < len && a.tc_start[at] <= x);
+        const int hit = 31 - __clz(below);
+        lo += hit * step;
+        len = min(step, len - hit * step);
+    }
+    Tile p{};
+    p.set(a, lo);
+    const long long off = x - a.tc_start[lo];
+    p.unit = static_cast<int>(off / p.tiles);
+    p.t = static_cast<int>(off - (long long)p.unit * p.tiles);
+    return p;
+}
+
+// One warp: the sequences whose rows a unit holds have a block id outside the cache.
+__device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
+    const int r0 = p.row0();
+    for (int s = r0 / a.gq + (threadIdx.x & 31); s <= (r0 + p.rows() - 1) / a.gq; s += 32) atomicOr(a.seq_err + p.it.x + s, TSV_DERR_BLOCK);
+}
+
+// Two weights (0 or normal numbers) as the sum of two bf16 each, both parts positive: hi is the next
+// bf16 below the weight, lo the rest, so an infinite value stays infinite.
+__device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h0 = max(__float_as_uint(w0), 1u) - 1u, h1 = max(__float_as_uint(w1), 1u) - 1u;
+    *hi = __byte_perm(h0, h1, 0x7632);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(w0 - __uint_as_float(h0 & 0xffff0000u), w1 - __uint_as_float(h1 & 0xffff0000u));
+    *lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                     int q_tiles) {
+    constexpr int HALVES = D / 64;
+    constexpr uint32_t SLOT = 128u * D * 2u;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Layout lay = layout<D>(q_tiles);
+    const int nslots = lay.slots;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
+    Tile* s_first = reinterpret_cast<Tile*>(smem + lay.misc);
+    const uint32_t bar0 = smem_u32(bars);
+    auto bar = [=](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int bs = 1 << a.bs_log2;
+
+    if (tid == 0) {
+        for (int i = 0; i < nslots; ++i) {
+            mbar_init(bar(Bars::kFull + i), 1);
+            mbar_init(bar(Bars::kEmpty + i), 1);
+        }
+        for (int m = 0; m < 2; ++m) {
+            mbar_init(bar(Bars::kS + m), 1);
+            mbar_init(bar(Bars::kP + m), 128);
+            mbar_init(bar(Bars::kO + m), 1);
+        }
+        mbar_init(bar(Bars::kQ), 256);
+        mbar_init(bar(Bars::kDone), 1);
+        *s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(s_tmem), 512);
+        tmem_relinquish();
+    }
+    pdl_wait();  // the plan
+    pdl_launch_dependents();
+    const long long T = a.tc_start[a.G];
+    const int lanes = static_cast<int>(min(T, (long long)a.tc_lanes)), me = blockIdx.x;
+    const long long x0 = me < lanes ? (long long)me * T / lanes : T, x1 = me < lanes ? (long long)(me + 1) * T / lanes : T;
+    const int count = static_cast<int>(x1 - x0);  // tiles of this CTA
+    if (warp == 2 && count > 0) {
+        const Tile p = locate(a, x0);
+        if (lane == 0) *s_first = p;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const Tile first = *s_first;
+    int my_err = 0;
+    int err_g = first.g;  // the group whose sequences are told if a wait of this thread gives up
+
+    if (warp < 4) regs_dec<kRegsProducer>();
+    if (count == 0) {
+        if (warp >= 4) regs_inc<kRegsSoftmax>();
+    } else if (warp == 0) {
+        // ============================ TMA producer: lane j loads the id of the tile's j-th block and issues
+        // that block's boxes; the next tile's ids are loaded while this tile's fills wait for their slots
+        Tile p = first;
+        auto ids = [&](const Tile& q) {
+            const int u0 = q.t * kTileKeys, nb = (min(u0 + kTileKeys, q.it.z) - u0 + bs - 1) >> a.bs_log2;
+            return lane < nb ? a.block_table[(long long)q.it.x * a.max_blocks + (u0 >> a.bs_log2) + lane] : 0;
+        };
+        int blk = ids(p), issued = 0;
+        const uint64_t policy = l2_evict_first_policy();
+        const bool once = p.groups == 1;
+        for (int j = 0; j < count && !my_err; ++j) {
+            const int u0 = p.t * kTileKeys, nblk = (min(u0 + kTileKeys, p.it.z) - u0 + bs - 1) >> a.bs_log2;
+            const int g = p.head(), cur = blk;
+            const bool bad = lane < nblk && static_cast<unsigned>(cur) >= static_cast<unsigned>(a.num_blocks);
+            if (__any_sync(0xffffffffu, bad)) flag_unit(a, p);
+            // a bad id reads zeros past the cache
+            const int slot_row = bad ? a.num_blocks * bs : cur * bs;
+            err_g = p.g;
+            if (j + 1 < count) {
+                if (++p.t >= p.tiles) p.next_unit(a);
+                blk = ids(p);
+            }
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                const int f = 2 * j + kv, slot = f % nslots, use = f / nslots;
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(Bars::kEmpty + slot), (use - 1) & 1, s_abort))) {
+                    my_err = 1;
+                    break;
+                }
+                const uint32_t dst = smem_u32(smem + lay.ring + slot * SLOT);
+                if (lane == 0) mbar_expect_tx(bar(Bars::kFull + slot), static_cast<uint32_t>(nblk * bs * 128 * HALVES));
+                __syncwarp();
+                if (lane < nblk) {
+#pragma unroll
+                    for (int hh = 0; hh < HALVES; ++hh) {
+                        if (once)
+                            tma_load_3d(dst + hh * kHalfBytes + lane * bs * 128, kv ? &tmv : &tmk, bar(Bars::kFull + slot), hh * 64, g, slot_row, policy);
+                        else
+                            tma_load_3d_keep(dst + hh * kHalfBytes + lane * bs * 128, kv ? &tmv : &tmk, bar(Bars::kFull + slot), hh * 64, g, slot_row);
+                    }
+                }
+                issued = f + 1;
+            }
+        }
+        // never leave with copies in flight
+        if (lane == 0) {
+            for (int f = max(0, issued - nslots); f < issued; ++f) {
+                volatile int never = 0;
+                if (!mbar_wait(bar(Bars::kFull + f % nslots), (f / nslots) & 1, &never)) my_err = 1;
+            }
+        }
+    } else if (warp == 1) {
+        // ============================ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
+            const uint64_t dQ = sdesc_sw128(smem_u32(smem), 16, 1024);                         // K-major Q tiles
+            const uint64_t dK = sdesc_sw128(smem_u32(smem + lay.ring), 16, 1024);              // K-major K tiles
+            const uint64_t dV = sdesc_sw128(smem_u32(smem + lay.ring), kHalfBytes, 1024);      // MN-major V tiles
+            // S of stream m = Q tile qt . K^T
+            auto issue_S = [=](int m, int qt, int slot) {
+                const uint64_t qa = dQ + ((qt * SLOT) >> 4), kb = dK + ((slot * SLOT) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                    mma_bf16(tmem + m * 128, qa + off, kb + off, idS, k > 0);
+                }
+            };
+            // O of stream m += (hi + lo) . V; hi in the first 64 columns of S, lo in the others
+            auto issue_PV = [=](int m, int slot, bool more) {
+                const uint64_t vb = dV + ((slot * SLOT) >> 4);
+                const uint32_t d = tmem + 256 + m * D, pa = tmem + m * 128;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < kTileKeys / 16; ++k)
+                        mma_bf16_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
+            };
+            auto full = [&](int f) { return mbar_wait(bar(Bars::kFull + f % nslots), (f / nslots) & 1, s_abort); };
+            auto free_slot = [&](int f) { mma_commit(bar(Bars::kEmpty + f % nslots)); };
+            Tile p = first;
+            int n_p[2] = {0, 0};  // weights waited for, of each stream
+            bool ok = true;
+            for (int j = 0, seg = 0; j < count && ok; ++seg) {
+                const int n = min(p.tiles - p.t, count - j);
+                err_g = p.g;
+                ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
+                if (!p.by_tile()) {
+                    ok = ok && full(2 * j);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int m = 0; m < 2; ++m) {
+                        issue_S(m, m, (2 * j) % nslots);
+                        mma_commit(bar(Bars::kS + m));
+                    }
+                    free_slot(2 * j);
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int fV = 2 * (j + i) + 1, fK = fV + 1;
+                        const bool next = i + 1 < n;
+                        ok = full(fV) && (!next || full(fK));
+                        for (int m = 0; m < 2 && ok; ++m) {
+                            ok = mbar_wait(bar(Bars::kP + m), n_p[m]++ & 1, s_abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_PV(m, fV % nslots, i > 0);
+                            if (next) issue_S(m, m, fK % nslots);
+                            mma_commit(bar(Bars::kO + m));
+                            if (next) mma_commit(bar(Bars::kS + m));
+                        }
+                        if (!ok) break;
+                        free_slot(fV);
+                        if (next) free_slot(fK);
+                    }
+                } else {
+                    for (int m = 0; m < 2 && m < n && ok; ++m) {
+                        const int fK = 2 * (j + m);
+                        ok = full(fK);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_S(m, 0, fK % nslots);
+                        mma_commit(bar(Bars::kS + m));
+                        free_slot(fK);
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int m = i & 1, fV = 2 * (j + i) + 1, fK = fV + 3;
+                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), n_p[m]++ & 1, s_abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_PV(m, fV % nslots, i > 1);
+                        mma_commit(bar(Bars::kO + m));
+                        free_slot(fV);
+                        if (i + 2 < n) {
+                            ok = full(fK);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_S(m, 0, fK % nslots);
+                            mma_commit(bar(Bars::kS + m));
+                            free_slot(fK);
+                        }
+                    }
+                }
+                j += n;
+                if (j < count) p.next_unit(a);
+            }
+            if (!ok) my_err = 1;
+            // every issued product completes before TMEM is released
+            mma_commit(bar(Bars::kDone));
+            volatile int never = 0;
+            if (!mbar_wait(bar(Bars::kDone), 0, &never)) my_err = 1;
+        }
+    } else if (warp >= 4) {
+        // ============================ softmax, a stream each warpgroup
+        regs_inc<kRegsSoftmax>();
+        const int wg = (warp - 4) >> 2, tw = (tid - 128) & 127;  // stream, row of its M tile (TMEM lane)
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + wg * 128, tO = tmem + lane_base + 256 + wg * D;
+        const float sl2 = a.scale_log2;
+        Tile p = first;
+        bool ok = true;
+        int n_s = 0;  // tiles of this stream so far
+        for (int j = 0, seg = 0; j < count; ++seg) {
+            const int n = min(p.tiles - p.t, count - j);
+            const bool by_tile = p.by_tile(), whole = n == p.tiles;
+            err_g = p.g;
+            // This thread's row.  A partial M tile deals its rows round over the four 32-lane quadrants of
+            // TMEM, so that all four warps share the work.
+            const int r_tile = by_tile ? 0 : wg * 128, rows_here = min(128, p.rows() - r_tile);
+            const int rl = rows_here < 128 ? 4 * (tw & 31) + (tw >> 5) : tw;
+            const bool valid = rl < rows_here;
+            const bool active = __any_sync(0xffffffffu, valid);
+            const int x = p.row0() + r_tile + rl, sq = x / a.gq, hj = x - sq * a.gq;  // row of the item: sequence and head
+            const long long place = (long long)(p.it.x + sq) * a.Hq + p.head() * a.gq + hj;  // of the row, in [B, Hq]
+            if (!by_tile || wg == 0) {
+                // Q rows: 64-element halves of [128 rows x 128 B], 16-byte chunk c of row r at c ^ (r & 7)
+                const uint32_t dst = smem_u32(smem + (r_tile >> 7) * SLOT) + (tw >> 3) * 1024u + (tw & 7) * 128u;
+                const bool take = valid && TSV_IN_BOUNDS(place, (long long)a.B * a.Hq, a.seq_err + p.it.x);
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (take ? place * D : 0));
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) cp_async16(dst + (c >> 3) * kHalfBytes + (((c & 7) ^ (tw & 7)) << 4), src + c, take);
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(bar(Bars::kQ));
+            float m_run = -INFINITY, l_run = 0.0f;
+            int steps = 0;
+            for (int i = by_tile ? wg : 0; i < n; i += by_tile ? 2 : 1) {
+                if (!ok) break;
+                const int left = p.it.z - (p.t + i) * kTileKeys;  // keys from the tile's first on
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kS + wg), n_s & 1, s_abort));
+                if (!ok) {
+                    *s_abort = 1;
+                    break;
+                }
+                ++n_s;
+                ++steps;
+                tc_fence_after();
+                if (active) {
+                    uint32_t sv[128];
+                    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
+                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
+                    tmem_wait_ld();
+                    if (left < kTileKeys) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) sv[c] = c < left ? sv[c] : 0xff800000u;  // -inf
+                    }
+                    float mxa[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mxa[q] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 16)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) mxa[q] = max3f(mxa[q], __uint_as_float(sv[c + 2 * q]), __uint_as_float(sv[c + 2 * q + 1]));
+                    const float mx = sl2 * max3f(max3f(mxa[0], mxa[1], mxa[2]), max3f(mxa[3], mxa[4], mxa[5]), fmaxf(mxa[6], mxa[7]));
+                    // The last product of this stream is done before O is rescaled: the issuer committed the S
+                    // just waited for after it.  A segment's first product overwrites O.
+                    bool rescale = false;
+                    float factor = 1.0f;
+                    if (m_run == -INFINITY) {
+                        m_run = mx;
+                    } else if (mx > m_run + 8.0f) {
+                        factor = ex2(m_run - mx);
+                        m_run = mx;
+                        rescale = true;
+                    }
+                    l_run *= factor;
+                    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                        for (int q4 = 0; q4 < D / 32; ++q4) {
+                            uint32_t ov[32];
+                            tmem_ld32(tO + q4 * 32, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * factor);
+                            tmem_st32(tO + q4 * 32, ov);
+                        }
+                        tmem_wait_st();
+                    }
+                    // a row whose scores are all -inf so far keeps weights of 0
+                    const float ref = m_run == -INFINITY ? 0.0f : m_run;
+                    const unsigned long long sc2 = f2_pack(sl2, sl2), off2 = f2_pack(-ref, -ref);
+                    unsigned long long la2[4] = {0ull, 0ull, 0ull, 0ull};
+                    uint32_t hi[64];
+#pragma unroll
+                    for (int q = 0; q < 64; ++q) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1])), sc2, off2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        la2[q & 3] = f2_add(la2[q & 3], f2_pack(p0, p1));
+                        split_bf16(p0, p1, &hi[q], &sv[q]);  // (scores 2q and 2q + 1 >= q have been read)
+                    }
+                    tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&hi[0]));
+                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&hi[32]));
+                    tmem_st32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_st32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                    tmem_wait_st();
+                    float s0, s1, s2, s3, s4, s5, s6, s7;
+                    f2_unpack(la2[0], s0, s1);
+                    f2_unpack(la2[1], s2, s3);
+                    f2_unpack(la2[2], s4, s5);
+                    f2_unpack(la2[3], s6, s7);
+                    l_run += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+                }
+                // V rows behind the prefix are zeroed before the product (they may hold anything, and 0 * NaN is
+                // NaN); with the rows halved the first stream does it, whose product is issued first
+                if (left < kTileKeys && (by_tile || wg == 0)) {
+                    const int fV = 2 * (j + i) + 1;
+                    ok = mbar_wait(bar(Bars::kFull + fV % nslots), (fV / nslots) & 1, s_abort);
+                    if (ok) {
+                        constexpr int kRowChunks = HALVES * 8, kRowsPerStep = 128 / kRowChunks;
+                        uint8_t* vt = smem + lay.ring + (fV % nslots) * SLOT + ((tw % kRowChunks) >> 3) * kHalfBytes + (tw & 7) * 16;
+                        for (int row = left + tw / kRowChunks; row < kTileKeys; row += kRowsPerStep)
+                            *reinterpret_cast<uint4*>(vt + row * 128) = make_uint4(0, 0, 0, 0);
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(bar(Bars::kP + wg));
+                if (!ok) *s_abort = 1;
+            }
+            // ---- the segment's (m, l, O)
+            if (ok && steps > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kO + wg), (n_s - 1) & 1, s_abort));
+                tc_fence_after();
+                if (!ok) *s_abort = 1;
+            }
+            if (ok && active) {
+                const long long row = whole ? place + (by_tile && wg ? 2LL * a.B * a.Hq : 0LL)
+                                            : ((long long)me * 4 + (seg == 0 ? 0 : 2) + wg) * 128 + rl;
+                const bool in = valid && TSV_IN_BOUNDS(row, whole ? 3LL * a.B * a.Hq : 512LL * a.tc_lanes, a.seq_err + p.it.x);
+                float* o = (whole ? a.whole_o : a.tc_o) + (in ? row * D : 0);
+                if (steps > 0) {
+#pragma unroll 1
+                    for (int q4 = 0; q4 < D / 32; ++q4) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + q4 * 32, ov);
+                        tmem_wait_ld();
+                        if (in) {
+#pragma unroll
+                            for (int v4 = 0; v4 < 8; ++v4)
+                                reinterpret_cast<uint4*>(o + q4 * 32)[v4] = make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2], ov[4 * v4 + 3]);
+                        }
+                    }
+                }
+                if (in) {
+                    (whole ? a.whole_m : a.tc_m)[row] = m_run;
+                    (whole ? a.whole_l : a.tc_l)[row] = l_run;
+                }
+            }
+            tc_fence_before();
+            j += n;
+            if (j < count) {
+                p.next_unit(a);
+                named_bar_sync(1, 256);  // both streams are done with Q
+            }
+        }
+        if (!ok) my_err = 1;
+    }
+    if (my_err) {
+        *s_abort = 1;
+        const int4 it = a.item[err_g];
+        for (int q = 0; q < it.w / a.gq; ++q) atomicOr(a.seq_err + it.x + q, TSV_DERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
+    CUtensorMap mk, mv;
+    const long long rows = static_cast<long long>(a.num_blocks) << a.bs_log2;
+    if (!make_cache_map(&mk, a.k_cache, D, a.Hkv, rows, 1 << a.bs_log2) || !make_cache_map(&mv, a.v_cache, D, a.Hkv, rows, 1 << a.bs_log2))
+        return cudaErrorInvalidValue;
+    // one Q tile where no group can have more rows, and two more slots of the ring
+    const int q_tiles = (long long)a.B * a.gq > 128 ? 2 : 1;
+    const Layout lay = layout<D>(q_tiles);
+    thread_local int smem_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev != smem_dev) {
+        const uint32_t most = layout<D>(1).total > layout<D>(2).total ? layout<D>(1).total : layout<D>(2).total;
+        e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+        if (e != cudaSuccess) return e;
+        smem_dev = dev;
+    }
+    return launch_pdl(prefix_tc_kernel<D>, dim3(static_cast<unsigned>(a.tc_lanes)), dim3(kThreads), lay.total, stream, 1u, a, mk, mv, q_tiles);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
+    return a.D == 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);
+}
+
+}  // namespace tsv

@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
 
 // ------------------------------------------------------------------ the schedule
 
-// A position in the row of tiles: tile t of the `tiles` of the team's unit `unit` of item i.
+// A position in the row of tiles: tile t of the `tiles` of item i, for its `chunk`-th group of rows and
+// the team's `heads`-th run of kv heads.
 struct Place {
-    int i, unit, t, tiles, units;
+    int i, chunk, heads, t, tiles, units;
     int4 it;  // first sequence, first key, end, rows
     template <int TILE>
     __device__ __forceinline__ void set(const PrefixArgs& a, int item) {
@@ -151,15 +152,17 @@ struct Place {
     __device__ __forceinline__ void next(const PrefixArgs& a) {
         if (++t < tiles) return;
         t = 0;
-        if (++unit < units) return;
-        unit = 0;
+        ++heads;
+        if (heads * a.team < a.Hkv) return;
+        heads = 0;
+        if (++chunk * a.rows < it.w) return;
+        chunk = 0;
         do {
             set<TILE>(a, i + 1);
         } while (tiles * units == 0 && i + 1 < a.G + a.B);
     }
-    __device__ __forceinline__ int chunk(const PrefixArgs& a) const { return unit / (a.Hkv / a.team); }
-    __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return unit % (a.Hkv / a.team) * a.team + member; }
-    __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk(a) * a.rows); }
+    __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return heads * a.team + member; }
+    __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk * a.rows); }
 };
 
 // One warp: the position of tile x (x < start[n]).
@@ -177,8 +180,10 @@ __device__ __forceinline__ Place locate(const PrefixArgs& a, long long x) {
     Place p{};
     p.set<TILE>(a, lo);
     const long long off = x - a.start[lo];
-    p.unit = static_cast<int>(off / p.tiles);
-    p.t = static_cast<int>(off - (long long)p.unit * p.tiles);
+    const int unit = static_cast<int>(off / p.tiles), runs = a.Hkv / a.team;
+    p.t = static_cast<int>(off - (long long)unit * p.tiles);
+    p.chunk = unit / runs;
+    p.heads = unit - p.chunk * runs;
     return p;
 }
 
@@ -282,7 +287,7 @@ struct ItemRows {
     const Elem* q;  // the kv head's first row of the item's first sequence
     int row, gq, seq;  // seq: elements from a sequence to the next
     __device__ __forceinline__ const Elem* operator()(int r) const {
-        const int x = row + r, s = x / gq;
+        const int x = row + r, s = x < gq ? 0 : x / gq;
         return q + (long long)s * seq + (x - s * gq) * D;
     }
 };
@@ -290,7 +295,7 @@ template <typename Core>
 __device__ __forceinline__ void load_rows(const PrefixArgs& a, const Place& p, int member, Core& core) {
     using Elem = typename Core::Elem;
     const Elem* q = static_cast<const Elem*>(a.q) + ((long long)p.it.x * a.Hq + p.head(a, member) * a.gq) * Core::D;
-    core.load_q(ItemRows<Elem, Core::D>{q, p.chunk(a) * a.rows, a.gq, a.Hq * Core::D}, p.rows(a));
+    core.load_q(ItemRows<Elem, Core::D>{q, p.chunk * a.rows, a.gq, a.Hq * Core::D}, p.rows(a));
 }
 
 // Where the rows of a whole unit go: each to its own place.
@@ -300,7 +305,7 @@ struct ToPlaces {
     int row, gq, Hq;
     long long first;  // the place of the item's row 0
     __device__ __forceinline__ long long place(int r) const {
-        const int x = row + r, s = x / gq;
+        const int x = row + r, s = x < gq ? 0 : x / gq;
         return first + (long long)s * Hq + (x - s * gq);
     }
     __device__ __forceinline__ void row_(int r, float m_, float l_) const {
@@ -355,7 +360,7 @@ __device__ __forceinline__ void stream_tiles(const PrefixArgs& a, uint32_t ring,
         // the segment's end
         const bool prefix = p.i < a.G, piece = t_first > 0 || p.t + 1 < p.tiles;
         const long long rows = (long long)a.B * a.Hq, slot = 2LL * me + (seg == 0 ? 0 : 1);
-        const int row0 = p.chunk(a) * a.rows;
+        const int row0 = p.chunk * a.rows;
         if (!TSV_IN_BOUNDS(slot, 2LL * a.lanes * a.team, a.seq_err + p.it.x)) return;
         const Leave<D> to{
             {a.whole_o, a.whole_m, a.whole_l, row0, a.gq, a.Hq, (prefix ? 0 : rows) + (long long)p.it.x * a.Hq + p.head(a, member) * a.gq},
@@ -397,7 +402,7 @@ struct Pieces {
     long long at = 0;   // row of the first piece, in the whole units' places or in the slots
     long long next = 0; // row of the second piece; the others follow at `step`
     long long step = 0;
-    const float *o, *m, *l;  // the array they lie in, and its rows
+    const float *o = nullptr, *m = nullptr, *l = nullptr;  // the array they lie in, and its rows
     long long rows = 0;
 };
 __device__ __forceinline__ void in_places(const PrefixArgs& a, Pieces& p) {
@@ -432,6 +437,21 @@ __device__ __forceinline__ Pieces find_pieces(const PrefixArgs& a, int i, int b,
     }
     return p;
 }
+__device__ __forceinline__ const float* of_ptr(const float* p, int lane) {
+    return reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), lane));
+}
+__device__ __forceinline__ void load_lane(const float* p, float (&x)[4]) {
+    const float4 y = *reinterpret_cast<const float4*>(p);
+    x[0] = y.x;
+    x[1] = y.y;
+    x[2] = y.z;
+    x[3] = y.w;
+}
+__device__ __forceinline__ void load_lane(const float* p, float (&x)[2]) {
+    const float2 y = *reinterpret_cast<const float2*>(p);
+    x[0] = y.x;
+    x[1] = y.y;
+}
 // The pieces of a prefix's row that the tensor-core kernel leaves.  Units of up to 128 rows have two from
 // each CTA, one of every other tile; the odd ones are a search of their own (`odd`).
 __device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int b, int kvh, int j, bool odd) {
@@ -463,90 +483,105 @@ __device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int
     return p;
 }
 
-// One CTA: kJoinRows query rows of a (sequence, kv head), kJoinGroups threads to four output elements,
-// each with kJoinAhead pieces in flight.  The pieces are joined in a fixed order.
-constexpr int kJoinGroups = 4, kJoinRows = 2, kJoinAhead = 4;
+// `wpr` warps to a query row, eight warps a CTA.  A lane holds the place, m and l of one piece at a time, a warp
+// takes 32 pieces and then their O together, kJoinAhead rows on their way.  Warps of the same row take
+// turns at the pieces and are joined in order, so the result does not depend on timing.  (A thread for
+// each output element that looks up and weighs every piece for itself took 49 us where this takes 10: 4096 rows of 12
+// pieces.)
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
 
 template <typename Elem, int D, int TILE>
-__global__ void __launch_bounds__(kJoinGroups* kJoinRows* D / 4) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
-    constexpr int VEC = D / 4, EL = kJoinRows * VEC;
-    __shared__ float s_part[kJoinGroups - 1][EL][6];
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixArgs a, int wpr) {
+    constexpr int C = D / 32;  // elements of a lane
+    __shared__ float s_part[kJoinThreads / 32][D + 2];
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
-    const int e = threadIdx.x % EL, grp = threadIdx.x / EL, d = (e % VEC) * 4, j = blockIdx.y * kJoinRows + e / VEC;
-    const long long T = a.start[a.G + a.B];
-    const int lanes = lanes_of(T, a.lanes), err = a.seq_err[b];
-    float M = -INFINITY, sum = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (err == 0 && j < a.gq) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % wpr;
+    const int h = blockIdx.x * (kJoinThreads / 32 / wpr) + warp / wpr;  // query row of all
+    const bool in = h < a.B * a.Hq;
+    const int b = in ? h / a.Hq : 0, j = in ? (h % a.Hq) % a.gq : 0, kvh = in ? (h % a.Hq) / a.gq : 0;
+    const int err = a.seq_err[b];
+    float M = -INFINITY, sum = 0.0f, acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+    if (in && err == 0) {
+        const long long T = a.start[a.G + a.B];
         const int g = a.group[b];
-#pragma unroll 1
-        for (int part = 0; part < (a.tc_lanes > 0 ? 3 : 2); ++part) {
-            const Pieces p = part == 0 ? find_pieces<TILE>(a, a.G + b, b, kvh, j, T, lanes)
-                             : a.tc_lanes > 0 ? find_tc_pieces(a, g, b, kvh, j, part == 2)
-                                              : find_pieces<TILE>(a, g, b, kvh, j, T, lanes);
-            for (int c = grp * kJoinAhead; c < p.n; c += kJoinAhead * kJoinGroups) {
-                float m[kJoinAhead], l[kJoinAhead];
-                float4 o[kJoinAhead];
+        // lane 0 looks up the pieces of the sequence's own keys, 1 those of the prefix, 2 its odd ones
+        Pieces mine;
+        if (lane == 0 || (lane == 1 && a.tc_lanes == 0))
+            mine = find_pieces<TILE>(a, lane == 0 ? a.G + b : g, b, kvh, j, T, lanes_of(T, a.lanes));
+        else if (lane < 3 && a.tc_lanes > 0)
+            mine = find_tc_pieces(a, g, b, kvh, j, lane == 2);
+        const int n0 = __shfl_sync(0xffffffffu, mine.n, 0), n1 = n0 + __shfl_sync(0xffffffffu, mine.n, 1),
+                  n = n1 + __shfl_sync(0xffffffffu, mine.n, 2);
+        for (int c0 = 32 * sub; c0 < n; c0 += 32 * wpr) {
+            const int i = c0 + lane, part = i < n0 ? 0 : i < n1 ? 1 : 2, k = i - (part == 0 ? 0 : part == 1 ? n0 : n1);
+            auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, part); };
+            const long long at = of(mine.at), next = of(mine.next), step = of(mine.step), rows = of(mine.rows);
+            const float *pm = of_ptr(mine.m, part), *pl = of_ptr(mine.l, part), *po = of_ptr(mine.o, part);
+            const long long row = k == 0 ? at : next + (k - 1) * step;
+            float m = -INFINITY, l = 0.0f;
+            if (i < n && TSV_IN_BOUNDS(row, rows, a.seq_err + b)) {
+                m = pm[row];
+                l = pl[row];
+            }
+            float m_new = fmaxf(M, m);
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) {
-                    m[i] = -INFINITY;
-                    l[i] = 0.0f;
-                    o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (c + i < p.n) {
-                        const long long row = c + i == 0 ? p.at : p.next + (c + i - 1) * p.step;
-                        if (!TSV_IN_BOUNDS(row, p.rows, a.seq_err + b)) continue;
-                        m[i] = p.m[row];
-                        l[i] = p.l[row];
-                        // (a piece without tiles, l = 0, leaves no O)
-                        const float4 x = *reinterpret_cast<const float4*>(p.o + row * D + d);
-                        if (l[i] != 0.0f) o[i] = x;
-                    }
+            for (int o = 16; o > 0; o >>= 1) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, o));
+            const float ms = safe_max(m_new), f0 = ex2(M - ms), f = ex2(m - ms);
+            float add = f * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+            M = m_new;
+            sum = fmaf(sum, f0, add);
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] *= f0;
+            // (a piece without tiles, l = 0, leaves no O)
+            const float* o = l != 0.0f ? po + row * D : nullptr;
+            const int most = min(32, n - c0);
+            for (int q = 0; q < most; q += kJoinAhead) {
+                float x[kJoinAhead][C], w[kJoinAhead];
+#pragma unroll
+                for (int u = 0; u < kJoinAhead; ++u) {
+                    const float* from = of_ptr(o, (q + u) & 31);
+                    w[u] = __shfl_sync(0xffffffffu, f, (q + u) & 31);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) x[u][c] = 0.0f;
+                    if (q + u < most && from != nullptr) load_lane(from + lane * C, x[u]);
                 }
-                float m_new = M;
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) m_new = fmaxf(m_new, m[i]);
-                const float ms = safe_max(m_new), f0 = ex2(M - ms);
-                M = m_new;
-                sum *= f0;
-                acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+                for (int u = 0; u < kJoinAhead; ++u)
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) {
-                    const float f = ex2(m[i] - ms);
-                    sum = fmaf(f, l[i], sum);
-                    acc = make_float4(fmaf(f, o[i].x, acc.x), fmaf(f, o[i].y, acc.y), fmaf(f, o[i].z, acc.z), fmaf(f, o[i].w, acc.w));
-                }
+                    for (int c = 0; c < C; ++c) acc[c] = fmaf(w[u], x[u][c], acc[c]);
             }
         }
     }
-    if (grp > 0) {
-        float* s = s_part[grp - 1][e];
-        s[0] = M;
-        s[1] = sum;
-        s[2] = acc.x;
-        s[3] = acc.y;
-        s[4] = acc.z;
-        s[5] = acc.w;
-    }
-    __syncthreads();
-    if (grp > 0 || j >= a.gq) return;
+    if (wpr > 1) {
 #pragma unroll
-    for (int i = 0; i < kJoinGroups - 1; ++i) {
-        const float* s = s_part[i][e];
-        const float m_new = fmaxf(M, s[0]), ms = safe_max(m_new);
-        const float f0 = ex2(M - ms), f1 = ex2(s[0] - ms);
-        M = m_new;
-        sum = sum * f0 + s[1] * f1;
-        acc = make_float4(acc.x * f0 + s[2] * f1, acc.y * f0 + s[3] * f1, acc.z * f0 + s[4] * f1, acc.w * f0 + s[5] * f1);
+        for (int c = 0; c < C; ++c) s_part[warp][lane * C + c] = acc[c];
+        if (lane == 0) {
+            s_part[warp][D] = M;
+            s_part[warp][D + 1] = sum;
+        }
+        __syncthreads();
+        if (sub > 0) return;
+        for (int w = warp + 1; w < warp + wpr; ++w) {
+            const float* s = s_part[w];
+            const float m_new = fmaxf(M, s[D]), ms = safe_max(m_new), f0 = ex2(M - ms), f1 = ex2(s[D] - ms);
+            M = m_new;
+            sum = sum * f0 + s[D + 1] * f1;
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] = acc[c] * f0 + s[lane * C + c] * f1;
+        }
     }
-    const long long h = (long long)b * a.Hq + kvh * a.gq + j;
-    const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, err != 0};
+    if (!in) return;
+    const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + (long long)h * D, a.lse ? a.lse + h : nullptr, err != 0};
     // no keys at all: zeros (and an lse of -infinity)
     const float inv = err == 0 && a.seq_lens[b] == 0 ? 0.0f : to.factor(sum);
-    to.two(0, d, acc.x * inv, acc.y * inv);
-    to.two(0, d + 2, acc.z * inv, acc.w * inv);
-    if (d == 0) to.row(0, M, sum);
+#pragma unroll
+    for (int c = 0; c < C; c += 2) to.two(0, lane * C + c, acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0) to.row(0, M, sum);
 }
 
 template <typename Core>
@@ -568,9 +603,10 @@ cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
     const int warps = a.lanes * a.team;
     e = launch_pdl(prefix_stream_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), kSmem, stream, 1u, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(prefix_join_kernel<Elem, Core::D, Core::KEYS>,
-                      dim3(static_cast<unsigned>(a.B * a.Hkv), static_cast<unsigned>((a.gq + kJoinRows - 1) / kJoinRows)),
-                      dim3(kJoinGroups * kJoinRows * Core::D / 4), 0, stream, 1u, a);
+    // warps to a row of the join: more where there are few rows, whose keys then lie in many pieces
+    const int rows = a.B * a.Hq, wpr = rows <= 256 ? 8 : rows <= 1024 ? 2 : 1, per = kJoinThreads / 32 / wpr;
+    return launch_pdl(prefix_join_kernel<Elem, Core::D, Core::KEYS>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kJoinThreads), 0,
+                      stream, 1u, a, wpr);
 }
 
 template <int D>

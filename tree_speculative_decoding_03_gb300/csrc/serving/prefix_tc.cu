@@ -120,12 +120,18 @@ __device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
     for (int s = r0 / a.gq + (threadIdx.x & 31); s <= (r0 + p.rows() - 1) / a.gq; s += 32) atomicOr(a.seq_err + p.it.x + s, TSV_DERR_BLOCK);
 }
 
-// Two weights (0 or normal numbers) as the sum of two bf16 each, both parts positive: hi is the next
-// bf16 below the weight, lo the rest, so an infinite value stays infinite.
+// Two weights (0 or normal numbers) as the sum of two bf16 each, hi and lo: hi is the weight cut off after bf16's
+// bits, lo the rest and 2^-23 of the weight more, so that a positive weight has two positive parts, which
+// keep an infinite value infinite.
 __device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uint32_t* lo) {
-    const uint32_t h0 = max(__float_as_uint(w0), 1u) - 1u, h1 = max(__float_as_uint(w1), 1u) - 1u;
-    *hi = __byte_perm(h0, h1, 0x7632);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(w0 - __uint_as_float(h0 & 0xffff0000u), w1 - __uint_as_float(h1 & 0xffff0000u));
+    const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
+    *hi = __byte_perm(u0, u1, 0x7632);
+    const float more = 1.0f + 0x1p-23f;
+    float l0, l1;
+    f2_unpack(f2_fma(f2_pack(w0, w1), f2_pack(more, more),
+                     f2_pack(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u), __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u))),
+              l0, l1);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(l0, l1);
     *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -431,19 +437,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float ref = m_run == -INFINITY ? 0.0f : m_run;
                     const unsigned long long sc2 = f2_pack(sl2, sl2), off2 = f2_pack(-ref, -ref);
                     unsigned long long la2[4] = {0ull, 0ull, 0ull, 0ull};
-                    uint32_t hi[64];
 #pragma unroll
-                    for (int q = 0; q < 64; ++q) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * q]), __uint_as_float(sv[2 * q + 1])), sc2, off2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        la2[q & 3] = f2_add(la2[q & 3], f2_pack(p0, p1));
-                        split_bf16(p0, p1, &hi[q], &sv[q]);  // (scores 2q and 2q + 1 >= q have been read)
+                    for (int q32 = 0; q32 < 64; q32 += 32) {
+                        uint32_t hi[32], lo[32];
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * (q32 + q)]), __uint_as_float(sv[2 * (q32 + q) + 1])), sc2, off2), x0, x1);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
+                            la2[q & 3] = f2_add(la2[q & 3], f2_pack(p0, p1));
+                            split_bf16(p0, p1, &hi[q], &lo[q]);
+                        }
+                        tmem_st32(tS + q32, hi);
+                        tmem_st32(tS + 64 + q32, lo);
                     }
-                    tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&hi[0]));
-                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&hi[32]));
-                    tmem_st32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                    tmem_st32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                     tmem_wait_st();
                     float s0, s1, s2, s3, s4, s5, s6, s7;
                     f2_unpack(la2[0], s0, s1);

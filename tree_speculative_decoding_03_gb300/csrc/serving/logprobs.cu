@@ -23,8 +23,7 @@ namespace tsv {
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kGroups = 64, kGroupThreads = kThreads / kGroups;
+constexpr int kGroups = 64;
 constexpr int kAhead = 4;  // vectors of a thread on their way together
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // z - m in units of log2 is held above this, where e^{z - m} is 0 in fp32: a logit of -inf then adds
@@ -59,6 +58,31 @@ __device__ __forceinline__ float key_value(Key k) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 __device__ __forceinline__ int key_index(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+
+// pairs of fp32, an instruction a pair
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float first(Pair p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float second(Pair p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 
 // A 16-byte vector of logits as floats.
 template <typename Elem>
@@ -169,9 +193,11 @@ struct Best {
     }
 };
 
+__host__ __device__ constexpr int threads_of(int cluster) { return cluster == 1 ? 256 : 512; }
+
 // Ranks the `n` keys of `keys` (distinct): the thread of rank r < top gives out[r].
 __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* out) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const Key k = keys[i];
         int r = 0;
         for (int j = 0; j < n; ++j) r += keys[j] > k;
@@ -179,9 +205,11 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* 
     }
 }
 
+// THREADS: 256, four CTAs an SM, where there is a row for each CTA, so that a row's end overlaps other rows' loads
+// (2000 rows of 128256 bf16 logits: 512 threads XXX us, 256 YYY); 512 in a cluster.
 template <typename Elem, int CLUSTER, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    constexpr int N = Vec<Elem>::N;
+__global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER)) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+    constexpr int N = Vec<Elem>::N, kThreads = threads_of(CLUSTER), kWarps = kThreads / 32, kGroupThreads = kThreads / kGroups;
     __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps], s_group[kGroups];
     __shared__ Stats s_stats;   // of the CTA
     __shared__ int s_bad, s_n;
@@ -232,19 +260,34 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __gri
             st.rise(top, c);
         }
         if (st.m == -INFINITY) continue;
-        float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
+        const Pair less = pair(-st.m, -st.m), by = pair(c, c);
+        Pair s2[2] = {0, 0}, w2[2] = {0, 0};  // (0.0f, 0.0f)
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float d = (y[u].get(i) - st.m) * c;
-                if (ENTROPY) d = fmaxf(d, kFloor);
-                const float p = ex2(d);
-                s[i & 1] += p;
-                if (ENTROPY) w[i & 1] = fmaf(p, d, w[i & 1]);
+            for (int i = 0; i < N; i += 2) {
+                const Pair d = mul2(add2(pair(y[u].get(i), y[u].get(i + 1)), less), by);
+                const Pair p = pair(ex2(first(d)), ex2(second(d)));
+                s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], p);
+                if (ENTROPY) w2[(i >> 1) & 1] = fma2(p, d, w2[(i >> 1) & 1]);
             }
-        st.s += s[0] + s[1];
-        st.w += w[0] + w[1];
+        const Pair ss = add2(s2[0], s2[1]), ww = add2(w2[0], w2[1]);
+        st.s += first(ss) + second(ss);
+        if (ENTROPY) {
+            float w = first(ww) + second(ww);
+            if (w != w) {
+                // entries of -inf among them, 0 * -inf: once more, without
+                w = 0.0f;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const float d = fmaxf((y[u].get(i) - st.m) * c, kFloor);
+                        w = fmaf(ex2(d), d, w);
+                    }
+            }
+            st.w += w;
+        }
     }
     const float slice_max = st.m;
     if (tid == 0) s_n = 0;
@@ -295,17 +338,25 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __gri
         while (slices) {
             const int owner = warp * 32 + __ffs(slices) - 1;
             slices &= slices - 1;
-            for (int v0 = begin + owner; v0 < end; v0 += 32 * kThreads) {
-                const int v = v0 + lane * kThreads;
-                Vec<Elem> y;
-                y.none();
-                if (v < end) y = row.load(v);
+            for (int v0 = begin + owner; v0 < end; v0 += 64 * kThreads) {
+                Vec<Elem> y[2];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int at = row.index(v) + i;
-                    const float z = y.get(i);
-                    const bool in = v < end && at >= 0 && at < a.V && z >= bound;
-                    if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
+                for (int u = 0; u < 2; ++u) {
+                    const int v = v0 + (32 * u + lane) * kThreads;
+                    y[u].none();
+                    if (v < end) y[u] = row.load(v);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int v = v0 + (32 * u + lane) * kThreads;
+                    if (!__any_sync(0xffffffffu, v < end && y[u].top() >= bound)) continue;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int at = row.index(v) + i;
+                        const float z = y[u].get(i);
+                        const bool in = v < end && at >= 0 && at < a.V && z >= bound;
+                        if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
+                    }
                 }
             }
         }
@@ -370,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const __gri
 template <typename Elem, int CLUSTER>
 cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t stream) {
     const auto kernel = a.entropy ? token_logprobs_kernel<Elem, CLUSTER, true> : token_logprobs_kernel<Elem, CLUSTER, false>;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.T) * CLUSTER), dim3(kThreads), 0, stream, static_cast<unsigned>(CLUSTER), a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(a.T) * CLUSTER), dim3(threads_of(CLUSTER)), 0, stream, static_cast<unsigned>(CLUSTER), a);
 }
 
 template <typename Elem>
@@ -378,7 +429,7 @@ cudaError_t launch_type(const LogprobArgs& a, int num_sms, cudaStream_t stream) 
     // CTAs a row: as many as still find a place (two an SM) and have a vector for each thread
     const long long vecs = ((long long)a.V + Vec<Elem>::N - 1) / Vec<Elem>::N;
     int n = 1;
-    while (n < 8 && 2LL * n * a.T <= 2LL * num_sms && vecs >= 2LL * n * kThreads) n *= 2;
+    while (n < 8 && 2LL * n * a.T <= 2LL * num_sms && vecs >= 2LL * n * threads_of(2)) n *= 2;
     switch (n) {
         case 8: return launch_rows<Elem, 8>(a, stream);
         case 4: return launch_rows<Elem, 4>(a, stream);

@@ -37,7 +37,7 @@ template <int TILE>
 __device__ __forceinline__ int item_tiles(const int4& it) {
     return it.z > it.y ? (it.z + TILE - 1) / TILE - it.y / TILE : 0;
 }
-// Units of item i, a team at a time; those of the tensor cores are not in the stream.
+// Units of item i in the stream, a team at a time.  With a tensor-core kernel the prefixes are that one's.
 __device__ __forceinline__ int item_units(const PrefixArgs& a, int i, const int4& it) {
     return i < a.G && a.tc_lanes > 0 ? 0 : ((it.w + a.rows - 1) / a.rows) * (a.Hkv / a.team);
 }
@@ -67,9 +67,28 @@ __device__ __forceinline__ long long block_before(long long mine, long long* s_w
     return incl - mine + (warp ? before : 0);
 }
 
+// Lanes that share T tiles: one tile each while there are lanes.
+__device__ __forceinline__ int stream_lanes(long long T, int lanes) { return T < lanes ? static_cast<int>(T) : lanes; }
+
+// The last i in [0, n) with start[i] <= x.
+__device__ __forceinline__ int last_not_above(const long long* start, int n, long long x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
 template <int TILE>
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
-    extern __shared__ int s_off[];  // [G + 1]
+    extern __shared__ __align__(16) uint8_t s_plan[];
+    long long* s_start = reinterpret_cast<long long*>(s_plan);  // [G + B + 1]
+    long long* s_tc_start = s_start + a.G + a.B + 1;           // [G + 1]
+    int* s_off = reinterpret_cast<int*>(s_tc_start + a.G + 1);  // [G + 1]
     __shared__ long long s_warp[32], s_tc_warp[32];
     pdl_wait();
     pdl_launch_dependents();
@@ -86,6 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     const long long cap = (long long)a.max_blocks << a.bs_log2;
     const int n = a.G + a.B, per = (n + kPlanThreads - 1) / kPlanThreads;
     long long mine = 0, tc_mine = 0;
+    int4 last = make_int4(0, 0, 0, 0);
     for (int u = 0; u < per; ++u) {
         const int i = tid * per + u;
         if (i >= n) break;
@@ -118,6 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             a.seq_err[b] = e;
         }
         a.item[i] = it;
+        last = it;
         mine += (long long)item_tiles<TILE>(it) * item_units(a, i, it);
         if (i < a.G) tc_mine += tc_tiles(a, it);
     }
@@ -125,12 +146,40 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     for (int u = 0; u < per; ++u) {
         const int i = tid * per + u;
         if (i >= n) break;
-        a.start[i] = at;
-        const int4 it = a.item[i];  // (this thread's own)
-        at += (long long)item_tiles<TILE>(it) * item_units(a, i, it);
-        if (i == n - 1) a.start[n] = at;
-        if (i <= a.G) a.tc_start[i] = tc_at;
+        const int4 it = per == 1 ? last : a.item[i];  // (this thread's own)
+        const long long end = at + (long long)item_tiles<TILE>(it) * item_units(a, i, it);
+        s_start[i] = a.start[i] = at;
+        at = end;
+        if (i == n - 1) s_start[n] = a.start[n] = at;
+        if (i <= a.G) s_tc_start[i] = a.tc_start[i] = tc_at;
         if (i < a.G) tc_at += tc_tiles(a, it);
+    }
+    __syncthreads();
+    // where each lane begins
+    const long long T = s_start[n], tc_T = a.tc_lanes > 0 ? s_tc_start[a.G] : 0;
+    const int lanes = stream_lanes(T, a.lanes), tc_lanes = stream_lanes(tc_T, a.tc_lanes);
+    for (int k = tid; k < a.lanes + a.tc_lanes; k += kPlanThreads) {
+        const bool tc = k >= a.lanes;
+        const int c = tc ? k - a.lanes : k, of = tc ? tc_lanes : lanes;
+        const long long all = tc ? tc_T : T;
+        int4 p = make_int4(0, 0, 0, 0);
+        int count = 0;
+        if (c < of) {
+            const long long x = lane_start(c, all, of);
+            count = static_cast<int>(lane_start(c + 1, all, of) - x);
+            const int i = last_not_above(tc ? s_tc_start : s_start, tc ? a.G : n, x);
+            const int4 it = a.item[i];
+            const long long off = x - (tc ? s_tc_start : s_start)[i];
+            const int tiles = tc ? (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys : item_tiles<TILE>(it);
+            const int unit = static_cast<int>(off / tiles), t = static_cast<int>(off - (long long)unit * tiles), runs = a.Hkv / a.team;
+            p = tc ? make_int4(i, unit, t, count) : make_int4(i, unit / runs, unit % runs, t);
+        }
+        if (tc) {
+            a.tc_begin[c] = p;
+        } else {
+            a.begin[2 * c] = p;
+            a.begin[2 * c + 1] = make_int4(count, 0, 0, 0);
+        }
     }
 }
 
@@ -140,11 +189,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
 // the team's `heads`-th run of kv heads.
 struct Place {
     int i, chunk, heads, t, tiles, units;
-    int4 it;  // first sequence, first key, end, rows
+    int4 it;     // first sequence, first key, end, rows
+    int4 ahead;  // the next item, on its way while this one lasts
     template <int TILE>
-    __device__ __forceinline__ void set(const PrefixArgs& a, int item) {
+    __device__ __forceinline__ void set(const PrefixArgs& a, int item, const int4& now) {
         i = item;
-        it = a.item[i];
+        it = now;
+        if (item + 1 < a.G + a.B) ahead = a.item[item + 1];
         tiles = item_tiles<TILE>(it);
         units = item_units(a, i, it);
     }
@@ -158,34 +209,12 @@ struct Place {
         if (++chunk * a.rows < it.w) return;
         chunk = 0;
         do {
-            set<TILE>(a, i + 1);
+            set<TILE>(a, i + 1, ahead);
         } while (tiles * units == 0 && i + 1 < a.G + a.B);
     }
     __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return heads * a.team + member; }
     __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk * a.rows); }
 };
-
-// One warp: the position of tile x (x < start[n]).
-template <int TILE>
-__device__ __forceinline__ Place locate(const PrefixArgs& a, long long x) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, len = a.G + a.B;  // the item lies in [lo, lo + len)
-    while (len > 1) {
-        const int step = (len + 31) >> 5, at = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, lane * step < len && a.start[at] <= x);
-        const int hit = 31 - __clz(below);  // start[lo] <= x
-        lo += hit * step;
-        len = min(step, len - hit * step);
-    }
-    Place p{};
-    p.set<TILE>(a, lo);
-    const long long off = x - a.start[lo];
-    const int unit = static_cast<int>(off / p.tiles), runs = a.Hkv / a.team;
-    p.t = static_cast<int>(off - (long long)unit * p.tiles);
-    p.chunk = unit / runs;
-    p.heads = unit - p.chunk * runs;
-    return p;
-}
 
 // ------------------------------------------------------------------ the stream of tiles
 
@@ -337,13 +366,15 @@ __device__ __forceinline__ void stream_tiles(const PrefixArgs& a, uint32_t ring,
     constexpr int D = Core::D, KEYS = Core::KEYS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int me = blockIdx.x * kWarps + warp, which = me / a.team, member = me % a.team;
-    const long long T = a.start[a.G + a.B];
-    const int lanes = lanes_of(T, a.lanes);
-    if (which >= lanes || T == 0) return;
-    const long long x = lane_start(which, T, lanes), x_end = lane_start(which + 1, T, lanes);
-    const int n = static_cast<int>(x_end - x);
-    if (n <= 0) return;
-    Place p = locate<KEYS>(a, x);
+    if (which >= a.lanes) return;
+    const int4 begin = a.begin[2 * which];
+    const int n = a.begin[2 * which + 1].x;
+    if (n == 0) return;
+    Place p{};
+    p.set<KEYS>(a, begin.x, a.item[begin.x]);
+    p.chunk = begin.y;
+    p.heads = begin.z;
+    p.t = begin.w;
     Stream<Core> stream(a, ring, member, p, n);
     stream.begin();
     Core core;
@@ -460,7 +491,7 @@ __device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int
     const int tiles = (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys, groups = (it.w + kPrefixTcRows - 1) / kPrefixTcRows;
     if (tiles == 0 || it.w == 0) return p;
     const long long T = a.tc_start[a.G];
-    const int lanes = static_cast<int>(min(T, (long long)a.tc_lanes));
+    const int lanes = stream_lanes(T, a.tc_lanes);
     const int x = (b - it.x) * a.gq + j, grp = x / kPrefixTcRows, r = x - grp * kPrefixTcRows;
     const bool by_tile = it.w - grp * kPrefixTcRows <= 128;
     if (odd && !by_tile) return p;
@@ -494,25 +525,30 @@ template <typename Elem, int D, int TILE>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixArgs a, int wpr) {
     constexpr int C = D / 32;  // elements of a lane
     __shared__ float s_part[kJoinThreads / 32][D + 2];
-    pdl_wait();
-    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % wpr;
     const int h = blockIdx.x * (kJoinThreads / 32 / wpr) + warp / wpr;  // query row of all
     const bool in = h < a.B * a.Hq;
     const int b = in ? h / a.Hq : 0, j = in ? (h % a.Hq) % a.gq : 0, kvh = in ? (h % a.Hq) / a.gq : 0;
+    // The plan is complete (the kernels in between waited for it before they let the next one start), so the
+    // pieces are known when the wait ends: lane 0 looks up those of the sequence's own keys, 1 those of the
+    // prefix, 2 its odd ones.
+    Pieces mine;
+    if (in) {
+        const long long T = a.start[a.G + a.B];
+        const int g = a.group[b];
+        const bool tc = a.tc_lanes > 0;
+        if (lane == 0 || (lane == 1 && !tc))
+            mine = find_pieces<TILE>(a, lane == 0 ? a.G + b : g, b, kvh, j, T, stream_lanes(T, a.lanes));
+        else if (lane < 3 && tc)
+            mine = find_tc_pieces(a, g, b, kvh, j, lane == 2);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
     const int err = a.seq_err[b];
     float M = -INFINITY, sum = 0.0f, acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.0f;
     if (in && err == 0) {
-        const long long T = a.start[a.G + a.B];
-        const int g = a.group[b];
-        // lane 0 looks up the pieces of the sequence's own keys, 1 those of the prefix, 2 its odd ones
-        Pieces mine;
-        if (lane == 0 || (lane == 1 && a.tc_lanes == 0))
-            mine = find_pieces<TILE>(a, lane == 0 ? a.G + b : g, b, kvh, j, T, lanes_of(T, a.lanes));
-        else if (lane < 3 && a.tc_lanes > 0)
-            mine = find_tc_pieces(a, g, b, kvh, j, lane == 2);
         const int n0 = __shfl_sync(0xffffffffu, mine.n, 0), n1 = n0 + __shfl_sync(0xffffffffu, mine.n, 1),
                   n = n1 + __shfl_sync(0xffffffffu, mine.n, 2);
         for (int c0 = 32 * sub; c0 < n; c0 += 32 * wpr) {
@@ -584,6 +620,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     if (lane == 0) to.row(0, M, sum);
 }
 
+constexpr size_t plan_smem(int B, int G) { return ((size_t)G + B + 1 + G + 1) * sizeof(long long) + ((size_t)G + 1) * sizeof(int); }
+static_assert(plan_smem(kPagesMaxSeqs, kPagesMaxSeqs) <= 232448 - 1024, "the plan's sums fit an SM's shared memory");
+
 template <typename Core>
 cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
     using Elem = typename Core::Elem;
@@ -593,10 +632,13 @@ cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev != smem_dev) {
         e = cudaFuncSetAttribute(prefix_stream_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(prefix_plan_kernel<Core::KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(plan_smem(kPagesMaxSeqs, kPagesMaxSeqs)));
         if (e != cudaSuccess) return e;
         smem_dev = dev;
     }
-    e = launch_pdl(prefix_plan_kernel<Core::KEYS>, dim3(1), dim3(kPlanThreads), (a.G + 1) * sizeof(int), stream, 1u, a);
+    e = launch_pdl(prefix_plan_kernel<Core::KEYS>, dim3(1), dim3(kPlanThreads), plan_smem(a.B, a.G), stream, 1u, a);
     if (e != cudaSuccess) return e;
     if (a.tc_lanes > 0) e = launch_prefix_tc(a, stream);
     if (e != cudaSuccess) return e;
@@ -623,9 +665,12 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     PrefixPlan p{};
     const int gq = Hq / Hkv;
     // a unit's rows: one or two 16-row fragments (bf16), 4 or 8 (fp32)
-    // (the prefixes of a bf16 call are units of 256 rows on the tensor cores)
-    p.tc_lanes = bf16 ? num_sms : 0;
     const long long rows = (long long)B * gq;
+    // bf16 prefixes go to the tensor-core kernel at any number of rows.  In the stream, whose warp-level products
+    // take 32 rows at a time, they are behind from some 16 rows on and ahead by little below: one prefix of
+    // 16384 keys, 8 / 16 / 32 / 128 rows of 128: 36 / 36 / 43 / 49 us there, 29 / 38 / 95 / 256 in the stream; 12 of 4096
+    // keys: 70 / 71 / 72 / 108 against 168 / 248 / 246 / 878.
+    p.tc_lanes = bf16 ? num_sms : 0;
     p.rows = bf16 ? (gq <= 16 ? 16 : 32) : (rows <= 4 ? 4 : 8);
     p.team = 1;
     for (int t = 2; t <= kMaxTeam; ++t)
@@ -636,7 +681,8 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     const long long cap_tiles = ((long long)max_blocks * block_size + tile - 1) / tile + 1;
     const long long units = (rows / p.rows + G) + (long long)B * ((gq + p.rows - 1) / p.rows);
     long long lanes = 2LL * kWarps * num_sms / p.team;
-    p.lanes = lanes_of(units * (Hkv / p.team) * cap_tiles, static_cast<int>(lanes < 1 ? 1 : lanes));
+    const long long most = units * (Hkv / p.team) * cap_tiles;
+    p.lanes = static_cast<int>(lanes < 1 ? 1 : lanes < most ? lanes : most);
     const size_t slots = 2 * (size_t)p.lanes * p.team * p.rows, whole = 3 * (size_t)B * Hq;
     size_t at = aligned(((size_t)G + B + 1) * sizeof(long long));
     auto take = [&at](size_t bytes) {
@@ -652,6 +698,8 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     p.whole_o = take(whole * D * sizeof(float));
     p.whole_m = take(whole * sizeof(float));
     p.whole_l = take(whole * sizeof(float));
+    p.begin = take((size_t)p.lanes * 2 * sizeof(int4));
+    p.tc_begin = take((size_t)p.tc_lanes * sizeof(int4));
     p.tc_start = take(((size_t)G + 1) * sizeof(long long));
     p.tc_o = take((size_t)p.tc_lanes * 512 * D * sizeof(float));
     p.tc_m = take((size_t)p.tc_lanes * 512 * sizeof(float));

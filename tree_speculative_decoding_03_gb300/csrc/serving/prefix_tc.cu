@@ -40,9 +40,9 @@ constexpr int kMaxSlots = 12;
 constexpr uint32_t kRegsProducer = 96, kRegsSoftmax = 200;
 static_assert(128 * kRegsProducer + 256 * kRegsSoftmax <= 384 * 168, "register split exceeds the launch");
 
-// Shared memory: Q tiles | ring of K/V slots | barriers | schedule.
+// Shared memory: Q tiles | ring of K/V slots | barriers.
 struct Layout {
-    uint32_t ring, bars, misc, total;
+    uint32_t ring, bars, total;
     int slots;
 };
 template <int D>
@@ -50,12 +50,11 @@ __host__ __device__ inline Layout layout(int q_tiles) {
     Layout l{};
     const uint32_t tile = 128u * D * 2u;
     l.ring = q_tiles * tile;
-    const uint32_t budget = 232448u - 1024u - 1024u;  // max dynamic smem - alignment slack - barriers and schedule
+    const uint32_t budget = 232448u - 1024u - 512u;  // max dynamic smem - alignment slack - barriers
     const int slots = static_cast<int>((budget - l.ring) / tile);
     l.slots = slots > kMaxSlots ? kMaxSlots : slots;
     l.bars = l.ring + l.slots * tile;
-    l.misc = l.bars + 512;
-    l.total = l.misc + 512 + 1024;
+    l.total = l.bars + 512 + 1024;
     return l;
 }
 
@@ -95,25 +94,6 @@ struct Tile {
     __device__ __forceinline__ bool by_tile() const { return rows() <= 128; }
 };
 
-// One warp: the position of tile x (x < tc_start[G]).
-__device__ __forceinline__ Tile locate(const PrefixArgs& a, long long x) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, len = a.G;
-    while (len > 1) {
-        const int step = (len + 31) >> 5, at = lo + lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, lane * step < len && a.tc_start[at] <= x);
-        const int hit = 31 - __clz(below);
-        lo += hit * step;
-        len = min(step, len - hit * step);
-    }
-    Tile p{};
-    p.set(a, lo);
-    const long long off = x - a.tc_start[lo];
-    p.unit = static_cast<int>(off / p.tiles);
-    p.t = static_cast<int>(off - (long long)p.unit * p.tiles);
-    return p;
-}
-
 // One warp: the sequences whose rows a unit holds have a block id outside the cache.
 __device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
     const int r0 = p.row0();
@@ -148,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
-    Tile* s_first = reinterpret_cast<Tile*>(smem + lay.misc);
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [=](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -175,19 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();  // the plan
     pdl_launch_dependents();
-    const long long T = a.tc_start[a.G];
-    const int lanes = static_cast<int>(min(T, (long long)a.tc_lanes)), me = blockIdx.x;
-    const long long x0 = me < lanes ? (long long)me * T / lanes : T, x1 = me < lanes ? (long long)(me + 1) * T / lanes : T;
-    const int count = static_cast<int>(x1 - x0);  // tiles of this CTA
-    if (warp == 2 && count > 0) {
-        const Tile p = locate(a, x0);
-        if (lane == 0) *s_first = p;
+    const int me = blockIdx.x;
+    const int4 begin = a.tc_begin[me];  // group, unit, tile, tiles of this CTA
+    const int count = begin.w;
+    Tile first{};
+    if (count > 0) {
+        first.set(a, begin.x);
+        first.unit = begin.y;
+        first.t = begin.z;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const Tile first = *s_first;
     int my_err = 0;
     int err_g = first.g;  // the group whose sequences are told if a wait of this thread gives up
 
@@ -195,27 +174,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (count == 0) {
         if (warp >= 4) regs_inc<kRegsSoftmax>();
     } else if (warp == 0) {
-        // ============================ TMA producer: lane j loads the id of the tile's j-th block and issues
-        // that block's boxes; the next tile's ids are loaded while this tile's fills wait for their slots
-        Tile p = first;
-        auto ids = [&](const Tile& q) {
-            const int u0 = q.t * kTileKeys, nb = (min(u0 + kTileKeys, q.it.z) - u0 + bs - 1) >> a.bs_log2;
-            return lane < nb ? a.block_table[(long long)q.it.x * a.max_blocks + (u0 >> a.bs_log2) + lane] : 0;
+        // ============================ TMA producer: a lane for each block of the tile issues that block's boxes.
+        // Block ids come 32 at a time, those of some tiles of a unit, a batch ahead.  (Two warps of 16-byte
+        // asynchronous copies instead: 4096 rows of 32768 keys 132 us against 140, 24 ragged groups of 64-wide heads 175
+        // against 118.)
+        const int per_tile = kTileKeys >> a.bs_log2, batch = 32 / per_tile;
+        Tile p = first, q = first;  // of the fills, of the next batch
+        int q_left = count;         // tiles in no batch yet
+        auto fetch = [&]() {
+            if (q_left <= 0) return 0;
+            const int e = q.t * per_tile + lane, n = min(batch, q.tiles - q.t);
+            const int id = e < (q.it.z + bs - 1) >> a.bs_log2 ? a.block_table[(long long)q.it.x * a.max_blocks + e] : 0;
+            q_left -= n;
+            if (q_left > 0) {
+                q.t += n;
+                if (q.t >= q.tiles) q.next_unit(a);
+            }
+            return id;
         };
-        int blk = ids(p), issued = 0;
-        const uint64_t policy = l2_evict_first_policy();
-        const bool once = p.groups == 1;
+        int blk = fetch(), blk_next = fetch(), k = 0;  // k: the tile's place in its batch
+        int issued = 0;
+        const uint64_t policy = l2_evict_first_policy();  // (also for keys that two units read: 122 us against 131)
         for (int j = 0; j < count && !my_err; ++j) {
-            const int u0 = p.t * kTileKeys, nblk = (min(u0 + kTileKeys, p.it.z) - u0 + bs - 1) >> a.bs_log2;
-            const int g = p.head(), cur = blk;
-            const bool bad = lane < nblk && static_cast<unsigned>(cur) >= static_cast<unsigned>(a.num_blocks);
+            const int nblk = (min(kTileKeys, p.it.z - p.t * kTileKeys) + bs - 1) >> a.bs_log2, g = p.head();
+            const int cur = __shfl_sync(0xffffffffu, blk, (k * per_tile + lane) & 31);
+            const bool mine = lane < nblk, bad = mine && static_cast<unsigned>(cur) >= static_cast<unsigned>(a.num_blocks);
             if (__any_sync(0xffffffffu, bad)) flag_unit(a, p);
-            // a bad id reads zeros past the cache
-            const int slot_row = bad ? a.num_blocks * bs : cur * bs;
+            const int slot_row = (bad ? a.num_blocks : cur) << a.bs_log2;  // (a bad id reads zeros past the cache)
             err_g = p.g;
             if (j + 1 < count) {
-                if (++p.t >= p.tiles) p.next_unit(a);
-                blk = ids(p);
+                ++k;
+                if (++p.t >= p.tiles) {
+                    p.next_unit(a);
+                    k = batch;
+                }
+                if (k == batch) {
+                    blk = blk_next;
+                    blk_next = fetch();
+                    k = 0;
+                }
             }
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
@@ -224,17 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     my_err = 1;
                     break;
                 }
-                const uint32_t dst = smem_u32(smem + lay.ring + slot * SLOT);
+                const uint32_t dst = smem_u32(smem + lay.ring + slot * SLOT) + lane * bs * 128;
                 if (lane == 0) mbar_expect_tx(bar(Bars::kFull + slot), static_cast<uint32_t>(nblk * bs * 128 * HALVES));
                 __syncwarp();
-                if (lane < nblk) {
+                if (mine) {
 #pragma unroll
-                    for (int hh = 0; hh < HALVES; ++hh) {
-                        if (once)
-                            tma_load_3d(dst + hh * kHalfBytes + lane * bs * 128, kv ? &tmv : &tmk, bar(Bars::kFull + slot), hh * 64, g, slot_row, policy);
-                        else
-                            tma_load_3d_keep(dst + hh * kHalfBytes + lane * bs * 128, kv ? &tmv : &tmk, bar(Bars::kFull + slot), hh * 64, g, slot_row);
-                    }
+                    for (int hh = 0; hh < HALVES; ++hh)
+                        tma_load_3d(dst + hh * kHalfBytes, kv ? &tmv : &tmk, bar(Bars::kFull + slot), hh * 64, g, slot_row, policy);
                 }
                 issued = f + 1;
             }

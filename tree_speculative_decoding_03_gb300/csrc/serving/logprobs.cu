@@ -138,18 +138,36 @@ struct Row {
         vecs = static_cast<int>(((long long)head + V + N - 1) / N);
     }
     __device__ __forceinline__ int index(int v) const { return v * N - head; }  // of the vector's first element
-    __device__ __forceinline__ Vec<Elem> load(int v) const {
+    // vectors between the first and the last
+    __device__ __forceinline__ int inner() const { return max(vecs - 2, 0); }
+    // the first or last vector of the row if it is thread t's (-1: it is not)
+    __device__ __forceinline__ int edge(int t, bool first_cta, bool last_cta) const {
+        return t == 0 && first_cta ? 0 : t == 1 && last_cta && vecs > 1 ? vecs - 1 : -1;
+    }
+    // a vector that may reach over the row's ends
+    __device__ __forceinline__ Vec<Elem> load_some(int v) const {
         Vec<Elem> y;
         const int i0 = index(v);
-        if (i0 >= 0 && i0 <= V - N) {
-            y.load(x + i0);
-        } else {
-            y.none();
+        y.none();
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i0 + i >= 0 && i0 + i < V) y.set(i, x + i0 + i);
-        }
+        for (int i = 0; i < N; ++i)
+            if (i0 + i >= 0 && i0 + i < V) y.set(i, x + i0 + i);
         return y;
+    }
+    // vectors v, v + step, ... below `end`, which lie inside the row
+    template <int COUNT>
+    __device__ __forceinline__ void load_tile(Vec<Elem> (&y)[COUNT], int v, int end, int step) const {
+        const Elem* p = x + index(v);
+        if (v + (COUNT - 1) * step < end) {
+#pragma unroll
+            for (int u = 0; u < COUNT; ++u) y[u].load(p + (long long)u * step * N);
+        } else {
+#pragma unroll
+            for (int u = 0; u < COUNT; ++u) {
+                y[u].none();
+                if (v + u * step < end) y[u].load(p + (long long)u * step * N);
+            }
+        }
     }
 };
 
@@ -171,6 +189,26 @@ struct Stats {
         w += o.w;
     }
 };
+
+// sum = sum of e^{z - m}, w = sum of e^{z - m} (z - m) log2(e) over a thread's vectors.  MASKED: the exponent is
+// held above kFloor, an instruction more for an entry.
+template <bool ENTROPY, bool MASKED, typename V>
+__device__ __forceinline__ void add_tile(const V (&y)[kAhead], Pair less, Pair by, float* sum, float* w) {
+    Pair s2[2] = {0, 0}, w2[2] = {0, 0};  // (0.0f, 0.0f)
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int i = 0; i < V::N; i += 2) {
+            Pair d = mul2(add2(pair(y[u].get(i), y[u].get(i + 1)), less), by);
+            if (ENTROPY && MASKED) d = pair(fmaxf(first(d), kFloor), fmaxf(second(d), kFloor));
+            const Pair p = pair(ex2(first(d)), ex2(second(d)));
+            s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], p);
+            if (ENTROPY) w2[(i >> 1) & 1] = fma2(p, d, w2[(i >> 1) & 1]);
+        }
+    const Pair ss = add2(s2[0], s2[1]), ww = add2(w2[0], w2[1]);
+    *sum = first(ss) + second(ss);
+    *w = first(ww) + second(ww);
+}
 
 // The best keys of a warp, in order: lane i holds the i-th (0: none).
 struct Best {
@@ -210,7 +248,8 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* 
 template <typename Elem, int CLUSTER, bool ENTROPY>
 __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER)) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     constexpr int N = Vec<Elem>::N, kThreads = threads_of(CLUSTER), kWarps = kThreads / 32, kGroupThreads = kThreads / kGroups;
-    __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps], s_group[kGroups];
+    __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps];
+    __shared__ __align__(16) float s_group[kGroups];
     __shared__ Stats s_stats;   // of the CTA
     __shared__ int s_bad, s_n;
     __shared__ float s_bound;
@@ -239,19 +278,35 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     }
     const Elem* x = static_cast<const Elem*>(a.logits) + (long long)t * a.stride;
     const Row<Elem> row(x, a.V);
-    const int begin = static_cast<int>((long long)row.vecs * rank / CLUSTER), end = static_cast<int>((long long)row.vecs * (rank + 1) / CLUSTER);
+    // the CTA's vectors, but for the row's first and last
+    const int begin = 1 + static_cast<int>((long long)row.inner() * rank / CLUSTER), end = 1 + static_cast<int>((long long)row.inner() * (rank + 1) / CLUSTER);
     const float c = a.inv_t * kLog2e;
     Stats st{-INFINITY, 0.0f, 0.0f};
-    bool bad = false;
+    bool bad = false, masked = false;
+    // The row's first and last vector, which may hold other elements too: the first two threads'.
+    const int edge = row.edge(tid, rank == 0, rank == CLUSTER - 1);
+    if (edge >= 0) {
+        const Vec<Elem> y = row.load_some(edge);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float z = y.get(i);
+            if (!(z <= st.m)) {
+                bad |= !(z < INFINITY);
+                st.rise(z, c);
+            }
+            const float d = st.m == -INFINITY ? kFloor : fmaxf((z - st.m) * c, kFloor), p = ex2(d);
+            st.s += p;
+            if (ENTROPY) st.w = fmaf(p, d, st.w);
+        }
+    }
+    // the others, the next ones on their way while a tile is added
+    Vec<Elem> next[kAhead];
+    row.load_tile(next, begin + tid, end, kThreads);
     for (int v = begin + tid; v < end; v += kAhead * kThreads) {
         Vec<Elem> y[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (v + u * kThreads < end)
-                y[u] = row.load(v + u * kThreads);
-            else
-                y[u].none();
-        }
+        for (int u = 0; u < kAhead; ++u) y[u] = next[u];
+        row.load_tile(next, v + kAhead * kThreads, end, kThreads);
         float top = y[0].top();
 #pragma unroll
         for (int u = 1; u < kAhead; ++u) top = max_nan(top, y[u].top());
@@ -261,36 +316,20 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
         }
         if (st.m == -INFINITY) continue;
         const Pair less = pair(-st.m, -st.m), by = pair(c, c);
-        Pair s2[2] = {0, 0}, w2[2] = {0, 0};  // (0.0f, 0.0f)
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const Pair d = mul2(add2(pair(y[u].get(i), y[u].get(i + 1)), less), by);
-                const Pair p = pair(ex2(first(d)), ex2(second(d)));
-                s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], p);
-                if (ENTROPY) w2[(i >> 1) & 1] = fma2(p, d, w2[(i >> 1) & 1]);
-            }
-        const Pair ss = add2(s2[0], s2[1]), ww = add2(w2[0], w2[1]);
-        st.s += first(ss) + second(ss);
-        if (ENTROPY) {
-            float w = first(ww) + second(ww);
-            if (w != w) {
-                // entries of -inf among them, 0 * -inf: once more, without
-                w = 0.0f;
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float d = fmaxf((y[u].get(i) - st.m) * c, kFloor);
-                        w = fmaf(ex2(d), d, w);
-                    }
-            }
-            st.w += w;
+        float sum, w;
+        if (!masked) {
+            add_tile<ENTROPY, false>(y, less, by, &sum, &w);
+            masked = ENTROPY && w != w;  // entries of -inf among them, 0 * -inf: once more and from now on without
         }
+        if (masked) add_tile<ENTROPY, true>(y, less, by, &sum, &w);
+        st.s += sum;
+        if (ENTROPY) st.w += w;
     }
     const float slice_max = st.m;
-    if (tid == 0) s_n = 0;
+    if (tid == 0) {
+        s_n = 0;
+        s_bound = -INFINITY;
+    }
     // the CTA's sums, in a fixed order
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -319,15 +358,14 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     }
     if (a.top > 0) {
         // the bound: the top-th largest of the group maxima (in a bad row, none may be found)
-        if (tid == 0) s_bound = -INFINITY;
-        __syncthreads();
         if (tid < kGroups) {
             const float g = s_group[tid];
             int r = 0;
-#pragma unroll 8
-            for (int j = 0; j < kGroups; ++j) {
-                const float o = s_group[j];
-                r += o > g || (o == g && j < tid);
+#pragma unroll
+            for (int j = 0; j < kGroups; j += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(s_group + j);
+                r += (o.x > g || (o.x == g && j < tid)) + (o.y > g || (o.y == g && j + 1 < tid)) + (o.z > g || (o.z == g && j + 2 < tid)) +
+                     (o.w > g || (o.w == g && j + 3 < tid));
             }
             if (r == a.top - 1) s_bound = g;
         }
@@ -338,26 +376,23 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
         while (slices) {
             const int owner = warp * 32 + __ffs(slices) - 1;
             slices &= slices - 1;
-            for (int v0 = begin + owner; v0 < end; v0 += 64 * kThreads) {
+            auto offer = [&](const Vec<Elem>& y, int v, bool have) {
+                if (!__any_sync(0xffffffffu, have && y.top() >= bound)) return;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int at = row.index(v) + i;
+                    const float z = y.get(i);
+                    const bool in = have && at >= 0 && at < a.V && z >= bound;
+                    if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
+                }
+            };
+            const int some = row.edge(owner, rank == 0, rank == CLUSTER - 1);
+            if (some >= 0) offer(row.load_some(some), some, lane == 0);
+            for (int v0 = begin + owner + lane * kThreads; v0 - lane * kThreads < end; v0 += 64 * kThreads) {
                 Vec<Elem> y[2];
+                row.load_tile(y, v0, end, 32 * kThreads);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int v = v0 + (32 * u + lane) * kThreads;
-                    y[u].none();
-                    if (v < end) y[u] = row.load(v);
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int v = v0 + (32 * u + lane) * kThreads;
-                    if (!__any_sync(0xffffffffu, v < end && y[u].top() >= bound)) continue;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int at = row.index(v) + i;
-                        const float z = y[u].get(i);
-                        const bool in = v < end && at >= 0 && at < a.V && z >= bound;
-                        if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
-                    }
-                }
+                for (int u = 0; u < 2; ++u) offer(y[u], v0 + 32 * u * kThreads, v0 + 32 * u * kThreads < end);
             }
         }
         // the warps' lists together

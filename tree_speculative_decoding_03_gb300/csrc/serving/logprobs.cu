@@ -8,8 +8,10 @@
 // The alternatives come from the same pass: a thread's running maximum is the largest of its
 // slice.  Of 64 groups of threads the n-th largest group maximum is a bound that at least n
 // entries reach, so only slices whose maximum reaches it hold alternatives -- some n of 512 --
-// and those few are read again, from L2, by whole warps, each of which keeps its n best in order,
-// one a lane.  Nothing depends on the values but the time: a row of equal logits is read twice.
+// and those few are read again by all threads.  The entries that reach the bound, hardly more than n, are
+// ranked among themselves; where they are many, warps keep lists in order.  Nothing depends on the values but
+// the time: a row of equal logits is read three times.  (Lists for every row, a slice at a time: 2000 rows of
+// 128256 bf16 with 5 / 20 / 32 alternatives 106 / 131 / 153 us, without any 91.)
 // Order: value descending (-0 and 0 are equal), then index ascending, as one 64-bit key.
 //
 // A row is taken by one CTA, or by a cluster of up to eight where there are too few rows to fill the GPU.
@@ -24,7 +26,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kGroups = 64;
-constexpr int kAhead = 4;  // vectors of a thread on their way together
+// vectors of a tile: neighbours, so that a thread's slice is read again in 64-byte pieces (16-byte pieces
+// spread over the row cost four times their bytes: 2000 rows of 128256 bf16, 20 alternatives, 126 us; these ZZZ)
+constexpr int kAhead = 2;
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // z - m in units of log2 is held above this, where e^{z - m} is 0 in fp32: a logit of -inf then adds
 // 0 * -200 to w and not 0 * -inf
@@ -84,44 +88,45 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     return d;
 }
 
-// A 16-byte vector of logits as floats.
+// A 32-byte vector of logits as floats.
 template <typename Elem>
 struct Vec;
-template <>
-struct Vec<float> {
-    static constexpr int N = 4;
-    uint4 r;
-    __device__ __forceinline__ void load(const void* p) { r = __ldcs(static_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void none() { r = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
-    __device__ __forceinline__ void set(int i, const float* p) {
-        const uint32_t u = __float_as_uint(*p);
-        if (i == 0) r.x = u;
-        if (i == 1) r.y = u;
-        if (i == 2) r.z = u;
-        if (i == 3) r.w = u;
+struct Raw {
+    uint32_t r[8];
+    __device__ __forceinline__ void load(const void* p) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "l"(p)
+                     : "memory");
     }
-    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w); }
-    __device__ __forceinline__ float top() const { return max_nan(max_nan(get(0), get(1)), max_nan(get(2), get(3))); }
 };
 template <>
-struct Vec<__nv_bfloat16> {
+struct Vec<float> : Raw {
     static constexpr int N = 8;
-    uint4 r;
-    __device__ __forceinline__ void load(const void* p) { r = __ldcs(static_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void none() { r = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
-    __device__ __forceinline__ void set(int i, const __nv_bfloat16* p) {
-        const uint32_t u = *reinterpret_cast<const unsigned short*>(p), keep = i & 1 ? 0x0000ffffu : 0xffff0000u, put = i & 1 ? u << 16 : u;
-        if (i >> 1 == 0) r.x = (r.x & keep) | put;
-        if (i >> 1 == 1) r.y = (r.y & keep) | put;
-        if (i >> 1 == 2) r.z = (r.z & keep) | put;
-        if (i >> 1 == 3) r.w = (r.w & keep) | put;
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = 0xff800000u;
     }
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t u = i >> 1 == 0 ? r.x : i >> 1 == 1 ? r.y : i >> 1 == 2 ? r.z : r.w;
-        return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
-    }
+    __device__ __forceinline__ void set(int i, const float* p) { r[i] = __float_as_uint(*p); }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(r[i]); }
     __device__ __forceinline__ float top() const {
-        const uint32_t u = max_nan2(max_nan2(r.x, r.y), max_nan2(r.z, r.w));
+        return max_nan(max_nan(max_nan(get(0), get(1)), max_nan(get(2), get(3))), max_nan(max_nan(get(4), get(5)), max_nan(get(6), get(7))));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> : Raw {
+    static constexpr int N = 16;
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = 0xff80ff80u;
+    }
+    __device__ __forceinline__ void set(int i, const __nv_bfloat16* p) {
+        const uint32_t u = *reinterpret_cast<const unsigned short*>(p);
+        r[i >> 1] = i & 1 ? (r[i >> 1] & 0x0000ffffu) | (u << 16) : (r[i >> 1] & 0xffff0000u) | u;
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16); }
+    __device__ __forceinline__ float top() const {
+        const uint32_t u = max_nan2(max_nan2(max_nan2(r[0], r[1]), max_nan2(r[2], r[3])), max_nan2(max_nan2(r[4], r[5]), max_nan2(r[6], r[7])));
         return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
 };
@@ -134,7 +139,7 @@ struct Row {
     const Elem* x;
     int head, V, vecs;  // elements of the first vector before the row
     __device__ __forceinline__ Row(const Elem* row, int V_)
-        : x(row), head(static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(Elem))), V(V_) {
+        : x(row), head(static_cast<int>((reinterpret_cast<uintptr_t>(row) & 31) / sizeof(Elem))), V(V_) {
         vecs = static_cast<int>(((long long)head + V + N - 1) / N);
     }
     __device__ __forceinline__ int index(int v) const { return v * N - head; }  // of the vector's first element
@@ -154,18 +159,18 @@ struct Row {
             if (i0 + i >= 0 && i0 + i < V) y.set(i, x + i0 + i);
         return y;
     }
-    // vectors v, v + step, ... below `end`, which lie inside the row
+    // vectors v, v + 1, ... below `end`, which lie inside the row
     template <int COUNT>
-    __device__ __forceinline__ void load_tile(Vec<Elem> (&y)[COUNT], int v, int end, int step) const {
+    __device__ __forceinline__ void load_tile(Vec<Elem> (&y)[COUNT], int v, int end) const {
         const Elem* p = x + index(v);
-        if (v + (COUNT - 1) * step < end) {
+        if (v + COUNT <= end) {
 #pragma unroll
-            for (int u = 0; u < COUNT; ++u) y[u].load(p + (long long)u * step * N);
+            for (int u = 0; u < COUNT; ++u) y[u].load(p + u * N);
         } else {
 #pragma unroll
             for (int u = 0; u < COUNT; ++u) {
                 y[u].none();
-                if (v + u * step < end) y[u].load(p + (long long)u * step * N);
+                if (v + u < end) y[u].load(p + u * N);
             }
         }
     }
@@ -233,6 +238,14 @@ struct Best {
 
 __host__ __device__ constexpr int threads_of(int cluster) { return cluster == 1 ? 256 : 512; }
 
+// Appends a key; beyond kKeys they are counted alone.  The order in the list does not matter: keys are
+// distinct and ranked later.
+constexpr int kKeys = 512;  // at least 32 a warp
+__device__ __forceinline__ void keep(Key* keys, int* n, Key k) {
+    const int at = atomicAdd(n, 1);
+    if (at < kKeys) keys[at] = k;
+}
+
 // Ranks the `n` keys of `keys` (distinct): the thread of rank r < top gives out[r].
 __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* out) {
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -251,9 +264,9 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps];
     __shared__ __align__(16) float s_group[kGroups];
     __shared__ Stats s_stats;   // of the CTA
-    __shared__ int s_bad, s_n;
+    __shared__ int s_bad, s_n, s_count, s_slices[kThreads];
     __shared__ float s_bound;
-    __shared__ Key s_keys[kWarps * 32], s_best[32];
+    __shared__ Key s_keys[kKeys], s_best[32];
     __shared__ Key s_all[CLUSTER > 1 ? CLUSTER * 32 : 1];
     pdl_wait();
     pdl_launch_dependents();
@@ -301,12 +314,12 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     }
     // the others, the next ones on their way while a tile is added
     Vec<Elem> next[kAhead];
-    row.load_tile(next, begin + tid, end, kThreads);
-    for (int v = begin + tid; v < end; v += kAhead * kThreads) {
+    row.load_tile(next, begin + kAhead * tid, end);
+    for (int v = begin + kAhead * tid; v < end; v += kAhead * kThreads) {
         Vec<Elem> y[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) y[u] = next[u];
-        row.load_tile(next, v + kAhead * kThreads, end, kThreads);
+        row.load_tile(next, v + kAhead * kThreads, end);
         float top = y[0].top();
 #pragma unroll
         for (int u = 1; u < kAhead; ++u) top = max_nan(top, y[u].top());
@@ -328,6 +341,7 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     const float slice_max = st.m;
     if (tid == 0) {
         s_n = 0;
+        s_count = 0;
         s_bound = -INFINITY;
     }
     // the CTA's sums, in a fixed order
@@ -371,38 +385,73 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
         }
         __syncthreads();
         const float bound = s_bound;
-        Best best;
-        unsigned slices = bad ? 0u : __ballot_sync(0xffffffffu, slice_max >= bound);
-        while (slices) {
-            const int owner = warp * 32 + __ffs(slices) - 1;
-            slices &= slices - 1;
-            auto offer = [&](const Vec<Elem>& y, int v, bool have) {
-                if (!__any_sync(0xffffffffu, have && y.top() >= bound)) return;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int at = row.index(v) + i;
-                    const float z = y.get(i);
-                    const bool in = have && at >= 0 && at < a.V && z >= bound;
-                    if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
-                }
-            };
-            const int some = row.edge(owner, rank == 0, rank == CLUSTER - 1);
-            if (some >= 0) offer(row.load_some(some), some, lane == 0);
-            for (int v0 = begin + owner + lane * kThreads; v0 - lane * kThreads < end; v0 += 64 * kThreads) {
-                Vec<Elem> y[2];
-                row.load_tile(y, v0, end, 32 * kThreads);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) offer(y[u], v0 + 32 * u * kThreads, v0 + 32 * u * kThreads < end);
-            }
-        }
-        // the warps' lists together
-        const unsigned have = __ballot_sync(0xffffffffu, best.key != 0 && lane < a.top);
-        int at = 0;
-        if (lane == 0 && have) at = atomicAdd(&s_n, __popc(have));
-        at = __shfl_sync(0xffffffffu, at, 0);
-        if ((have >> lane) & 1u) s_keys[at + lane] = best.key;
+        // slices that hold alternatives: some `top` of them
+        if (!bad && slice_max >= bound) s_slices[atomicAdd(&s_count, 1)] = tid;
         if (tid < 32) s_best[tid] = 0;
         __syncthreads();
+        const int slices = s_count, per_slice = (end - begin + kAhead * kThreads - 1) / (kAhead * kThreads) * kAhead;
+        // vector q of thread t's slice
+        auto slice_vec = [&](int t, int q) { return begin + kAhead * t + q % kAhead + q / kAhead * (kAhead * kThreads); };
+        // all their vectors, spread over the threads
+        for (int i0 = tid; i0 < slices * per_slice; i0 += 2 * kThreads) {
+            Vec<Elem> y[2];
+            int v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = i0 + u * kThreads, sl = i / per_slice;
+                v[u] = i < slices * per_slice ? slice_vec(s_slices[sl], i - sl * per_slice) : end;
+                y[u].none();
+                if (v[u] < end) y[u].load(x + row.index(v[u]));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (!(v[u] < end && y[u].top() >= bound)) continue;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (y[u].get(i) >= bound) keep(s_keys, &s_n, make_key(y[u].get(i), static_cast<uint32_t>(row.index(v[u]) + i)));
+            }
+        }
+        if (edge >= 0 && !bad) {
+            const Vec<Elem> y = row.load_some(edge);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = row.index(edge) + i;
+                if (at >= 0 && at < a.V && y.get(i) >= bound) keep(s_keys, &s_n, make_key(y.get(i), static_cast<uint32_t>(at)));
+            }
+        }
+        __syncthreads();
+        if (s_n > kKeys) {
+            // more entries reach the bound than there is room for (rows of equal or few distinct values, of
+            // rising ones): every warp keeps its best in order, one a lane, from whole slices
+            __syncthreads();
+            if (tid == 0) s_n = 0;
+            Best best;
+            for (int sl = warp; sl < slices; sl += kWarps) {
+                const int owner = s_slices[sl];
+                auto offer = [&](const Vec<Elem>& y, int v, bool have) {
+                    if (!__any_sync(0xffffffffu, have && y.top() >= bound)) return;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int at = row.index(v) + i;
+                        const float z = y.get(i);
+                        const bool in = have && at >= 0 && at < a.V && z >= bound;
+                        if (__any_sync(0xffffffffu, in)) best.add(in ? make_key(z, static_cast<uint32_t>(at)) : 0, a.top);
+                    }
+                };
+                const int some = row.edge(owner, rank == 0, rank == CLUSTER - 1);
+                if (some >= 0) offer(row.load_some(some), some, lane == 0);
+                for (int q0 = 0; q0 < per_slice; q0 += 32) {
+                    const int v = q0 + lane < per_slice ? slice_vec(owner, q0 + lane) : end;
+                    Vec<Elem> y;
+                    y.none();
+                    if (v < end) y.load(x + row.index(v));
+                    offer(y, v, v < end);
+                }
+            }
+            __syncthreads();
+            if (best.key != 0 && lane < a.top) keep(s_keys, &s_n, best.key);
+            __syncthreads();
+        }
         rank_keys(s_keys, s_n, a.top, s_best);
     }
     __syncthreads();

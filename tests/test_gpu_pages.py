@@ -179,7 +179,9 @@ def test_release_errors(extra):
             same(run_release(s, keep, 8, in_place), want)
 
 
-@pytest.mark.parametrize("B,bs,max_len,kw", SIZES + [(30, 8, 90, dict(extra=9000)), (30, 8, 900, dict(extra=40000)), (3, 8, 90, dict(free=0, extra=0))])
+@pytest.mark.parametrize("B,bs,max_len,kw", SIZES + [(30, 8, 90, dict(extra=9000)), (30, 8, 900, dict(extra=40000)), (3, 8, 90, dict(free=0, extra=0)),
+                                             (40, 8, 300, dict(max_blocks=2000, extra=9000)), (40, 8, 300, dict(max_blocks=2000, extra=70000)),
+                                             (3, 8, 90, dict(extra=70000)), (40, 8, 900, dict(extra=12000)), (5, 16, 90, dict(extra=1, free=31))])
 def test_compact(B, bs, max_len, kw):
     r = np.random.default_rng(B)
     s = U.pages_state(r, B, bs, max_len, **kw)

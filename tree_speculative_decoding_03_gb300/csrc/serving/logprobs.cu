@@ -27,7 +27,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kGroups = 64;
 // vectors of a tile: neighbours, so that a thread's slice is read again in 64-byte pieces (16-byte pieces
-// spread over the row cost four times their bytes: 2000 rows of 128256 bf16, 20 alternatives, 126 us; these ZZZ)
+// spread over the row cost four times their bytes: 2000 rows of 128256 bf16, 20 alternatives, 126 us; these 115)
 constexpr int kAhead = 2;
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
 // z - m in units of log2 is held above this, where e^{z - m} is 0 in fp32: a logit of -inf then adds
@@ -257,7 +257,7 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* 
 }
 
 // THREADS: 256, four CTAs an SM, where there is a row for each CTA, so that a row's end overlaps other rows' loads
-// (2000 rows of 128256 bf16 logits: 512 threads XXX us, 256 YYY); 512 in a cluster.
+// (2000 rows of 128256 bf16 logits); 512 in a cluster.
 template <typename Elem, int CLUSTER, bool ENTROPY>
 __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER)) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     constexpr int N = Vec<Elem>::N, kThreads = threads_of(CLUSTER), kWarps = kThreads / 32, kGroupThreads = kThreads / kGroups;

@@ -214,22 +214,27 @@ __device__ __forceinline__ int tile_ranks(const bool (&mark)[4], int (&rank)[4],
     return total;
 }
 
-// Sum of `mine` over the cluster's CTAs before this one; *all: over all CTAs.
+// Sums over the cluster's CTAs before this one, *all: over all CTAs.  s_slot must not be written again before a
+// barrier of the cluster.
 template <int CLUSTER>
-__device__ __forceinline__ int cluster_before(int mine, int* s_slot, int* all) {
+__device__ __forceinline__ int2 cluster_before(int2 mine, int2* s_slot, int2* all) {
     if (CLUSTER == 1) {
         *all = mine;
-        return 0;
+        return make_int2(0, 0);
     }
     cg::cluster_group cl = cg::this_cluster();
     if (threadIdx.x == 0) *s_slot = mine;
     cl.sync();
-    int before = 0, sum = 0;
+    int2 before = make_int2(0, 0), sum = make_int2(0, 0);
 #pragma unroll
     for (int r = 0; r < CLUSTER; ++r) {
-        const int x = *cl.map_shared_rank(s_slot, r);
-        before += r < static_cast<int>(cl.block_rank()) ? x : 0;
-        sum += x;
+        const int2 x = *cl.map_shared_rank(s_slot, r);
+        if (r < static_cast<int>(cl.block_rank())) {
+            before.x += x.x;
+            before.y += x.y;
+        }
+        sum.x += x.x;
+        sum.y += x.y;
     }
     *all = sum;
     return before;
@@ -296,7 +301,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_count_kernel(const __
 // One cluster: blocks without a reference go onto the pool in order of their ids.
 template <int CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __grid_constant__ ReleaseArgs a) {
-    __shared__ int s_warp[32], s_slot[2];
+    __shared__ int s_warp[32];
+    __shared__ int2 s_slot;
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, rank = cluster_rank<CLUSTER>();
@@ -312,11 +318,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
     }
     int sum;
     block_scan(mine, s_warp, &sum);
-    int all, any;
-    const int before = cluster_before<CLUSTER>(count_ok ? sum : 0, &s_slot[0], &all);
-    cluster_before<CLUSTER>(__syncthreads_or(over), &s_slot[1], &any);
-    const bool full = count_ok && all > a.num_blocks - count;
-    if (any || full) {
+    int2 all;  // blocks without a reference, whether any was given back too often
+    const int before = cluster_before<CLUSTER>(make_int2(count_ok ? sum : 0, __syncthreads_or(over) ? 1 : 0), &s_slot, &all).x;
+    const bool full = count_ok && all.x > a.num_blocks - count;
+    if (all.y || full) {
         // more references given back than there were, or more blocks than the pool has places: the
         // sequences that took part are told
         for (int b = rank; b < a.B; b += CLUSTER) {
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
         int err;
         a.held_out[b] = kept_blocks(a, a.held[b], a.keep_lens[b], count_ok, &err);
     }
-    if (rank == 0 && tid == 0) *a.free_count_out = count_ok ? min(count + all, a.num_blocks) : count;
+    if (rank == 0 && tid == 0) *a.free_count_out = count_ok ? min(count + all.x, a.num_blocks) : count;
 }
 
 // ------------------------------------------------------------------ compaction
@@ -393,23 +398,100 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_mark_kernel(const __g
     if (threadIdx.x == 0) a.seq_err[b] = !ok ? TSV_DERR_CAPACITY : bad ? TSV_DERR_BLOCK : 0;
 }
 
+// Small caches and tables, one CTA instead of the three kernels around it: the live ids are bits in shared
+// memory, their ranks come from running sums of the words.
+constexpr int kBitIds = 16384, kBitEntries = 65536;  // ids, and table entries, up to which it is taken
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_small_kernel(const __grid_constant__ CompactBlocksArgs a) {
+    constexpr int kWords = kBitIds / 32;  // a thread has at most one
+    static_assert(kWords <= kPlanThreads, "a word for each thread");
+    __shared__ uint32_t s_live[kWords];
+    __shared__ int s_before[kWords + 1];  // live ids before a word
+    __shared__ uint16_t s_from[kBitIds / 2], s_to[kBitIds / 2];
+    __shared__ int s_warp[32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, nb = a.num_blocks, words = (nb + 31) >> 5;
+    for (int w = tid; w < words; w += kPlanThreads) s_live[w] = 0;
+    __syncthreads();
+    for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {  // a warp a sequence
+        const int held = a.held[b];
+        const bool ok = held >= 0 && held <= a.max_blocks;
+        bool bad = false;
+        constexpr int U = 4;
+        if (ok)
+            for (int j0 = lane; j0 < held; j0 += 32 * U) {
+                int id[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) id[u] = j0 + 32 * u < held ? a.block_table[(long long)b * a.max_blocks + j0 + 32 * u] : -1;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (id[u] >= 0 && id[u] < nb)
+                        atomicOr(&s_live[id[u] >> 5], 1u << (id[u] & 31));
+                    else
+                        bad |= j0 + 32 * u < held;
+                }
+            }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) a.seq_err[b] = !ok ? TSV_DERR_CAPACITY : bad ? TSV_DERR_BLOCK : 0;
+    }
+    __syncthreads();
+    int n;
+    const int before = block_scan(tid < words ? __popc(s_live[tid]) : 0, s_warp, &n);
+    if (tid < kWords) s_before[tid] = before;
+    if (tid == 0) s_before[kWords] = n;
+    __syncthreads();
+    auto rank = [&](int id) { return s_before[id >> 5] + ((id & 31) ? __popc(s_live[id >> 5] & ((1u << (id & 31)) - 1)) : 0); };
+    const int moves = n - rank(n);
+    for (int id = tid; id < nb; id += kPlanThreads) {
+        const bool live = (s_live[id >> 5] >> (id & 31)) & 1u;
+        const int rk = rank(id);
+        if (live && id >= n) {
+            s_from[rk - (n - moves)] = static_cast<uint16_t>(id);  // its share moves with it, below
+        } else if (live) {
+            if (a.shares_out != a.shares) a.shares_out[id] = a.shares[id];
+        } else {
+            if (id < n) s_to[id - rk] = static_cast<uint16_t>(id);
+            a.shares_out[id] = 0;
+        }
+        if (id < nb - n) a.free_blocks[id] = nb - 1 - id;
+    }
+    __syncthreads();
+    for (int k = tid; k < nb / 2; k += kPlanThreads) {
+        const int from = k < moves ? s_from[k] : -1, to = k < moves ? s_to[k] : -1;
+        a.copy_src[k] = from;
+        a.copy_dst[k] = to;
+        if (from < 0) continue;
+        const int s = a.shares[from];
+        a.remap[from] = to;
+        a.shares_out[to] = s;
+        a.shares_out[from] = 0;
+    }
+    if (tid == 0) {
+        *a.free_count_out = nb - n;
+        *a.copy_count = moves;
+    }
+}
+
 // One cluster: with n live blocks, the k-th live id from n on moves to the k-th free id below n.
 template <int CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __grid_constant__ CompactBlocksArgs a) {
-    __shared__ int s_warp[32], s_slot[2];
+    __shared__ int s_warp[32];
+    __shared__ int2 s_slot[2];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, rank = cluster_rank<CLUSTER>();
     const IdRun run(a.num_blocks, rank, CLUSTER);
     int mine = 0;
     for (int id = run.first + tid; id < run.end; id += kPlanThreads) mine += a.remap[id];
-    int sum, n, moves;
+    int sum;
     block_scan(mine, s_warp, &sum);
-    const int before = cluster_before<CLUSTER>(sum, &s_slot[0], &n);
+    int2 all;
+    const int before = cluster_before<CLUSTER>(make_int2(sum, 0), &s_slot[0], &all).x, n = all.x;
     mine = 0;
     for (int id = max(run.first, n) + tid; id < run.end; id += kPlanThreads) mine += a.remap[id];
     block_scan(mine, s_warp, &sum);
-    cluster_before<CLUSTER>(sum, &s_slot[1], &moves);
+    cluster_before<CLUSTER>(make_int2(sum, 0), &s_slot[1], &all);
+    const int moves = all.x;
     cluster_barrier<CLUSTER>();
     int place = before;  // live ids before the tile
     for (int tile = run.first; tile < run.end; tile += kTileIds) {
@@ -427,7 +509,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __g
             if (id >= run.end) continue;
             const int rk = place + r[u];
             if (mark[u] && id < n) {
-                a.remap[id] = id;
                 if (a.shares_out != a.shares) a.shares_out[id] = a.shares[id];
             } else if (mark[u]) {
                 // its share moves with it, below
@@ -459,7 +540,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __g
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_rows_kernel(const __grid_constant__ CompactBlocksArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.x, held = a.held[b];
+    const int b = blockIdx.x, held = a.held[b], n = a.num_blocks - *a.free_count_out;  // ids below n stay
     const int mine = held <= a.max_blocks ? held : 0;
     const int end = a.block_table_out == a.block_table ? mine : a.max_blocks;
     const int32_t* row = a.block_table + (long long)b * a.max_blocks;
@@ -471,7 +552,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_rows_kernel(const __g
 #pragma unroll
         for (int u = 0; u < U; ++u) id[u] = j0 + u * step < end ? row[j0 + u * step] : -1;
 #pragma unroll
-        for (int u = 0; u < U; ++u) to[u] = j0 + u * step < mine && id[u] >= 0 && id[u] < a.num_blocks ? a.remap[id[u]] : id[u];
+        for (int u = 0; u < U; ++u) to[u] = j0 + u * step < mine && id[u] >= n && id[u] < a.num_blocks ? a.remap[id[u]] : id[u];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (j0 + u * step < end) out[j0 + u * step] = to[u];
@@ -582,14 +663,19 @@ cudaError_t launch_kv_release(const ReleaseArgs& a, int num_sms, cudaStream_t st
 cudaError_t launch_kv_compact_blocks(const CompactBlocksArgs& a, int num_sms, cudaStream_t stream) {
     thread_local int of_dev = -1;
     thread_local bool fits = false;
-    cudaError_t e = launch_pdl(kv_compact_clear_kernel, dim3(int_ctas(a.num_blocks, num_sms)), dim3(256), 0, stream, 1u, a);
-    if (e == cudaSuccess && a.B > 0)
-        e = launch_pdl(kv_compact_mark_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
-    if (e != cudaSuccess) return e;
-    if (a.num_blocks > kOneCtaIds && cluster8_fits(kv_compact_plan_kernel<8>, of_dev, fits))
-        e = launch_pdl(kv_compact_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, stream, 8u, a);
-    else
-        e = launch_pdl(kv_compact_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
+    cudaError_t e;
+    if (a.num_blocks <= kBitIds && (long long)a.B * a.max_blocks <= kBitEntries) {
+        e = launch_pdl(kv_compact_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
+    } else {
+        e = launch_pdl(kv_compact_clear_kernel, dim3(int_ctas(a.num_blocks, num_sms)), dim3(256), 0, stream, 1u, a);
+        if (e == cudaSuccess && a.B > 0)
+            e = launch_pdl(kv_compact_mark_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
+        if (e != cudaSuccess) return e;
+        if (a.num_blocks > kOneCtaIds && cluster8_fits(kv_compact_plan_kernel<8>, of_dev, fits))
+            e = launch_pdl(kv_compact_plan_kernel<8>, dim3(8), dim3(kPlanThreads), 0, stream, 8u, a);
+        else
+            e = launch_pdl(kv_compact_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
+    }
     if (e != cudaSuccess || a.B == 0) return e;
     return launch_pdl(kv_compact_rows_kernel, dim3(static_cast<unsigned>(a.B)), dim3(row_threads(a.max_blocks)), 0, stream, 1u, a);
 }

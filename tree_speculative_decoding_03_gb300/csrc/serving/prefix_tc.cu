@@ -45,18 +45,31 @@ struct Layout {
     uint32_t ring, bars, total;
     int slots;
 };
-template <int D>
-__host__ __device__ inline Layout layout(int q_tiles) {
+template <int D, int QT>  // QT: Q tiles
+__host__ __device__ constexpr Layout layout() {
     Layout l{};
-    const uint32_t tile = 128u * D * 2u;
-    l.ring = q_tiles * tile;
-    const uint32_t budget = 232448u - 1024u - 512u;  // max dynamic smem - alignment slack - barriers
+    constexpr uint32_t tile = 128u * D * 2u, budget = 232448u - 1024u - 512u;  // max dynamic smem - alignment slack - barriers
+    l.ring = QT * tile;
     const int slots = static_cast<int>((budget - l.ring) / tile);
     l.slots = slots > kMaxSlots ? kMaxSlots : slots;
     l.bars = l.ring + l.slots * tile;
     l.total = l.bars + 512 + 1024;
     return l;
 }
+
+// A place in the ring: the slot of a fill, and the parity of its barriers' phase.
+template <int SLOTS>
+struct Slot {
+    int slot;
+    uint32_t parity;
+    __device__ __forceinline__ void skip(int fills) {  // fills <= SLOTS
+        slot += fills;
+        if (slot >= SLOTS) {
+            slot -= SLOTS;
+            parity ^= 1;
+        }
+    }
+};
 
 struct Bars {
     static constexpr int kFull = 0;           // [slots]
@@ -115,16 +128,16 @@ __device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uin
     *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <int D>
+template <int D, int QT>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                     int q_tiles) {
+    prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     constexpr int HALVES = D / 64;
     constexpr uint32_t SLOT = 128u * D * 2u;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const Layout lay = layout<D>(q_tiles);
-    const int nslots = lay.slots;
+    constexpr Layout lay = layout<D, QT>();
+    constexpr int nslots = lay.slots;
+    using Place = Slot<nslots>;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
@@ -265,68 +278,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kTileKeys / 16; ++k)
                         mma_bf16_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
             };
-            auto full = [&](int f) { return mbar_wait(bar(Bars::kFull + f % nslots), (f / nslots) & 1, s_abort); };
-            auto free_slot = [&](int f) { mma_commit(bar(Bars::kEmpty + f % nslots)); };
+            // The products are issued as fast as the tensor pipe takes them, and it holds few: what this thread does in
+            // between is time that the pipe stands still.  So places in the ring are counted on, without
+            // divisions (with them 1650 of a tile's 6500 cycles went by between its last product and the next's first).
+            auto full = [&](const Place& f) { return mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort); };
+            auto free_slot = [&](const Place& f) { mma_commit(bar(Bars::kEmpty + f.slot)); };
             Tile p = first;
-            int n_p[2] = {0, 0};  // weights waited for, of each stream
+            Place fK{0, 0}, fV{1, 0};  // of the next K and V tile
+            uint32_t p_parity[2] = {0, 0};
             bool ok = true;
             for (int j = 0, seg = 0; j < count && ok; ++seg) {
                 const int n = min(p.tiles - p.t, count - j);
                 err_g = p.g;
                 ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
                 if (!p.by_tile()) {
-                    ok = ok && full(2 * j);
+                    ok = ok && full(fK);
                     if (!ok) break;
                     tc_fence_after();
                     for (int m = 0; m < 2; ++m) {
-                        issue_S(m, m, (2 * j) % nslots);
+                        issue_S(m, m, fK.slot);
                         mma_commit(bar(Bars::kS + m));
                     }
-                    free_slot(2 * j);
+                    free_slot(fK);
+                    fK.skip(2);
+                    ok = full(fV) && (n == 1 || full(fK));
                     for (int i = 0; i < n && ok; ++i) {
-                        const int fV = 2 * (j + i) + 1, fK = fV + 1;
                         const bool next = i + 1 < n;
-                        ok = full(fV) && (!next || full(fK));
-                        for (int m = 0; m < 2 && ok; ++m) {
-                            ok = mbar_wait(bar(Bars::kP + m), n_p[m]++ & 1, s_abort);
+                        Place nV = fV, nK = fK;
+                        nV.skip(2);
+                        nK.skip(2);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            ok = mbar_wait(bar(Bars::kP + m), p_parity[m], s_abort);
                             if (!ok) break;
+                            p_parity[m] ^= 1;
                             tc_fence_after();
-                            issue_PV(m, fV % nslots, i > 0);
-                            if (next) issue_S(m, m, fK % nslots);
+                            issue_PV(m, fV.slot, i > 0);
+                            if (next) issue_S(m, m, fK.slot);
                             mma_commit(bar(Bars::kO + m));
                             if (next) mma_commit(bar(Bars::kS + m));
                         }
                         if (!ok) break;
                         free_slot(fV);
-                        if (next) free_slot(fK);
-                    }
-                } else {
-                    for (int m = 0; m < 2 && m < n && ok; ++m) {
-                        const int fK = 2 * (j + m);
-                        ok = full(fK);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_S(m, 0, fK % nslots);
-                        mma_commit(bar(Bars::kS + m));
-                        free_slot(fK);
-                    }
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int m = i & 1, fV = 2 * (j + i) + 1, fK = fV + 3;
-                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), n_p[m]++ & 1, s_abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_PV(m, fV % nslots, i > 1);
-                        mma_commit(bar(Bars::kO + m));
-                        free_slot(fV);
-                        if (i + 2 < n) {
-                            ok = full(fK);
-                            if (!ok) break;
-                            tc_fence_after();
-                            issue_S(m, 0, fK % nslots);
-                            mma_commit(bar(Bars::kS + m));
+                        fV = nV;
+                        if (next) {
                             free_slot(fK);
+                            fK = nK;
+                            // what the next tile's products read besides P
+                            ok = full(fV) && (i + 2 >= n || full(fK));
                         }
                     }
+                } else {
+                    Place sK = fK;  // of the K tile whose scores come next
+                    for (int m = 0; m < 2 && m < n && ok; ++m) {
+                        ok = full(sK);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_S(m, 0, sK.slot);
+                        mma_commit(bar(Bars::kS + m));
+                        free_slot(sK);
+                        sK.skip(2);
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const int m = i & 1;
+                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), p_parity[m], s_abort);
+                        if (!ok) break;
+                        p_parity[m] ^= 1;
+                        tc_fence_after();
+                        issue_PV(m, fV.slot, i > 1);
+                        mma_commit(bar(Bars::kO + m));
+                        free_slot(fV);
+                        fV.skip(2);
+                        if (i + 2 < n) {
+                            ok = full(sK);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_S(m, 0, sK.slot);
+                            mma_commit(bar(Bars::kS + m));
+                            free_slot(sK);
+                            sK.skip(2);
+                        }
+                    }
+                    fK = sK;
                 }
                 j += n;
                 if (j < count) p.next_unit(a);
@@ -519,26 +552,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
-cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
+template <int D, int QT>
+cudaError_t launch_tiles(const PrefixArgs& a, cudaStream_t stream) {
     CUtensorMap mk, mv;
     const long long rows = static_cast<long long>(a.num_blocks) << a.bs_log2;
     if (!make_cache_map(&mk, a.k_cache, D, a.Hkv, rows, 1 << a.bs_log2) || !make_cache_map(&mv, a.v_cache, D, a.Hkv, rows, 1 << a.bs_log2))
         return cudaErrorInvalidValue;
-    // one Q tile where no group can have more rows, and two more slots of the ring
-    const int q_tiles = (long long)a.B * a.gq > 128 ? 2 : 1;
-    const Layout lay = layout<D>(q_tiles);
+    constexpr int total = static_cast<int>(layout<D, QT>().total);
     thread_local int smem_dev = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev != smem_dev) {
-        const uint32_t most = layout<D>(1).total > layout<D>(2).total ? layout<D>(1).total : layout<D>(2).total;
-        e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+        e = cudaFuncSetAttribute(prefix_tc_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
         if (e != cudaSuccess) return e;
         smem_dev = dev;
     }
-    return launch_pdl(prefix_tc_kernel<D>, dim3(static_cast<unsigned>(a.tc_lanes)), dim3(kThreads), lay.total, stream, 1u, a, mk, mv, q_tiles);
+    return launch_pdl(prefix_tc_kernel<D, QT>, dim3(static_cast<unsigned>(a.tc_lanes)), dim3(kThreads), total, stream, 1u, a, mk, mv);
+}
+
+template <int D>
+cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
+    // one Q tile where no group can have more rows, which leaves the ring another slot
+    return (long long)a.B * a.gq > 128 ? launch_tiles<D, 2>(a, stream) : launch_tiles<D, 1>(a, stream);
 }
 
 }  // namespace

@@ -14,8 +14,8 @@
 // the rows, on the same tiles; with fewer they take the same rows, on every other tile, so that one's
 // products run during the other's softmax in both cases.
 //
-// Warp roles (384 threads): warp 0 loads K and V tiles by TMA into a ring of slots, ahead across segments; warp 1
-// issues the products, S = Q K^T into TMEM and O += P V with P in TMEM; warps 4 - 11 are the softmax, a thread
+// Warp roles (384 threads): warp 0 loads K and V tiles by TMA into a ring of slots, ahead across segments; warps 1
+// and 2 issue the products, S = Q K^T into TMEM and O += P V with P in TMEM; warps 4 - 11 are the softmax, a thread
 // a row: all 128 scores of a tile in registers, O rescaled only when the maximum has grown by more than 2^8.
 //
 // Precision: a weight goes into the second product as two bf16 parts, as in the single-token attention
@@ -78,8 +78,8 @@ struct Bars {
     static constexpr int kP = kS + 2;         // [2] its weights are
     static constexpr int kO = kP + 2;         // [2] its product with V is done
     static constexpr int kQ = kO + 2;         // a segment's Q rows are in shared memory
-    static constexpr int kDone = kQ + 1;
-    static constexpr int kCount = kDone + 1;
+    static constexpr int kDone = kQ + 1;  // [2]
+    static constexpr int kCount = kDone + 2;
 };
 
 // A position in the row of tiles: tile t of the `tiles` of unit `unit` of group g.
@@ -106,6 +106,28 @@ struct Tile {
     // both streams on the same rows, each with every other tile
     __device__ __forceinline__ bool by_tile() const { return rows() <= 128; }
 };
+
+// The products with descriptors given by their low words.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024 bytes between 8-row groups, version 1, 128-byte swizzle
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %4};\nmov.b64 db, {%2, %4};\nsetp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b64 db;\nmov.b64 db, {%2, %4};\nsetp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t opaque_u32(uint32_t x) {
+    uint32_t y;
+    asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 // One warp: the sequences whose rows a unit holds have a block id outside the cache.
 __device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
@@ -155,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(Bars::kS + m), 1);
             mbar_init(bar(Bars::kP + m), 128);
             mbar_init(bar(Bars::kO + m), 1);
+            mbar_init(bar(Bars::kDone + m), 1);
         }
         mbar_init(bar(Bars::kQ), 256);
-        mbar_init(bar(Bars::kDone), 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -252,46 +274,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(bar(Bars::kFull + f % nslots), (f / nslots) & 1, &never)) my_err = 1;
             }
         }
-    } else if (warp == 1) {
-        // ============================ MMA issuer
+    } else if (warp < 3) {
+        // ============================ MMA issuers.  The products are issued as fast as the tensor pipe takes them,
+        // and it holds few: what the issuing thread does in between (waits, places in the ring) is time that the
+        // pipe stands still.  So places are counted on without divisions.  Streams on the same tiles have one
+        // issuer, which keeps a stream's O and next S together; streams on every other tile one each, so
+        // that neither waits for the other's fills.  (One prompt of 32768 keys, 64 sequences: 139 us, with an issuer
+        // each 147, with divisions 150; 24 ragged groups: 166 with one issuer, 155 with two.)
         if (lane == 0) {
+            const int me_m = warp - 1;
             constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
-            const uint64_t dQ = sdesc_sw128(smem_u32(smem), 16, 1024);                         // K-major Q tiles
-            const uint64_t dK = sdesc_sw128(smem_u32(smem + lay.ring), 16, 1024);              // K-major K tiles
-            const uint64_t dV = sdesc_sw128(smem_u32(smem + lay.ring), kHalfBytes, 1024);      // MN-major V tiles
+            // Descriptors of Q and K tiles (K-major) and V tiles (MN-major): the high words are constants, the low ones
+            // hold the address in units of 16 bytes, so that an operand costs one 32-bit add.
+            const uint32_t dQ = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem), 16, 1024));
+            const uint32_t dK = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + lay.ring), 16, 1024));
+            const uint32_t dV = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + lay.ring), kHalfBytes, 1024));
             // S of stream m = Q tile qt . K^T
             auto issue_S = [=](int m, int qt, int slot) {
-                const uint64_t qa = dQ + ((qt * SLOT) >> 4), kb = dK + ((slot * SLOT) >> 4);
+                const uint32_t qa = opaque_u32(dQ + ((qt * SLOT) >> 4)), kb = opaque_u32(dK + ((slot * SLOT) >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-                    mma_bf16(tmem + m * 128, qa + off, kb + off, idS, k > 0);
+                    mma_ss(tmem + m * 128, qa + off, kb + off, idS, k > 0);
                 }
             };
             // O of stream m += (hi + lo) . V; hi in the first 64 columns of S, lo in the others
             auto issue_PV = [=](int m, int slot, bool more) {
-                const uint64_t vb = dV + ((slot * SLOT) >> 4);
+                const uint32_t vb = opaque_u32(dV + ((slot * SLOT) >> 4));
                 const uint32_t d = tmem + 256 + m * D, pa = tmem + m * 128;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < kTileKeys / 16; ++k)
-                        mma_bf16_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
+                        mma_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
             };
-            // The products are issued as fast as the tensor pipe takes them, and it holds few: what this thread does in
-            // between is time that the pipe stands still.  So places in the ring are counted on, without
-            // divisions (with them 1650 of a tile's 6500 cycles went by between its last product and the next's first).
             auto full = [&](const Place& f) { return mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort); };
             auto free_slot = [&](const Place& f) { mma_commit(bar(Bars::kEmpty + f.slot)); };
             Tile p = first;
-            Place fK{0, 0}, fV{1, 0};  // of the next K and V tile
-            uint32_t p_parity[2] = {0, 0};
+            uint32_t n_p[2] = {0, 0};  // tiles of each stream before the segment
             bool ok = true;
             for (int j = 0, seg = 0; j < count && ok; ++seg) {
                 const int n = min(p.tiles - p.t, count - j);
+                const bool by_tile = p.by_tile();
                 err_g = p.g;
                 ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
-                if (!p.by_tile()) {
+                Place fK{2 * j % nslots, static_cast<uint32_t>(2 * j / nslots) & 1u}, fV = fK;  // of the next K and V tile
+                fV.skip(1);
+                if (!by_tile && me_m == 0) {
                     ok = ok && full(fK);
                     if (!ok) break;
                     tc_fence_after();
@@ -309,9 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         nK.skip(2);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
-                            ok = mbar_wait(bar(Bars::kP + m), p_parity[m], s_abort);
+                            ok = mbar_wait(bar(Bars::kP + m), (n_p[m] + i) & 1, s_abort);
                             if (!ok) break;
-                            p_parity[m] ^= 1;
                             tc_fence_after();
                             issue_PV(m, fV.slot, i > 0);
                             if (next) issue_S(m, m, fK.slot);
@@ -328,47 +356,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = full(fV) && (i + 2 >= n || full(fK));
                         }
                     }
-                } else {
-                    Place sK = fK;  // of the K tile whose scores come next
-                    for (int m = 0; m < 2 && m < n && ok; ++m) {
-                        ok = full(sK);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_S(m, 0, sK.slot);
-                        mma_commit(bar(Bars::kS + m));
-                        free_slot(sK);
-                        sK.skip(2);
+                } else if (by_tile && me_m < n && ok) {
+                    const int m = me_m;
+                    if (m > 0) {
+                        fK.skip(2);
+                        fV.skip(2);
                     }
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int m = i & 1;
-                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), p_parity[m], s_abort);
+                    ok = full(fK);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_S(m, 0, fK.slot);
+                    mma_commit(bar(Bars::kS + m));
+                    free_slot(fK);
+                    for (int i = m, q = 0; i < n; i += 2, ++q) {
+                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), (n_p[m] + q) & 1, s_abort);
                         if (!ok) break;
-                        p_parity[m] ^= 1;
                         tc_fence_after();
-                        issue_PV(m, fV.slot, i > 1);
+                        issue_PV(m, fV.slot, q > 0);
                         mma_commit(bar(Bars::kO + m));
                         free_slot(fV);
-                        fV.skip(2);
+                        fV.skip(4);
+                        fK.skip(4);
                         if (i + 2 < n) {
-                            ok = full(sK);
+                            ok = full(fK);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_S(m, 0, sK.slot);
+                            issue_S(m, 0, fK.slot);
                             mma_commit(bar(Bars::kS + m));
-                            free_slot(sK);
-                            sK.skip(2);
+                            free_slot(fK);
                         }
                     }
-                    fK = sK;
                 }
+                n_p[0] += by_tile ? (n + 1) / 2 : n;
+                n_p[1] += by_tile ? n / 2 : n;
                 j += n;
                 if (j < count) p.next_unit(a);
             }
             if (!ok) my_err = 1;
             // every issued product completes before TMEM is released
-            mma_commit(bar(Bars::kDone));
+            mma_commit(bar(Bars::kDone + me_m));
             volatile int never = 0;
-            if (!mbar_wait(bar(Bars::kDone), 0, &never)) my_err = 1;
+            if (!mbar_wait(bar(Bars::kDone + me_m), 0, &never)) my_err = 1;
         }
     } else if (warp >= 4) {
         // ============================ softmax, a stream each warpgroup
@@ -486,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l_run += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
                 }
                 // V rows behind the prefix are zeroed before the product (they may hold anything, and 0 * NaN is
-                // NaN); with the rows halved the first stream does it, whose product is issued first
+                // NaN); on a tile of both streams the first does it, whose product is issued first
                 if (left < kTileKeys && (by_tile || wg == 0)) {
                     const int fV = 2 * (j + i) + 1;
                     ok = mbar_wait(bar(Bars::kFull + fV % nslots), (fV / nslots) & 1, s_abort);

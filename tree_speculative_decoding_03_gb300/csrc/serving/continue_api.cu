@@ -207,6 +207,7 @@ tsv_status tsv_prefix_decode_attn(const void* q, const void* k_cache, const void
     a.whole_o = reinterpret_cast<float*>(ws + p.whole_o);
     a.whole_m = reinterpret_cast<float*>(ws + p.whole_m);
     a.whole_l = reinterpret_cast<float*>(ws + p.whole_l);
+    a.used = reinterpret_cast<int2*>(ws + p.used);
     a.begin = reinterpret_cast<int4*>(ws + p.begin);
     a.tc_begin = reinterpret_cast<int4*>(ws + p.tc_begin);
     a.tc_start = reinterpret_cast<long long*>(ws + p.tc_start);

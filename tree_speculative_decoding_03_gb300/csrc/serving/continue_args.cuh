@@ -87,7 +87,7 @@ struct PrefixPlan {
     int lanes;  // teams the key tiles are divided between
     int tc_lanes;  // CTAs that the prefixes' tiles are divided between on the tensor cores (0: not there)
     // byte offsets of the workspace's parts, and its size
-    size_t item, group, part_o, part_m, part_l, whole_o, whole_m, whole_l, begin, tc_begin, tc_start, tc_o, tc_m, tc_l, ws_bytes;
+    size_t item, group, part_o, part_m, part_l, whole_o, whole_m, whole_l, used, begin, tc_begin, tc_start, tc_o, tc_m, tc_l, ws_bytes;
 };
 PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size, int max_blocks, bool bf16, int num_sms);
 
@@ -113,6 +113,7 @@ struct PrefixArgs {
     float* whole_o;  // [3][B * Hq][D]: units in one piece: prefixes, the sequences' own keys, prefixes' odd tiles
     float* whole_m;
     float* whole_l;
+    int2* used;           // lanes and tensor-core CTAs that have tiles
     int4* begin;          // [lanes][2]: where a lane's tiles begin: item, chunk, run of heads, tile; their number
     int4* tc_begin;       // [tc_lanes]: group, unit, tile, number of tiles
     long long* tc_start;  // [G + 1]: running sums of the prefixes' tiles on the tensor cores

@@ -68,7 +68,21 @@ __device__ __forceinline__ long long block_before(long long mine, long long* s_w
 }
 
 // Lanes that share T tiles: one tile each while there are lanes.
-__device__ __forceinline__ int stream_lanes(long long T, int lanes) { return T < lanes ? static_cast<int>(T) : lanes; }
+__device__ __forceinline__ int lanes_for(long long T, int lanes) { return T < lanes ? static_cast<int>(T) : lanes; }
+
+// SMs left to the stream while the tensor-core kernel has the others: both have work that lasts about as
+// long, and neither kernel's start and end leave the GPU empty.  Times measured at full load, in us of an SM: a
+// tile of 128 keys and up to 256 rows 2.5 (heads of 128) or 2 (64) and a unit 3 more; a tile of the stream 1.4 on one of
+// eight warps and a unit 6 more.  (One after the other: 64 samples of a 32k prompt 134 us, with the division 120; 24
+// ragged groups 162 and 140.)
+__device__ __forceinline__ int stream_sms(const PrefixArgs& a, long long T, long long tc_T) {
+    if (T == 0 || tc_T == 0) return a.tc_lanes;
+    const float units = static_cast<float>(a.B) * (a.Hkv / a.team) * ((a.gq + a.rows - 1) / a.rows);
+    const float st = (6.0f * units + 1.4f * static_cast<float>(T)) * a.team / (2 * kWarps);
+    const float tc = (a.D == 128 ? 2.5f : 2.0f) * static_cast<float>(tc_T) + 3.0f * (static_cast<float>(a.G) * a.Hkv + a.tc_lanes);
+    const int k = static_cast<int>(a.tc_lanes * st / (st + tc) + 0.5f), idle = tc_T < a.tc_lanes ? a.tc_lanes - static_cast<int>(tc_T) : 0;
+    return min(max(max(k, idle), 1), a.tc_lanes - 1);
+}
 
 // The last i in [0, n) with start[i] <= x.
 __device__ __forceinline__ int last_not_above(const long long* start, int n, long long x) {
@@ -157,7 +171,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     __syncthreads();
     // where each lane begins
     const long long T = s_start[n], tc_T = a.tc_lanes > 0 ? s_tc_start[a.G] : 0;
-    const int lanes = stream_lanes(T, a.lanes), tc_lanes = stream_lanes(tc_T, a.tc_lanes);
+    const int sms = a.tc_lanes > 1 ? stream_sms(a, T, tc_T) : 0;
+    const int lanes = lanes_for(T, sms > 0 ? min(a.lanes, max(2 * kWarps * sms / a.team, 1)) : a.lanes);
+    const int tc_lanes = lanes_for(tc_T, sms > 0 && T > 0 ? a.tc_lanes - sms : a.tc_lanes);
+    if (tid == 0) *a.used = make_int2(lanes, tc_lanes);
     for (int k = tid; k < a.lanes + a.tc_lanes; k += kPlanThreads) {
         const bool tc = k >= a.lanes;
         const int c = tc ? k - a.lanes : k, of = tc ? tc_lanes : lanes;
@@ -485,13 +502,12 @@ __device__ __forceinline__ void load_lane(const float* p, float (&x)[2]) {
 }
 // The pieces of a prefix's row that the tensor-core kernel leaves.  Units of up to 128 rows have two from
 // each CTA, one of every other tile; the odd ones are a search of their own (`odd`).
-__device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int b, int kvh, int j, bool odd) {
+__device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int b, int kvh, int j, int lanes, bool odd) {
     Pieces p;
     const int4 it = a.item[g];
     const int tiles = (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys, groups = (it.w + kPrefixTcRows - 1) / kPrefixTcRows;
     if (tiles == 0 || it.w == 0) return p;
     const long long T = a.tc_start[a.G];
-    const int lanes = stream_lanes(T, a.tc_lanes);
     const int x = (b - it.x) * a.gq + j, grp = x / kPrefixTcRows, r = x - grp * kPrefixTcRows;
     const bool by_tile = it.w - grp * kPrefixTcRows <= 128;
     if (odd && !by_tile) return p;
@@ -535,12 +551,13 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     Pieces mine;
     if (in) {
         const long long T = a.start[a.G + a.B];
+        const int2 used = *a.used;
         const int g = a.group[b];
         const bool tc = a.tc_lanes > 0;
         if (lane == 0 || (lane == 1 && !tc))
-            mine = find_pieces<TILE>(a, lane == 0 ? a.G + b : g, b, kvh, j, T, stream_lanes(T, a.lanes));
+            mine = find_pieces<TILE>(a, lane == 0 ? a.G + b : g, b, kvh, j, T, used.x);
         else if (lane < 3 && tc)
-            mine = find_tc_pieces(a, g, b, kvh, j, lane == 2);
+            mine = find_tc_pieces(a, g, b, kvh, j, used.y, lane == 2);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -698,6 +715,7 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     p.whole_o = take(whole * D * sizeof(float));
     p.whole_m = take(whole * sizeof(float));
     p.whole_l = take(whole * sizeof(float));
+    p.used = take(sizeof(int2));
     p.begin = take((size_t)p.lanes * 2 * sizeof(int4));
     p.tc_begin = take((size_t)p.tc_lanes * sizeof(int4));
     p.tc_start = take(((size_t)G + 1) * sizeof(long long));

@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and it holds few: what the issuing thread does in between (waits, places in the ring) is time that the
         // pipe stands still.  So places are counted on without divisions.  Streams on the same tiles have one
         // issuer, which keeps a stream's O and next S together; streams on every other tile one each, so
-        // that neither waits for the other's fills.  (One prompt of 32768 keys, 64 sequences: 139 us, with an issuer
-        // each 147, with divisions 150; 24 ragged groups: 166 with one issuer, 155 with two.)
+        // that neither waits for the other's fills.  (One prompt of 32768 keys, 64 sequences: 134 us, with an issuer
+        // each 147, with divisions and 64-bit descriptors 150; 24 ragged groups: 162, with one issuer 166.)
         if (lane == 0) {
             const int me_m = warp - 1;
             constexpr uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);

@@ -597,10 +597,17 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
     }
 }
 
+#ifdef TSV_TEST_HOOKS
+bool g_test_pages_cluster = true;  // test build: whether the cluster counts as resident
+#endif
+
 // Whether a cluster of eight CTAs of the kernel can be resident (a partitioned GPU may not have as
 // many SMs in one group); looked up once per device and host thread.
 template <typename K>
 bool cluster8_fits(K kernel, int& of_dev, bool& fits) {
+#ifdef TSV_TEST_HOOKS
+    if (!g_test_pages_cluster) return false;
+#endif
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (dev != of_dev) {
@@ -636,6 +643,11 @@ unsigned int_ctas(int n, int num_sms) {
 constexpr int kOneCtaIds = 8192;
 
 }  // namespace
+
+#ifdef TSV_TEST_HOOKS
+// test build only: 0 = the cluster counts as not resident
+extern "C" void tsv_test_set_pages_cluster(int on) { g_test_pages_cluster = on != 0; }
+#endif
 
 cudaError_t launch_kv_fork(const ForkArgs& a, int num_sms, cudaStream_t stream) {
     const unsigned copiers = a.shares_out == a.shares ? 0u : int_ctas(a.num_blocks, num_sms);

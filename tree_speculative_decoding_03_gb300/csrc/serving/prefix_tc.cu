@@ -79,8 +79,14 @@ struct Bars {
     static constexpr int kO = kP + 2;         // [2] its product with V is done
     static constexpr int kQ = kO + 2;         // a segment's Q rows are in shared memory
     static constexpr int kDone = kQ + 1;  // [2]
-    static constexpr int kCount = kDone + 2;
+    static constexpr int kStall = kDone + 2;  // never completed (test build: the stalled wait)
+    static constexpr int kCount = kStall + 1;
 };
+
+#ifdef TSV_TEST_HOOKS
+// test build only: one wait can be pointed at a barrier that nothing completes
+__device__ int g_test_prefix_stall = 0;
+#endif
 
 // A position in the row of tiles: tile t of the `tiles` of unit `unit` of group g.
 struct Tile {
@@ -180,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(Bars::kDone + m), 1);
         }
         mbar_init(bar(Bars::kQ), 256);
+        mbar_init(bar(Bars::kStall), 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -436,7 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = by_tile ? wg : 0; i < n; i += by_tile ? 2 : 1) {
                 if (!ok) break;
                 const int left = p.it.z - (p.t + i) * kTileKeys;  // keys from the tile's first on
+#ifdef TSV_TEST_HOOKS
+                const bool stall = g_test_prefix_stall != 0 && n_s == 0 && wg == 0;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(stall ? Bars::kStall : Bars::kS + wg), n_s & 1, s_abort));
+#else
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kS + wg), n_s & 1, s_abort));
+#endif
                 if (!ok) {
                     *s_abort = 1;
                     break;
@@ -606,6 +618,13 @@ cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef TSV_TEST_HOOKS
+// test build only: 1 = the next calls stall one wait until it gives up
+extern "C" int tsv_test_set_prefix_stall(int mode) {
+    return static_cast<int>(cudaMemcpyToSymbol(g_test_prefix_stall, &mode, sizeof(int)));
+}
+#endif
 
 cudaError_t launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
     return a.D == 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);

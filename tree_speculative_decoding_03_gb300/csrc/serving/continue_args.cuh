@@ -114,8 +114,8 @@ struct PrefixArgs {
     float* whole_m;
     float* whole_l;
     int2* used;           // lanes and tensor-core CTAs that have tiles
-    int4* begin;          // [lanes][2]: where a lane's tiles begin: item, chunk, run of heads, tile; their number
-    int4* tc_begin;       // [tc_lanes]: group, unit, tile, number of tiles
+    int4* begin;          // [lanes][3]: where a lane's tiles begin: item, chunk, run of heads, tile; the item; their number
+    int4* tc_begin;       // [tc_lanes][2]: group, unit, tile, number of tiles; the group's item
     long long* tc_start;  // [G + 1]: running sums of the prefixes' tiles on the tensor cores
     float* tc_o;          // [4 * tc_lanes][128][D]: pieces there; a CTA's first and last unit, two streams each
     float* tc_m;

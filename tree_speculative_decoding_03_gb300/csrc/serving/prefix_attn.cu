@@ -179,23 +179,25 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         const bool tc = k >= a.lanes;
         const int c = tc ? k - a.lanes : k, of = tc ? tc_lanes : lanes;
         const long long all = tc ? tc_T : T;
-        int4 p = make_int4(0, 0, 0, 0);
+        int4 p = make_int4(0, 0, 0, 0), it = p;
         int count = 0;
         if (c < of) {
             const long long x = lane_start(c, all, of);
             count = static_cast<int>(lane_start(c + 1, all, of) - x);
             const int i = last_not_above(tc ? s_tc_start : s_start, tc ? a.G : n, x);
-            const int4 it = a.item[i];
+            it = a.item[i];
             const long long off = x - (tc ? s_tc_start : s_start)[i];
             const int tiles = tc ? (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys : item_tiles<TILE>(it);
             const int unit = static_cast<int>(off / tiles), t = static_cast<int>(off - (long long)unit * tiles), runs = a.Hkv / a.team;
             p = tc ? make_int4(i, unit, t, count) : make_int4(i, unit / runs, unit % runs, t);
         }
         if (tc) {
-            a.tc_begin[c] = p;
+            a.tc_begin[2 * c] = p;
+            a.tc_begin[2 * c + 1] = it;
         } else {
-            a.begin[2 * c] = p;
-            a.begin[2 * c + 1] = make_int4(count, 0, 0, 0);
+            a.begin[3 * c] = p;
+            a.begin[3 * c + 1] = it;
+            a.begin[3 * c + 2] = make_int4(count, 0, 0, 0);
         }
     }
 }
@@ -384,11 +386,11 @@ __device__ __forceinline__ void stream_tiles(const PrefixArgs& a, uint32_t ring,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int me = blockIdx.x * kWarps + warp, which = me / a.team, member = me % a.team;
     if (which >= a.lanes) return;
-    const int4 begin = a.begin[2 * which];
-    const int n = a.begin[2 * which + 1].x;
+    const int4 begin = a.begin[3 * which], item = a.begin[3 * which + 1];
+    const int n = a.begin[3 * which + 2].x;
     if (n == 0) return;
     Place p{};
-    p.set<KEYS>(a, begin.x, a.item[begin.x]);
+    p.set<KEYS>(a, begin.x, item);
     p.chunk = begin.y;
     p.heads = begin.z;
     p.t = begin.w;
@@ -531,7 +533,7 @@ __device__ __forceinline__ Pieces find_tc_pieces(const PrefixArgs& a, int g, int
 }
 
 // `wpr` warps to a query row, eight warps a CTA.  A lane holds the place, m and l of one piece at a time, a warp
-// takes 32 pieces and then their O together, kJoinAhead rows on their way.  Warps of the same row take
+// takes up to 32 pieces and then their O together, kJoinAhead rows on their way.  Warps of the same row take
 // turns at the pieces and are joined in order, so the result does not depend on timing.  (A thread for
 // each output element that looks up and weighs every piece for itself took 49 us where this takes 10: 4096 rows of 12
 // pieces.)
@@ -568,8 +570,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     if (in && err == 0) {
         const int n0 = __shfl_sync(0xffffffffu, mine.n, 0), n1 = n0 + __shfl_sync(0xffffffffu, mine.n, 1),
                   n = n1 + __shfl_sync(0xffffffffu, mine.n, 2);
-        for (int c0 = 32 * sub; c0 < n; c0 += 32 * wpr) {
-            const int i = c0 + lane, part = i < n0 ? 0 : i < n1 ? 1 : 2, k = i - (part == 0 ? 0 : part == 1 ? n0 : n1);
+        const int run = min(32, (n + wpr - 1) / wpr);  // pieces of a warp's turn
+        for (int c0 = run * sub; c0 < n; c0 += run * wpr) {
+            const int i = lane < run ? c0 + lane : n, part = i < n0 ? 0 : i < n1 ? 1 : 2, k = i - (part == 0 ? 0 : part == 1 ? n0 : n1);
             auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, part); };
             const long long at = of(mine.at), next = of(mine.next), step = of(mine.step), rows = of(mine.rows);
             const float *pm = of_ptr(mine.m, part), *pl = of_ptr(mine.l, part), *po = of_ptr(mine.o, part);
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
             for (int c = 0; c < C; ++c) acc[c] *= f0;
             // (a piece without tiles, l = 0, leaves no O)
             const float* o = l != 0.0f ? po + row * D : nullptr;
-            const int most = min(32, n - c0);
+            const int most = min(run, n - c0);
             for (int q = 0; q < most; q += kJoinAhead) {
                 float x[kJoinAhead][C], w[kJoinAhead];
 #pragma unroll
@@ -716,8 +719,8 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     p.whole_m = take(whole * sizeof(float));
     p.whole_l = take(whole * sizeof(float));
     p.used = take(sizeof(int2));
-    p.begin = take((size_t)p.lanes * 2 * sizeof(int4));
-    p.tc_begin = take((size_t)p.tc_lanes * sizeof(int4));
+    p.begin = take((size_t)p.lanes * 3 * sizeof(int4));
+    p.tc_begin = take((size_t)p.tc_lanes * 2 * sizeof(int4));
     p.tc_start = take(((size_t)G + 1) * sizeof(long long));
     p.tc_o = take((size_t)p.tc_lanes * 512 * D * sizeof(float));
     p.tc_m = take((size_t)p.tc_lanes * 512 * sizeof(float));

@@ -92,9 +92,9 @@ __device__ int g_test_prefix_stall = 0;
 struct Tile {
     int g, unit, t, tiles, groups;  // groups: of 256 rows
     int4 it;                        // first sequence, first key (0), end, rows
-    __device__ __forceinline__ void set(const PrefixArgs& a, int group) {
+    __device__ __forceinline__ void set(int group, const int4& item) {
         g = group;
-        it = a.item[group];
+        it = item;
         tiles = (it.z + kTileKeys - 1) / kTileKeys;
         groups = (it.w + kUnitRows - 1) / kUnitRows;
     }
@@ -103,7 +103,7 @@ struct Tile {
         if (++unit < groups * a.Hkv) return;
         unit = 0;
         do {
-            set(a, g + 1);
+            set(g + 1, a.item[g + 1]);
         } while (tiles * groups == 0 && g + 1 < a.G);
     }
     __device__ __forceinline__ int head() const { return unit / groups; }
@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // the plan
     pdl_launch_dependents();
     const int me = blockIdx.x;
-    const int4 begin = a.tc_begin[me];  // group, unit, tile, tiles of this CTA
+    const int4 begin = a.tc_begin[2 * me], item = a.tc_begin[2 * me + 1];  // group, unit, tile, tiles of this CTA
     const int count = begin.w;
     Tile first{};
     if (count > 0) {
-        first.set(a, begin.x);
+        first.set(begin.x, item);
         first.unit = begin.y;
         first.t = begin.z;
     }

@@ -481,7 +481,8 @@ tsv_status tsv_kv_release_seqs(const int32_t *keep_lens, const int32_t *block_ta
  * block is both source and destination.
  * seq_err[b], overwritten: TSV_DERR_CAPACITY (blocks_held[b] outside [0, max_blocks]: the row is copied as it is and
  * its blocks do not count as live), TSV_DERR_BLOCK (a block id outside [0, num_blocks): the entry stays).
- * `workspace` holds tsv_kv_compact_workspace_size(num_blocks) bytes, 4-byte aligned.  max_blocks up to 2^27.
+ * `workspace` holds tsv_kv_compact_workspace_size(num_blocks) bytes, 4-byte aligned; calls that may overlap on the
+ * GPU need one each.  max_blocks up to 2^27.
  * ------------------------------------------------------------------------- */
 size_t tsv_kv_compact_workspace_size(int num_blocks);
 

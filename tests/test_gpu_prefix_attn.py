@@ -107,6 +107,37 @@ def test_it_is_single_token_attention_on_joined_tables(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,G", [(1023, 1), (1024, 1), (1500, 400), (2100, 2100)])
+def test_many_sequences(dtype, B, G):
+    """More items than the plan has threads, and just as many; groups of none to many."""
+    r = np.random.default_rng(B)
+    members = np.bincount(r.integers(0, G, B), minlength=G) if G > 1 else np.array([B])
+    prefix = r.integers(0, 40, G) * (r.random(G) < 0.8)
+    c = rounded(U.prefix_case(r, list(members), list(prefix), list(r.integers(0, 20, B)), 2, 1, 64, 8), dtype)
+    d = on_device(c, dtype)
+    tsv.prefix_decode_attn(**d)
+    check(c, d)
+
+
+def test_slots_past_32_bits():
+    """Rows of the cache beyond 2^31 elements: one prefix and the sequences' own keys at its far end."""
+    nb, bs, Hkv, D = 70000, 128, 4, 128  # 4.6e9 elements a cache
+    kc, vc = (torch.zeros(nb, bs, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    r = np.random.default_rng(1)
+    c = rounded(U.prefix_case(r, [3], [200], [5, 1, 140], 8, Hkv, D, bs), torch.bfloat16)
+    d = on_device(c, torch.bfloat16)
+    far = nb - len(c["k_cache"])
+    kc[far:], vc[far:] = d["k_cache"], d["v_cache"]
+    tsv.prefix_decode_attn(**{**d, "k_cache": kc, "v_cache": vc, "block_table": d["block_table"] + far})
+    check(c, d)
+    src, dst = torch.tensor([0, nb - 1], dtype=torch.int32, device="cuda"), torch.tensor([nb - 2, 1], dtype=torch.int32, device="cuda")
+    kc[0], vc[0], kc[nb - 1] = 3.0, 5.0, 7.0
+    err = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    tsv.kv_copy_blocks(kc, vc, src, dst, err)
+    assert not err.any() and (kc[nb - 2] == 3).all() and (vc[nb - 2] == 5).all() and (kc[1] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_errors(dtype):
     c = rounded(U.prefix_case(np.random.default_rng(5), [3, 2, 2, 3], [40, 16, 24, 33], [5, 1, 9, 2, 30, 1, 1, 4, 20, 3], 8, 2, 64, 8), dtype)
     nb = len(c["k_cache"])

@@ -100,24 +100,29 @@ __device__ __forceinline__ int last_not_above(const long long* start, int n, lon
 template <int TILE>
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ __align__(16) uint8_t s_plan[];
-    long long* s_start = reinterpret_cast<long long*>(s_plan);  // [G + B + 1]
-    long long* s_tc_start = s_start + a.G + a.B + 1;           // [G + 1]
-    int* s_off = reinterpret_cast<int*>(s_tc_start + a.G + 1);  // [G + 1]
+    const int n = a.G + a.B, per = (n + kPlanThreads - 1) / kPlanThreads;
+    int4* s_item = reinterpret_cast<int4*>(s_plan);  // [n] where a thread has one item
+    long long* s_start = reinterpret_cast<long long*>(s_item + (per == 1 ? n : 0));  // [n + 1]
+    long long* s_tc_start = s_start + n + 1;                                         // [G + 1]
+    int* s_off = reinterpret_cast<int*>(s_tc_start + a.G + 1);                       // [G + 1]
+    int* s_prefix = reinterpret_cast<int*>(s_tc_start);  // [G], until the sums are written there
     __shared__ long long s_warp[32], s_tc_warp[32];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
+    // (with one item a thread, its length is on its way beside the offsets)
+    const int len = per == 1 && tid >= a.G && tid < n ? a.seq_lens[tid - a.G] : 0;
     bool wrong = false;
     for (int g = tid; g <= a.G; g += kPlanThreads) {
         const int x = a.group_offsets[g];
         s_off[g] = x;
+        if (g < a.G) s_prefix[g] = a.prefix_lens[g];
         wrong |= x < 0 || x > a.B || (g == 0 && x != 0) || (g == a.G && x != a.B);
     }
     __syncthreads();
     for (int g = tid; g < a.G; g += kPlanThreads) wrong |= s_off[g] > s_off[g + 1];
     wrong = __syncthreads_or(wrong);
     const long long cap = (long long)a.max_blocks << a.bs_log2;
-    const int n = a.G + a.B, per = (n + kPlanThreads - 1) / kPlanThreads;
     long long mine = 0, tc_mine = 0;
     int4 last = make_int4(0, 0, 0, 0);
     for (int u = 0; u < per; ++u) {
@@ -125,11 +130,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         if (i >= n) break;
         int4 it = make_int4(0, 0, 0, 0);
         if (i < a.G) {
-            const int P = a.prefix_lens[i];
+            const int P = s_prefix[i];
             if (!wrong && s_off[i + 1] > s_off[i])
                 it = make_int4(s_off[i], 0, P > 0 && P <= cap ? P : 0, (s_off[i + 1] - s_off[i]) * a.gq);
         } else {
-            const int b = i - a.G, L = a.seq_lens[b];
+            const int b = i - a.G, L = per == 1 ? len : a.seq_lens[b];
             int g = 0, e = 0, P = 0;
             if (wrong) {
                 e = TSV_DERR_SEQ;
@@ -144,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
                         hi = mid;
                 }
                 g = lo;
-                P = a.prefix_lens[g];
+                P = s_prefix[g];
                 if (L < 0 || L > cap || P < 0 || P > L) e = TSV_DERR_CAPACITY;
             }
             it = make_int4(b, e ? 0 : P, e ? 0 : L, a.gq);
@@ -152,10 +157,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             a.seq_err[b] = e;
         }
         a.item[i] = it;
+        if (per == 1) s_item[i] = it;
         last = it;
         mine += (long long)item_tiles<TILE>(it) * item_units(a, i, it);
         if (i < a.G) tc_mine += tc_tiles(a, it);
     }
+    __syncthreads();  // the prefix lengths have been read
     long long at = block_before(mine, s_warp), tc_at = block_before(tc_mine, s_tc_warp);
     for (int u = 0; u < per; ++u) {
         const int i = tid * per + u;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
             const long long x = lane_start(c, all, of);
             count = static_cast<int>(lane_start(c + 1, all, of) - x);
             const int i = last_not_above(tc ? s_tc_start : s_start, tc ? a.G : n, x);
-            it = a.item[i];
+            it = per == 1 ? s_item[i] : a.item[i];
             const long long off = x - (tc ? s_tc_start : s_start)[i];
             const int tiles = tc ? (it.z + kPrefixTcKeys - 1) / kPrefixTcKeys : item_tiles<TILE>(it);
             const int unit = static_cast<int>(off / tiles), t = static_cast<int>(off - (long long)unit * tiles), runs = a.Hkv / a.team;
@@ -640,7 +647,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     if (lane == 0) to.row(0, M, sum);
 }
 
-constexpr size_t plan_smem(int B, int G) { return ((size_t)G + B + 1 + G + 1) * sizeof(long long) + ((size_t)G + 1) * sizeof(int); }
+constexpr size_t plan_smem(int B, int G) {
+    return (G + B <= kPlanThreads ? ((size_t)G + B) * sizeof(int4) : 0) + ((size_t)G + B + 1 + G + 1) * sizeof(long long) + ((size_t)G + 1) * sizeof(int);
+}
 static_assert(plan_smem(kPagesMaxSeqs, kPagesMaxSeqs) <= 232448 - 1024, "the plan's sums fit an SM's shared memory");
 
 template <typename Core>

@@ -76,7 +76,7 @@ struct Bars {
     static constexpr int kEmpty = kMaxSlots;  // [slots]
     static constexpr int kS = 2 * kMaxSlots;  // [2] scores of a stream's tile are in TMEM
     static constexpr int kP = kS + 2;         // [2] its weights are
-    static constexpr int kO = kP + 2;         // [2] its product with V is done
+    static constexpr int kO = kP + 2;         // [2] a segment's last product with V is done
     static constexpr int kQ = kO + 2;         // a segment's Q rows are in shared memory
     static constexpr int kDone = kQ + 1;  // [2]
     static constexpr int kStall = kDone + 2;  // never completed (test build: the stalled wait)
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int m = 0; m < 2; ++m) {
             mbar_init(bar(Bars::kS + m), 1);
-            mbar_init(bar(Bars::kP + m), 128);
+            mbar_init(bar(Bars::kP + m), m == 0 ? 129 : 128);  // and for stream 0, that the tile has landed
             mbar_init(bar(Bars::kO + m), 1);
             mbar_init(bar(Bars::kDone + m), 1);
         }
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================ MMA issuers.  The products are issued as fast as the tensor pipe takes them,
         // and it holds few: what the issuing thread does in between (waits, places in the ring) is time that the
         // pipe stands still.  So places are counted on without divisions.  Streams on the same tiles have one
-        // issuer, which keeps a stream's O and next S together; streams on every other tile one each, so
-        // that neither waits for the other's fills.  (One prompt of 32768 keys, 64 sequences: 134 us, with an issuer
+        // issuer, which keeps a stream's O and next S together, while the other warp waits for the fills; streams
+        // on every other tile one each, so that neither waits for the other's fills.  (One prompt of 32768 keys, 64 sequences: 134 us, with an issuer
         // each 147, with divisions and 64-bit descriptors 150; 24 ragged groups: 162, with one issuer 166.)
         if (lane == 0) {
             const int me_m = warp - 1;
@@ -327,7 +327,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
                 Place fK{2 * j % nslots, static_cast<uint32_t>(2 * j / nslots) & 1u}, fV = fK;  // of the next K and V tile
                 fV.skip(1);
-                if (!by_tile && me_m == 0) {
+                if (!by_tile && me_m == 1) {
+                    // what a tile's products read besides the weights: one arrival with those of stream 0, and
+                    // not before the last tile's have all come
+                    for (int i = 0; i < n && ok; ++i) {
+                        fK.skip(2);
+                        ok = full(fV) && (i + 1 == n || full(fK));
+                        if (!ok) break;
+                        mbar_arrive(bar(Bars::kP));
+                        fV.skip(2);
+                        ok = mbar_wait(bar(Bars::kP), (n_p[0] + i) & 1, s_abort);
+                    }
+                } else if (!by_tile) {
                     ok = ok && full(fK);
                     if (!ok) break;
                     tc_fence_after();
@@ -337,12 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     free_slot(fK);
                     fK.skip(2);
-                    ok = full(fV) && (n == 1 || full(fK));
                     for (int i = 0; i < n && ok; ++i) {
                         const bool next = i + 1 < n;
-                        Place nV = fV, nK = fK;
-                        nV.skip(2);
-                        nK.skip(2);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             ok = mbar_wait(bar(Bars::kP + m), (n_p[m] + i) & 1, s_abort);
@@ -350,18 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_after();
                             issue_PV(m, fV.slot, i > 0);
                             if (next) issue_S(m, m, fK.slot);
-                            mma_commit(bar(Bars::kO + m));
-                            if (next) mma_commit(bar(Bars::kS + m));
+                            mma_commit(bar((next ? Bars::kS : Bars::kO) + m));
                         }
                         if (!ok) break;
                         free_slot(fV);
-                        fV = nV;
-                        if (next) {
-                            free_slot(fK);
-                            fK = nK;
-                            // what the next tile's products read besides P
-                            ok = full(fV) && (i + 2 >= n || full(fK));
-                        }
+                        if (next) free_slot(fK);
+                        fV.skip(2);
+                        fK.skip(2);
                     }
                 } else if (by_tile && me_m < n && ok) {
                     const int m = me_m;
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         issue_PV(m, fV.slot, q > 0);
-                        mma_commit(bar(Bars::kO + m));
+                        if (i + 2 >= n) mma_commit(bar(Bars::kO + m));
                         free_slot(fV);
                         fV.skip(4);
                         fK.skip(4);
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = a.scale_log2;
         Tile p = first;
         bool ok = true;
-        int n_s = 0;  // tiles of this stream so far
+        int n_s = 0, n_o = 0;  // tiles and segments of this stream so far
         for (int j = 0, seg = 0; j < count; ++seg) {
             const int n = min(p.tiles - p.t, count - j);
             const bool by_tile = p.by_tile(), whole = n == p.tiles;
@@ -541,13 +543,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(bar(Bars::kP + wg));
+                if (by_tile && wg == 0 && tw == 0) mbar_arrive(bar(Bars::kP));  // (its issuer waits for the tile itself)
                 if (!ok) *s_abort = 1;
             }
             // ---- the segment's (m, l, O)
             if (ok && steps > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kO + wg), (n_s - 1) & 1, s_abort));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kO + wg), n_o & 1, s_abort));
                 tc_fence_after();
                 if (!ok) *s_abort = 1;
+                ++n_o;
             }
             if (ok && active) {
                 const long long row = whole ? place + (by_tile && wg ? 2LL * a.B * a.Hq : 0LL)

@@ -558,7 +558,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             : ((long long)me * 4 + (seg == 0 ? 0 : 2) + wg) * 128 + rl;
                 const bool in = valid && TSV_IN_BOUNDS(row, whole ? 3LL * a.B * a.Hq : 512LL * a.tc_lanes, a.seq_err + p.it.x);
                 float* o = (whole ? a.whole_o : a.tc_o) + (in ? row * D : 0);
-                if (steps > 0) {
+                // They go through shared memory, so that a warp writes whole runs of a row and not 16 bytes of 32 rows:
+                // a Q tile that no product reads any more, 16 KB or 32 (QT = 1 has none: streams of every other
+                // tile share theirs)
+                if (steps > 0 && QT == 2) {
+                    constexpr int kCols = D == 128 ? 32 : 16, kChunks = kCols / 4, kRowsIt = 32 / kChunks;  // of a pass, of a row, of a store
+                    uint8_t* stage = smem + (by_tile ? SLOT + (warp - 4) * 128 * kCols : wg * SLOT + (warp & 3) * 128 * kCols);
+                    const unsigned rows_in = __ballot_sync(0xffffffffu, in);
+                    auto swizzle = [](int row) { return kCols == 32 ? row & 7 : (row >> 1) & 3; };
+                    const int row = lane / kChunks, chunk = lane % kChunks;  // of the first store; the next are kRowsIt rows on
+                    float* to[kChunks];
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+                        to[i] = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), kRowsIt * i + row));
+#pragma unroll 1
+                    for (int q4 = 0; q4 < D / 32; ++q4) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + q4 * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int h = 0; h < 32 / kCols; ++h) {
+                            __syncwarp();
+#pragma unroll
+                            for (int c = 0; c < kChunks; ++c)
+                                *reinterpret_cast<uint4*>(stage + lane * 4 * kCols + ((c ^ swizzle(lane)) << 4)) =
+                                    make_uint4(ov[h * kCols + 4 * c], ov[h * kCols + 4 * c + 1], ov[h * kCols + 4 * c + 2], ov[h * kCols + 4 * c + 3]);
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < kChunks; ++i) {
+                                const int r = kRowsIt * i + row;
+                                if ((rows_in >> r) & 1u)
+                                    reinterpret_cast<uint4*>(to[i] + q4 * 32 + h * kCols)[chunk] =
+                                        *reinterpret_cast<const uint4*>(stage + r * 4 * kCols + ((chunk ^ swizzle(r)) << 4));
+                            }
+                        }
+                    }
+                } else if (steps > 0) {
 #pragma unroll 1
                     for (int q4 = 0; q4 < D / 32; ++q4) {
                         uint32_t ov[32];

@@ -430,12 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int x = p.row0() + r_tile + rl, sq = x / a.gq, hj = x - sq * a.gq;  // row of the item: sequence and head
             const long long place = (long long)(p.it.x + sq) * a.Hq + p.head() * a.gq + hj;  // of the row, in [B, Hq]
             if (!by_tile || wg == 0) {
-                // Q rows: 64-element halves of [128 rows x 128 B], 16-byte chunk c of row r at c ^ (r & 7)
-                const uint32_t dst = smem_u32(smem + (r_tile >> 7) * SLOT) + (tw >> 3) * 1024u + (tw & 7) * 128u;
-                const bool take = valid && TSV_IN_BOUNDS(place, (long long)a.B * a.Hq, a.seq_err + p.it.x);
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (take ? place * D : 0));
+                // Q rows: 64-element halves of [128 rows x 128 B], 16-byte chunk c of row r at c ^ (r & 7).  A warp copies
+                // the rows of its threads, whole rows at a time.
+                constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes;
+                const bool have = valid && TSV_IN_BOUNDS(place, (long long)a.B * a.Hq, a.seq_err + p.it.x);
+                const int mine = have ? static_cast<int>(place) : -1, c = lane % kRowLanes;  // (at most 2^24 places)
+                const uint32_t tile = smem_u32(smem + (r_tile >> 7) * SLOT) + (c >> 3) * kHalfBytes;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) cp_async16(dst + (c >> 3) * kHalfBytes + (((c & 7) ^ (tw & 7)) << 4), src + c, take);
+                for (int i = 0; i < 32; i += kRows) {
+                    const int r = i + lane / kRowLanes, from = __shfl_sync(0xffffffffu, mine, r), t = (tw & ~31) + r;
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (long long)max(from, 0) * D) + c;
+                    cp_async16(tile + (t >> 3) * 1024u + (t & 7) * 128u + (((c & 7) ^ (t & 7)) << 4), src, from >= 0);
+                }
                 cp_async_wait_all();
                 fence_proxy_async_smem();
             }

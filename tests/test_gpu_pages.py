@@ -66,7 +66,8 @@ def args(s):
 
 
 SIZES = [(1, 8, 1, {}), (3, 16, 40, {}), (40, 16, 300, {}), (40, 128, 300, dict(empty=0.8)), (300, 8, 700, {}), (1500, 16, 90, dict(empty=0.5, free=900)),
-         (2, 8, 30000, dict(empty=0.5)), (8, 8, 20000, dict(max_blocks=9001)), (8192, 8, 9, dict(empty=0.7, free=8000))]
+         (2, 8, 30000, dict(empty=0.5)), (8, 8, 20000, dict(max_blocks=9001)), (8192, 8, 9, dict(empty=0.7, free=8000)),
+         (600, 8, 300, dict(max_blocks=200, free=400)), (90, 16, 3000, dict(extra=17000))]
 
 
 @pytest.mark.parametrize("B,bs,max_len,kw", SIZES)

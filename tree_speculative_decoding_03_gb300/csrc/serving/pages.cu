@@ -49,9 +49,39 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
 
 // ------------------------------------------------------------------ fork
 
+// Fork i, by the threads first, first + step, ...: the source's full blocks go into the destination's row, a
+// reference each.
+__device__ __forceinline__ void fork_row(const ForkArgs& a, int i, int first, int step) {
+    const int src = a.fork_src[i];
+    if (src < 0 || (__ldcg(a.fork_err + i) & kFatal)) return;
+    const int dst = a.fork_dst[i], full = __ldcg(a.seq_lens_out + dst) >> a.bs_log2;
+    const int32_t* from = a.block_table + (long long)src * a.max_blocks;
+    int32_t* to = a.block_table + (long long)dst * a.max_blocks;
+    constexpr int U = 4;
+    bool bad = false;
+    for (int j0 = first; j0 < full; j0 += U * step) {
+        int id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = j0 + u * step < full ? from[j0 + u * step] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * step;
+            if (j >= full || !TSV_IN_BOUNDS(j, a.max_blocks, a.fork_err + i)) continue;
+            to[j] = id[u];
+            if (id[u] >= 0 && id[u] < a.num_blocks)
+                atomicAdd(a.shares_out + id[u], 1);
+            else
+                bad = true;
+        }
+    }
+    if (bad) atomicOr(a.fork_err + i, TSV_DERR_BLOCK);
+}
+
 // CTA 0 checks the forks, gives each its fresh block and writes the lists; the others copy the
-// shares when the result is another array.
-__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ ForkArgs a) {
+// shares when the result is another array.  Small calls have one CTA for it all, the rows too (7 forks of
+// 2053 tokens and their copy: 7.3 -> 6.2 us).
+constexpr int kForkSmallIds = 16384, kForkSmallEntries = 32768;  // block ids, and table entries of all forks, up to which
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ ForkArgs a, int alone) {
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -67,6 +97,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid
         if (a.held_out != a.held) a.held_out[b] = a.held[b];
         if (a.seq_lens_out != a.seq_lens) a.seq_lens_out[b] = a.seq_lens[b];
     }
+    if (alone && a.shares_out != a.shares)
+        for (int i = tid; i < a.num_blocks; i += kPlanThreads) a.shares_out[i] = a.shares[i];
     const int count = *a.free_count;
     const bool count_ok = count >= 0 && count <= a.num_blocks;
     __syncthreads();
@@ -147,37 +179,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid
         a.fork_err[i] = e;
     }
     if (tid == 0) *a.free_count_out = count_ok ? count - min(total, count) : count;
+    if (!alone) return;
+    __syncthreads();  // what the rows need is written, by this CTA
+    for (int i = tid >> 5; i < a.F; i += kPlanThreads / 32) fork_row(a, i, tid & 31, 32);
 }
 
-// One fork a CTA (blockIdx.y divides long rows): the source's full blocks go into the destination's
-// row, a reference each.
+// One fork a CTA; blockIdx.y divides long rows.
 __global__ void __launch_bounds__(kRowThreads) kv_fork_rows_kernel(const __grid_constant__ ForkArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int i = blockIdx.x, src = a.fork_src[i];
-    if (src < 0 || (a.fork_err[i] & kFatal)) return;
-    const int dst = a.fork_dst[i], full = a.seq_lens_out[dst] >> a.bs_log2;
-    const int32_t* from = a.block_table + (long long)src * a.max_blocks;
-    int32_t* to = a.block_table + (long long)dst * a.max_blocks;
-    constexpr int U = 4;
-    bool bad = false;
-    for (int j0 = (blockIdx.y * U) * kRowThreads + threadIdx.x; j0 < full; j0 += gridDim.y * U * kRowThreads) {
-        int id[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = j0 + u * kRowThreads < full ? from[j0 + u * kRowThreads] : 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u * kRowThreads;
-            if (j >= full || !TSV_IN_BOUNDS(j, a.max_blocks, a.fork_err + i)) continue;
-            to[j] = id[u];
-            if (id[u] >= 0 && id[u] < a.num_blocks)
-                atomicAdd(a.shares_out + id[u], 1);
-            else
-                bad = true;
-        }
-    }
-    if (bad) atomicOr(a.fork_err + i, TSV_DERR_BLOCK);
+    fork_row(a, blockIdx.x, blockIdx.y * kRowThreads + threadIdx.x, gridDim.y * kRowThreads);
 }
+
 
 // ------------------------------------------------------------------ scans over the block ids
 
@@ -269,19 +282,16 @@ __global__ void __launch_bounds__(256) copy_ints_kernel(int32_t* to, const int32
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) to[i] = from[i];
 }
 
-// One sequence a CTA: each released entry takes one reference off its block; -1 is none left.
-__global__ void __launch_bounds__(kPlanThreads) kv_release_count_kernel(const __grid_constant__ ReleaseArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int b = blockIdx.x, count = *a.free_count, held = a.held[b];
-    int err;
-    const int stay = kept_blocks(a, held, a.keep_lens[b], count >= 0 && count <= a.num_blocks, &err);
+// Sequence b, by the threads first, first + n, ...: each released entry takes one reference off its block; -1 is
+// none left.  True if a block id is outside the cache.
+__device__ __forceinline__ bool release_row(const ReleaseArgs& a, int b, int first, int n, int* err) {
+    const int count = *a.free_count, held = a.held[b];
+    const int stay = kept_blocks(a, held, a.keep_lens[b], count >= 0 && count <= a.num_blocks, err);
     const int32_t* row = a.block_table + (long long)b * a.max_blocks;
     bool bad = false;
     constexpr int U = 4;
-    const int n = blockDim.x;
-    if (err == 0)
-        for (int j0 = stay + threadIdx.x; j0 < held; j0 += U * n) {
+    if (*err == 0)
+        for (int j0 = stay + first; j0 < held; j0 += U * n) {
             int id[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) id[u] = j0 + u * n < held ? row[j0 + u * n] : 0;
@@ -294,17 +304,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_count_kernel(const __
                     bad = true;
             }
         }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : err;
+    return bad;
+}
+
+// One sequence a CTA.
+__global__ void __launch_bounds__(kPlanThreads) kv_release_count_kernel(const __grid_constant__ ReleaseArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    int err;
+    const bool bad = __syncthreads_or(release_row(a, blockIdx.x, threadIdx.x, blockDim.x, &err));
+    if (threadIdx.x == 0) a.seq_err[blockIdx.x] = bad ? TSV_DERR_BLOCK : err;
 }
 
 // One cluster: blocks without a reference go onto the pool in order of their ids.
 template <int CLUSTER>
-__global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __grid_constant__ ReleaseArgs a) {
+__device__ __forceinline__ void release_push(const ReleaseArgs& a) {
     __shared__ int s_warp[32];
     __shared__ int2 s_slot;
-    pdl_wait();
-    pdl_launch_dependents();
     const int tid = threadIdx.x, rank = cluster_rank<CLUSTER>();
     const IdRun run(a.num_blocks, rank, CLUSTER);
     const int count = *a.free_count;
@@ -312,7 +328,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
     int mine = 0;
     bool over = false;
     for (int id = run.first + tid; id < run.end; id += kPlanThreads) {
-        const int s = a.shares_out[id];
+        const int s = __ldcg(a.shares_out + id);
         mine += s < 0;
         over |= s < -1;
     }
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
             if (err == 0)
                 for (int j = stay + tid; j < held; j += kPlanThreads) {
                     const int id = a.block_table[(long long)b * a.max_blocks + j];
-                    hit |= id >= 0 && id < a.num_blocks && a.shares_out[id] < -1;
+                    hit |= id >= 0 && id < a.num_blocks && __ldcg(a.shares_out + id) < -1;
                 }
             if (__syncthreads_or(hit) && tid == 0) a.seq_err[b] |= TSV_DERR_POOL;
         }
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int id = IdRun::id(tile, u);
-            mark[u] = count_ok && id < run.end && a.shares_out[id] < 0;
+            mark[u] = count_ok && id < run.end && __ldcg(a.shares_out + id) < 0;
         }
         const int n = tile_ranks(mark, r, s_warp);
 #pragma unroll
@@ -362,6 +378,29 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __g
         a.held_out[b] = kept_blocks(a, a.held[b], a.keep_lens[b], count_ok, &err);
     }
     if (rank == 0 && tid == 0) *a.free_count_out = count_ok ? min(count + all.x, a.num_blocks) : count;
+}
+template <int CLUSTER>
+__global__ void __launch_bounds__(kPlanThreads) kv_release_push_kernel(const __grid_constant__ ReleaseArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    release_push<CLUSTER>(a);
+}
+
+// Small calls: one CTA for it all (8 sequences of 2053 tokens: 10 -> 4.2 us).
+constexpr int kReleaseSmallIds = 8192, kReleaseSmallEntries = 32768;  // block ids, and table entries, up to which
+__global__ void __launch_bounds__(kPlanThreads) kv_release_small_kernel(const __grid_constant__ ReleaseArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (a.shares_out != a.shares)
+        for (int i = threadIdx.x; i < a.num_blocks; i += kPlanThreads) a.shares_out[i] = a.shares[i];
+    __syncthreads();
+    for (int b = threadIdx.x >> 5; b < a.B; b += kPlanThreads / 32) {
+        int err;
+        const bool bad = __any_sync(0xffffffffu, release_row(a, b, threadIdx.x & 31, 32, &err));
+        if ((threadIdx.x & 31) == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : err;
+    }
+    __syncthreads();
+    release_push<1>(a);
 }
 
 // ------------------------------------------------------------------ compaction
@@ -650,9 +689,10 @@ extern "C" void tsv_test_set_pages_cluster(int on) { g_test_pages_cluster = on !
 #endif
 
 cudaError_t launch_kv_fork(const ForkArgs& a, int num_sms, cudaStream_t stream) {
-    const unsigned copiers = a.shares_out == a.shares ? 0u : int_ctas(a.num_blocks, num_sms);
-    cudaError_t e = launch_pdl(kv_fork_plan_kernel, dim3(1 + copiers), dim3(kPlanThreads), a.B * sizeof(int), stream, 1u, a);
-    if (e != cudaSuccess || a.F == 0) return e;
+    const bool alone = (a.shares_out == a.shares || a.num_blocks <= kForkSmallIds) && (long long)a.F * a.max_blocks <= kForkSmallEntries;
+    const unsigned copiers = alone || a.shares_out == a.shares ? 0u : int_ctas(a.num_blocks, num_sms);
+    cudaError_t e = launch_pdl(kv_fork_plan_kernel, dim3(1 + copiers), dim3(kPlanThreads), a.B * sizeof(int), stream, 1u, a, alone ? 1 : 0);
+    if (e != cudaSuccess || a.F == 0 || alone) return e;
     const int split = (a.max_blocks + 4 * kRowThreads - 1) / (4 * kRowThreads);
     return launch_pdl(kv_fork_rows_kernel, dim3(static_cast<unsigned>(a.F), static_cast<unsigned>(split < 16 ? split : 16)), dim3(kRowThreads),
                       0, stream, 1u, a);
@@ -661,6 +701,8 @@ cudaError_t launch_kv_fork(const ForkArgs& a, int num_sms, cudaStream_t stream) 
 cudaError_t launch_kv_release(const ReleaseArgs& a, int num_sms, cudaStream_t stream) {
     thread_local int of_dev = -1;
     thread_local bool fits = false;
+    if (a.num_blocks <= kReleaseSmallIds && (long long)a.B * a.max_blocks <= kReleaseSmallEntries)
+        return launch_pdl(kv_release_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1u, a);
     cudaError_t e = cudaSuccess;
     if (a.shares_out != a.shares)
         e = launch_pdl(copy_ints_kernel, dim3(int_ctas(a.num_blocks, num_sms)), dim3(256), 0, stream, 1u, a.shares_out, a.shares, a.num_blocks);

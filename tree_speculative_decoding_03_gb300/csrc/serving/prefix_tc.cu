@@ -421,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = min(p.tiles - p.t, count - j);
             const bool by_tile = p.by_tile(), whole = n == p.tiles;
             err_g = p.g;
-            // This thread's row.  A partial M tile deals its rows round over the four 32-lane quadrants of
-            // TMEM, so that all four warps share the work.
+            // This thread's row: the tile's rows in order, so that a partial tile leaves warps idle.  (A warp's time does
+            // not depend on how many rows it has; dealing them round over the four warps changes nothing.)
             const int r_tile = by_tile ? 0 : wg * 128, rows_here = min(128, p.rows() - r_tile);
-            const int rl = rows_here < 128 ? 4 * (tw & 31) + (tw >> 5) : tw;
+            const int rl = tw;
             const bool valid = rl < rows_here;
             const bool active = __any_sync(0xffffffffu, valid);
             const int x = p.row0() + r_tile + rl, sq = x / a.gq, hj = x - sq * a.gq;  // row of the item: sequence and head

@@ -208,6 +208,22 @@ def test_compact_errors():
         same(run_compact(s, in_place), want)
 
 
+@pytest.mark.parametrize("nb", [1, 2, 3, 31, 32, 33])
+@pytest.mark.parametrize("held", [0, 1])
+def test_caches_of_few_blocks(nb, held):
+    """One sequence on the last block, or none: it moves to block 0, and everything else is free."""
+    s = dict(seq_lens=np.array([5 * held], np.int32), table=np.array([[nb - 1, 99]], np.int32), held=np.array([held], np.int32),
+             shares=np.zeros(nb, np.int32), free_blocks=np.arange(nb, dtype=np.int32), free_count=nb - held)
+    want = C.compact(s["table"], s["held"], s["shares"], s["free_blocks"])
+    assert want["copy_count"] == (held if nb > 1 else 0)
+    for in_place in (False, True):
+        same(run_compact(s, in_place), want)
+    keep = np.zeros(1, np.int32)
+    a = args(s)
+    del a["seq_lens"]
+    same(run_release(s, keep, 8), C.release(keep, block_size=8, **a))
+
+
 def test_empty_batches():
     s = U.pages_state(np.random.default_rng(0), 4, 8, 30)
     s.update(table=np.zeros((0, 3), np.int32), held=np.zeros(0, np.int32), seq_lens=np.zeros(0, np.int32), shares=0 * s["shares"])

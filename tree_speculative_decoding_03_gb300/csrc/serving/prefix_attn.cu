@@ -73,12 +73,12 @@ __device__ __forceinline__ int lanes_for(long long T, int lanes) { return T < la
 // SMs left to the stream while the tensor-core kernel has the others: both have work that lasts about as
 // long, and neither kernel's start and end leave the GPU empty.  Times measured at full load, in us of an SM: a
 // tile of 128 keys and up to 256 rows 2.5 (heads of 128) or 2 (64) and a unit 3 more; a tile of the stream 1.4 on one of
-// eight warps and a unit 6 more.  (One after the other: 64 samples of a 32k prompt 134 us, with the division 120; 24
+// eight warps and a unit 9 more.  (One after the other: 64 samples of a 32k prompt 134 us, with the division then 120; 24
 // ragged groups 162 and 140.)
 __device__ __forceinline__ int stream_sms(const PrefixArgs& a, long long T, long long tc_T) {
     if (T == 0 || tc_T == 0) return a.tc_lanes;
     const float units = static_cast<float>(a.B) * (a.Hkv / a.team) * ((a.gq + a.rows - 1) / a.rows);
-    const float st = (6.0f * units + 1.4f * static_cast<float>(T)) * a.team / (2 * kWarps);
+    const float st = (9.0f * units + 1.4f * static_cast<float>(T)) * a.team / (2 * kWarps);
     const float tc = (a.D == 128 ? 2.5f : 2.0f) * static_cast<float>(tc_T) + 3.0f * (static_cast<float>(a.G) * a.Hkv + a.tc_lanes);
     const int k = static_cast<int>(a.tc_lanes * st / (st + tc) + 0.5f), idle = tc_T < a.tc_lanes ? a.tc_lanes - static_cast<int>(tc_T) : 0;
     return min(max(max(k, idle), 1), a.tc_lanes - 1);

@@ -421,20 +421,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = min(p.tiles - p.t, count - j);
             const bool by_tile = p.by_tile(), whole = n == p.tiles;
             err_g = p.g;
-            // This thread's row: the tile's rows in order, so that a partial tile leaves warps idle.  (A warp's time does
-            // not depend on how many rows it has; dealing them round over the four warps changes nothing.)
+            // This thread's row.  Up to 64 rows that both streams have lie in the tile twice, and the streams take one copy
+            // each: their warps, of which a warp's time does not depend on how many rows it has, then run on
+            // different schedulers (24 ragged groups with one key of their own 108 us, one copy 114; rows dealt round over all warps the same).
             const int r_tile = by_tile ? 0 : wg * 128, rows_here = min(128, p.rows() - r_tile);
-            const int rl = tw;
-            const bool valid = rl < rows_here;
+            const bool twice = by_tile && rows_here <= 64;
+            const int rl = tw - (twice ? 64 * wg : 0);
+            const bool valid = rl >= 0 && rl < rows_here;
             const bool active = __any_sync(0xffffffffu, valid);
-            const int x = p.row0() + r_tile + rl, sq = x / a.gq, hj = x - sq * a.gq;  // row of the item: sequence and head
-            const long long place = (long long)(p.it.x + sq) * a.Hq + p.head() * a.gq + hj;  // of the row, in [B, Hq]
+            // the place of a row, in [B, Hq]
+            auto place_of = [&](int r) {
+                const int x = p.row0() + r_tile + r, sq = x / a.gq;  // row and sequence of the item
+                return (long long)(p.it.x + sq) * a.Hq + p.head() * a.gq + (x - sq * a.gq);
+            };
+            const long long place = place_of(max(rl, 0));
             if (!by_tile || wg == 0) {
                 // Q rows: 64-element halves of [128 rows x 128 B], 16-byte chunk c of row r at c ^ (r & 7).  A warp copies
                 // the rows of its threads, whole rows at a time.
                 constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes;
-                const bool have = valid && TSV_IN_BOUNDS(place, (long long)a.B * a.Hq, a.seq_err + p.it.x);
-                const int mine = have ? static_cast<int>(place) : -1, c = lane % kRowLanes;  // (at most 2^24 places)
+                const int ql = twice ? tw & 63 : tw, c = lane % kRowLanes;
+                const long long q_place = twice ? place_of(ql) : place;
+                const bool have = ql < rows_here && TSV_IN_BOUNDS(q_place, (long long)a.B * a.Hq, a.seq_err + p.it.x);
+                const int mine = have ? static_cast<int>(q_place) : -1;  // (at most 2^24 places)
                 const uint32_t tile = smem_u32(smem + (r_tile >> 7) * SLOT) + (c >> 3) * kHalfBytes;
 #pragma unroll
                 for (int i = 0; i < 32; i += kRows) {

@@ -135,3 +135,21 @@ def test_captured_on_a_stream_of_its_own():
         torch.cuda.synchronize()
         check(x, np.arange(33), dict(logprobs=lp.cpu().numpy(), err=err.cpu().numpy(), top_ids=ids.cpu().numpy(),
                                      top_logprobs=tops.cpu().numpy()), 1.0, 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [33, 64, 65, 200, 256, 257, 400, 1024, 1025, 1500, 2999, 5000])
+def test_rows_of_few_entries(dtype, V):
+    """Rows that a warp holds, and rows with fewer slices than there are groups: random, rising, equal, few distinct,
+    masked, without a distribution, padding and wrong tokens among them."""
+    r = np.random.default_rng(V)
+    rows = [r.standard_normal(V), 9 * r.standard_normal(V), np.linspace(-30, 30, V), np.linspace(30, -30, V), np.zeros(V), r.integers(0, 3, V),
+            np.where(r.random(V) < 0.97, -np.inf, r.standard_normal(V)), np.where(np.arange(V) == V - 3, 5.0, -np.inf), np.full(V, -np.inf),
+            np.where(np.arange(V) == V - 1, np.nan, 0.0), np.where(np.arange(V) == 1, np.inf, 0.0), np.repeat(r.standard_normal(V), 7)[:V],
+            np.full(V, -1e38), 1e30 * r.standard_normal(V), np.where(r.random(V) < 0.5, 0.0, -0.0), r.standard_normal(V), r.standard_normal(V),
+            r.standard_normal(V)]
+    x = torch.from_numpy(np.stack(rows).astype(np.float32)).to(dtype).cuda()
+    tok = [V - 3] * 15 + [-1, V, 0]
+    for top, temp, entropy in ((0, 1.0, True), (1, 0.75, True), (5, 1.0, False), (20, 1.5, True), (32, 1.0, True)):
+        check(x, tok, run(x, tok, temp, top, entropy), temp, top)
+        check(x[2:3], tok[2:3], run(x[2:3], tok[2:3], temp, top, entropy), temp, top)

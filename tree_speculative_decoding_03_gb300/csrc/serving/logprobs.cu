@@ -14,7 +14,8 @@
 // 128256 bf16 with 5 / 20 / 32 alternatives 106 / 131 / 153 us, without any 91.)
 // Order: value descending (-0 and 0 are equal), then index ascending, as one 64-bit key.
 //
-// A row is taken by one CTA, or by a cluster of up to eight where there are too few rows to fill the GPU.
+// A row is taken by one CTA, by a cluster of up to eight where there are too few rows to fill the GPU, or, where it is
+// short, by a warp.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -256,11 +257,134 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int top, Key* 
     }
 }
 
+// Row t has no token: padding, or a wrong one.
+__device__ __forceinline__ void no_row(const LogprobArgs& a, int t, int token, int tid) {
+    const float x = token < 0 ? 0.0f : __int_as_float(0x7fc00000);
+    if (tid == 0) {
+        a.logprob[t] = x;
+        if (a.entropy) a.entropy[t] = x;
+        a.tok_err[t] = token < 0 ? 0 : TSV_DERR_TOKEN;
+    }
+    if (tid < a.top) {
+        a.top_ids[(long long)t * a.top + tid] = -1;
+        a.top_logprobs[(long long)t * a.top + tid] = x;
+    }
+}
+
+// Short rows, a warp a row, PER entries of it in a lane's registers; the bound comes from 64 groups of every
+// 64th entry.  (A CTA a row has too few threads with a slice for 64 groups and waits through its barriers: 4000
+// rows of 400 bf16 with 20 alternatives 141 us there, 10.7 here; 100 rows 13 and 6.)
+constexpr int kShortWarps = 4, kShortKeys = 128;
+constexpr int kShortRow = 1024;  // entries up to which a row is short: 32 a lane
+template <typename Elem, int PER>
+__global__ void __launch_bounds__(32 * kShortWarps) token_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
+    __shared__ __align__(16) float s_group[kShortWarps][kGroups];
+    __shared__ Key s_keys[kShortWarps][kShortKeys], s_best[kShortWarps][32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = static_cast<int>(blockIdx.x) * kShortWarps + warp;
+    if (t >= a.T) return;
+    const int token = a.tokens[t];
+    if (token < 0 || token >= a.V) {
+        no_row(a, t, token, lane);
+        return;
+    }
+    const Elem* x = static_cast<const Elem*>(a.logits) + (long long)t * a.stride;
+    const float xt = static_cast<float>(x[token]), c = a.inv_t * kLog2e;
+    float z[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z[i] = 32 * i + lane < a.V ? static_cast<float>(x[32 * i + lane]) : -INFINITY;
+    float mine[2] = {z[0], z[1]};  // the lane's two groups
+#pragma unroll
+    for (int i = 2; i < PER; ++i) mine[i & 1] = max_nan(mine[i & 1], z[i]);
+    float m = max_nan(mine[0], mine[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float nan = __int_as_float(0x7fc00000);
+    if (!(m < INFINITY && m > -INFINITY)) {  // a NaN or +inf, or no finite logit: no distribution
+        if (lane == 0) {
+            a.logprob[t] = nan;
+            if (a.entropy) a.entropy[t] = nan;
+            a.tok_err[t] = TSV_DERR_NONFINITE;
+        }
+        if (lane < a.top) {
+            a.top_ids[(long long)t * a.top + lane] = -1;
+            a.top_logprobs[(long long)t * a.top + lane] = nan;
+        }
+        return;
+    }
+    float s = 0.0f, w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const float d = fmaxf((z[i] - m) * c, kFloor), p = ex2(d);
+        s += p;
+        w = fmaf(p, d, w);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        w += __shfl_xor_sync(0xffffffffu, w, o);
+    }
+    const float log_s = logf(s);
+    if (lane == 0) {
+        a.logprob[t] = (xt - m) * a.inv_t - log_s;
+        if (a.entropy) a.entropy[t] = log_s - kLn2 * (w / s);
+        a.tok_err[t] = 0;
+    }
+    if (a.top == 0) return;
+    // the bound: the top-th largest of the group maxima
+    s_group[warp][lane] = mine[0];
+    s_group[warp][32 + lane] = mine[1];
+    __syncwarp();
+    int r0 = 0, r1 = 0;
+#pragma unroll 4
+    for (int j = 0; j < kGroups; ++j) {
+        const float o = s_group[warp][j];
+        r0 += o > mine[0] || (o == mine[0] && j < lane);
+        r1 += o > mine[1] || (o == mine[1] && j < 32 + lane);
+    }
+    const unsigned at0 = __ballot_sync(0xffffffffu, r0 == a.top - 1), at1 = __ballot_sync(0xffffffffu, r1 == a.top - 1);
+    const float bound = __shfl_sync(0xffffffffu, at0 ? mine[0] : mine[1], __ffs(at0 ? at0 : at1) - 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = 32 * i + lane < a.V && z[i] >= bound;
+        const unsigned all = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(all & ((1u << lane) - 1));
+        if (in && at < kShortKeys) s_keys[warp][at] = make_key(z[i], static_cast<uint32_t>(32 * i + lane));
+        n += __popc(all);
+    }
+    __syncwarp();
+    if (n <= kShortKeys) {
+        for (int i = lane; i < n; i += 32) {
+            const Key k = s_keys[warp][i];
+            int r = 0;
+            for (int j = 0; j < n; ++j) r += s_keys[warp][j] > k;
+            if (r < a.top) s_best[warp][r] = k;
+        }
+    } else {  // ties: the best in order, one a lane
+        Best best;
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i) {
+            const int at = 32 * i + lane;
+            const float y = at < a.V ? static_cast<float>(x[at]) : -INFINITY;
+            best.add(at < a.V && y >= bound ? make_key(y, static_cast<uint32_t>(at)) : 0, a.top);
+        }
+        s_best[warp][lane] = best.key;
+    }
+    __syncwarp();
+    if (lane < a.top) {
+        const Key k = s_best[warp][lane];
+        a.top_ids[(long long)t * a.top + lane] = key_index(k);
+        a.top_logprobs[(long long)t * a.top + lane] = (key_value(k) - m) * a.inv_t - log_s;
+    }
+}
+
 // THREADS: 256, four CTAs an SM, where there is a row for each CTA, so that a row's end overlaps other rows' loads
 // (2000 rows of 128256 bf16 logits); 512 in a cluster.
 template <typename Elem, int CLUSTER, bool ENTROPY>
 __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER)) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    constexpr int N = Vec<Elem>::N, kThreads = threads_of(CLUSTER), kWarps = kThreads / 32, kGroupThreads = kThreads / kGroups;
+    constexpr int N = Vec<Elem>::N, kThreads = threads_of(CLUSTER), kWarps = kThreads / 32;
     __shared__ float s_m[kWarps], s_s[kWarps], s_w[kWarps];
     __shared__ __align__(16) float s_group[kGroups];
     __shared__ Stats s_stats;   // of the CTA
@@ -275,18 +399,7 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     const int t = static_cast<int>(blockIdx.x / CLUSTER);
     const int token = a.tokens[t];
     if (token < 0 || token >= a.V) {  // padding, or a wrong token: the same in every CTA of the cluster
-        if (rank == 0) {
-            const float x = token < 0 ? 0.0f : __int_as_float(0x7fc00000);
-            if (tid == 0) {
-                a.logprob[t] = x;
-                if (ENTROPY) a.entropy[t] = x;
-                a.tok_err[t] = token < 0 ? 0 : TSV_DERR_TOKEN;
-            }
-            if (tid < a.top) {
-                a.top_ids[(long long)t * a.top + tid] = -1;
-                a.top_logprobs[(long long)t * a.top + tid] = x;
-            }
-        }
+        if (rank == 0) no_row(a, t, token, tid);
         return;
     }
     const Elem* x = static_cast<const Elem*>(a.logits) + (long long)t * a.stride;
@@ -354,10 +467,15 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
         s_w[warp] = st.w;
     }
     if (a.top > 0) {
+        // groups of neighbours, as few as make 64 groups of the threads that have a slice: then half of the groups
+        // hold entries wherever 32 threads do (4000 rows of 3000 bf16 with 32 alternatives and four threads a
+        // group, most groups empty and the bound -inf: 462 us; 52)
+        const int threads = min((end - begin + kAhead - 1) / kAhead, kThreads);
+        int log2 = 0;
+        while (threads > kGroups << log2) ++log2;
         float g = slice_max;
-#pragma unroll
-        for (int o = 1; o < kGroupThreads; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if (tid % kGroupThreads == 0) s_group[tid / kGroupThreads] = g;
+        for (int o = 1; o < 1 << log2; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if ((tid & ((1 << log2) - 1)) == 0 && tid >> log2 < kGroups) s_group[tid >> log2] = g;
     }
     bad = __syncthreads_or(bad);
     if (warp == 0) {
@@ -508,8 +626,17 @@ cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t stream) {
     return launch_pdl(kernel, dim3(static_cast<unsigned>(a.T) * CLUSTER), dim3(threads_of(CLUSTER)), 0, stream, static_cast<unsigned>(CLUSTER), a);
 }
 
+template <typename Elem, int PER>
+cudaError_t launch_short(const LogprobArgs& a, cudaStream_t stream) {
+    return launch_pdl(token_logprobs_short_kernel<Elem, PER>, dim3(static_cast<unsigned>((a.T + kShortWarps - 1) / kShortWarps)),
+                      dim3(32 * kShortWarps), 0, stream, 1u, a);
+}
+
 template <typename Elem>
 cudaError_t launch_type(const LogprobArgs& a, int num_sms, cudaStream_t stream) {
+    if (a.V <= 64) return launch_short<Elem, 2>(a, stream);
+    if (a.V <= 256) return launch_short<Elem, 8>(a, stream);
+    if (a.V <= kShortRow) return launch_short<Elem, kShortRow / 32>(a, stream);
     // CTAs a row: as many as still find a place (two an SM) and have a vector for each thread
     const long long vecs = ((long long)a.V + Vec<Elem>::N - 1) / Vec<Elem>::N;
     int n = 1;

@@ -518,7 +518,8 @@ tsv_status tsv_kv_copy_blocks(void *k_cache, void *v_cache, const int32_t *copy_
  * that may overlap on the GPU need one each.  out and lse must not overlap the inputs.
  * seq_err[b]: TSV_DERR_SEQ (all sequences: the offsets are not as above), TSV_DERR_CAPACITY (L_b < 0 or
  * > max_blocks * block_size, P_g < 0 or > L_b), TSV_DERR_BLOCK (a block id that covers one of the sequence's keys,
- * the shared ones included, outside [0, num_blocks)); rows of a flagged sequence are NaN.
+ * the shared ones included, outside [0, num_blocks)), TSV_DERR_TIMEOUT (bf16: a wait gave up; a group's sequences
+ * are told together, and those of other groups with them); rows of a flagged sequence are NaN.
  * D in {64, 128}; Hq % Hkv == 0; block_size a power of two in [8, 128]; B and G up to 8192;
  * max_blocks * block_size and num_blocks * block_size up to 2^30, B * Hq up to 2^24; scale > 0, scale * log2(e)
  * finite.

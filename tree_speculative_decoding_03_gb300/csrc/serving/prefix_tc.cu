@@ -22,7 +22,8 @@
 // (the second part's products take half as long again as the others together; with one part alone the result is off by
 // another rounding of bf16).  Both lie in the columns of S that the weights came from.
 //
-// Every wait is bounded; a wait that gives up sets TSV_DERR_TIMEOUT for the group's sequences.
+// Every wait is bounded.  One that gives up sets TSV_DERR_TIMEOUT for the sequences of all groups from its own
+// to the CTA's last: a CTA does nothing more after it.
 #include <cuda_bf16.h>
 
 #include "../common.cuh"
@@ -84,7 +85,7 @@ struct Bars {
 };
 
 #ifdef TSV_TEST_HOOKS
-// test build only: one wait can be pointed at a barrier that nothing completes
+// test build only: the wait for each CTA's n-th tile of the first stream is pointed at a barrier that nothing completes
 __device__ int g_test_prefix_stall = 0;
 #endif
 
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
+    int* s_lost = reinterpret_cast<int*>(smem + lay.bars + 8 * Bars::kCount + 8);  // first group in which a wait gave up
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [=](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(Bars::kQ), 256);
         mbar_init(bar(Bars::kStall), 1);
         *s_abort = 0;
+        *s_lost = a.G;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     int my_err = 0;
-    int err_g = first.g;  // the group whose sequences are told if a wait of this thread gives up
+    int err_g = first.g;  // the group in which a wait of this thread is or gave up
 
     if (warp < 4) regs_dec<kRegsProducer>();
     if (count == 0) {
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0, seg = 0; j < count; ++seg) {
             const int n = min(p.tiles - p.t, count - j);
             const bool by_tile = p.by_tile(), whole = n == p.tiles;
-            err_g = p.g;
+            if (ok) err_g = p.g;
             // This thread's row.  Up to 64 rows that both streams have lie in the tile twice, and the streams take one copy
             // each: their warps, of which a warp's time does not depend on how many rows it has, then run on
             // different schedulers (24 ragged groups with one key of their own 108 us, one copy 114; rows dealt round over all warps the same).
@@ -460,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const int left = p.it.z - (p.t + i) * kTileKeys;  // keys from the tile's first on
 #ifdef TSV_TEST_HOOKS
-                const bool stall = g_test_prefix_stall != 0 && n_s == 0 && wg == 0;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(stall ? Bars::kStall : Bars::kS + wg), n_s & 1, s_abort));
+                const bool stall = g_test_prefix_stall == n_s + 1 && wg == 0;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(stall ? Bars::kStall : Bars::kS + wg), stall ? 0 : n_s & 1, s_abort));
 #else
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(Bars::kS + wg), n_s & 1, s_abort));
 #endif
@@ -636,12 +639,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (my_err) {
         *s_abort = 1;
-        const int4 it = a.item[err_g];
-        for (int q = 0; q < it.w / a.gq; ++q) atomicOr(a.seq_err + it.x + q, TSV_DERR_TIMEOUT);
+        atomicMin(s_lost, err_g);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*s_lost < a.G) {
+        const int4 from = a.tc_begin[2 * blockIdx.x];
+        Tile p{};
+        p.set(from.x, a.tc_begin[2 * blockIdx.x + 1]);
+        p.unit = from.y;
+        p.t = from.z;
+        for (int left = from.w; left > 0;) {
+            if (p.g >= *s_lost)
+                for (int q = threadIdx.x; q < p.it.w / a.gq; q += kThreads) atomicOr(a.seq_err + p.it.x + q, TSV_DERR_TIMEOUT);
+            left -= p.tiles - p.t;
+            if (left > 0) p.next_unit(a);
+        }
+    }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
@@ -673,7 +688,7 @@ cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
 }  // namespace
 
 #ifdef TSV_TEST_HOOKS
-// test build only: 1 = the next calls stall one wait until it gives up
+// test build only: n = the next calls stall the wait for the n-th tile of each CTA's first stream until it gives up; 0 = none
 extern "C" int tsv_test_set_prefix_stall(int mode) {
     return static_cast<int>(cudaMemcpyToSymbol(g_test_prefix_stall, &mode, sizeof(int)));
 }

@@ -30,7 +30,10 @@ __device__ __forceinline__ bool checked_in_bounds(long long i, long long n, int3
 // Programmatic dependent launch: every kernel of the library lets the next kernel in the
 // stream start launching early (pdl_launch_dependents) and waits for the previous one to
 // complete, with its writes visible, before reading anything (pdl_wait).  Without the
-// launch attribute both are no-ops.
+// launch attribute both are no-ops.  What an earlier kernel has written is promised to a kernel that
+// has waited, not to one whose predecessor has.  (Two kernels read inputs of their call ahead of
+// their own wait, none of which a kernel of the call writes: the tree attention's, the lengths, the tables, Q and K/V of
+// the prefix; the join of the single-token attention, the lengths, past the L1 cache.)
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -59,6 +62,14 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.attrs = attr;
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// 2^x, 0 below the normal numbers
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Validates one sequence's tree: parent[0] == -1 and 0 <= parent[i] < i.

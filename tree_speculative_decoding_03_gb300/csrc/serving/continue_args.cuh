@@ -85,7 +85,7 @@ struct PrefixPlan {
     int rows;   // query rows of a unit of the stream
     int team;   // warps that go through the same keys, each with a kv head of its own
     int lanes;  // teams the key tiles are divided between
-    int tc_lanes;  // CTAs that the prefixes' tiles are divided between on the tensor cores (0: not there)
+    int tc_lanes;  // CTAs of the bf16 kernel (0: fp32), first those of the prefixes' tiles, then those of the stream
     // byte offsets of the workspace's parts, and its size
     size_t item, group, part_o, part_m, part_l, whole_o, whole_m, whole_l, used, begin, tc_begin, tc_start, tc_o, tc_m, tc_l, ws_bytes;
 };
@@ -115,7 +115,8 @@ struct PrefixArgs {
     float* whole_l;
     int2* used;           // lanes and tensor-core CTAs that have tiles
     int4* begin;          // [lanes][3]: where a lane's tiles begin: item, chunk, run of heads, tile; the item; their number
-    int4* tc_begin;       // [tc_lanes][2]: group, unit, tile, number of tiles; the group's item
+    int4* tc_begin;       // [tc_lanes][2]: group, unit, tile, number of tiles; the group's item.  No tiles: the first of its
+                          // warps of the stream and their number, -, 0
     long long* tc_start;  // [G + 1]: running sums of the prefixes' tiles on the tensor cores
     float* tc_o;          // [4 * tc_lanes][128][D]: pieces there; a CTA's first and last unit, two streams each
     float* tc_m;

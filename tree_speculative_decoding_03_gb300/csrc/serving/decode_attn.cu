@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(ROWS* GROUPS* D / 4) decode_join_kernel(const 
         const long long h = (long long)b * a.Hq + (unit / a.groups) * a.G + row0 + r;
         const ToResult<Elem, D> to{static_cast<Elem*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, bad != 0};
         const float inv = to.factor(sum);
-        to.two(0, d, acc.x * inv, acc.y * inv);
-        to.two(0, d + 2, acc.z * inv, acc.w * inv);
+        store2(to.base(0) + d, acc.x * inv, acc.y * inv);
+        store2(to.base(0) + d + 2, acc.z * inv, acc.w * inv);
         if (d == 0) to.row(0, M, sum);
         if (d == 0 && r == 0 && unit == 0) a.seq_err[b] = bad ? TSV_DERR_BLOCK : 0;
     }

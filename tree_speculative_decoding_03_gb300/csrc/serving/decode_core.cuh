@@ -17,7 +17,6 @@ constexpr int kFewLanes = 64;  // up to here two tiles do (one sequence of 256 f
 // Keys of a tile: its K and V rows are 8 KB.
 __host__ __device__ constexpr int tile_keys(bool bf16, int D) { return 4096 / (D * (bf16 ? 2 : 4)); }
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory; `take` false writes zeros and reads nothing
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
@@ -46,11 +45,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
@@ -64,6 +58,9 @@ __device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uin
     *hi = __byte_perm(h0, h1, 0x7632);
     *lo = pack_bf16(w0 - __uint_as_float(h0 & 0xffff0000u), w1 - __uint_as_float(h1 & 0xffff0000u));
 }
+// two neighbours of a row of results, for bf16 with their one rounding
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) { *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y); }
 // the reference point of the exponentials; a row that has seen only -inf scores keeps P = 0
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -96,13 +93,14 @@ struct Bf16Core {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             const int r0 = 16 * t + (lane >> 2), r1 = r0 + 8, c = (lane & 3) * 2;
+            const Elem *q0 = q(r0) + c, *q1 = q(r1) + c;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const int d = kk * 16 + c;
-                qf[t][kk][0] = r0 < nrows ? *reinterpret_cast<const uint32_t*>(q(r0) + d) : 0u;
-                qf[t][kk][1] = r1 < nrows ? *reinterpret_cast<const uint32_t*>(q(r1) + d) : 0u;
-                qf[t][kk][2] = r0 < nrows ? *reinterpret_cast<const uint32_t*>(q(r0) + d + 8) : 0u;
-                qf[t][kk][3] = r1 < nrows ? *reinterpret_cast<const uint32_t*>(q(r1) + d + 8) : 0u;
+                const int d = kk * 16;
+                qf[t][kk][0] = r0 < nrows ? *reinterpret_cast<const uint32_t*>(q0 + d) : 0u;
+                qf[t][kk][1] = r1 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + d) : 0u;
+                qf[t][kk][2] = r0 < nrows ? *reinterpret_cast<const uint32_t*>(q0 + d + 8) : 0u;
+                qf[t][kk][3] = r1 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) : 0u;
             }
         }
     }
@@ -216,8 +214,9 @@ struct Bf16Core {
                 if (row >= nrows) continue;
                 if ((lane & 3) == 0) sink.row(row, m[t][r], sum);
                 const float inv = sink.factor(sum);
+                auto* to = sink.base(row) + (lane & 3) * 2;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) sink.two(row, 8 * i + (lane & 3) * 2, o[t][i][2 * r] * inv, o[t][i][2 * r + 1] * inv);
+                for (int i = 0; i < D / 8; ++i) store2(to + 8 * i, o[t][i][2 * r] * inv, o[t][i][2 * r + 1] * inv);
             }
     }
 };
@@ -253,9 +252,10 @@ struct F32Core {
         const int i = (threadIdx.x & 31) % LPK;
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
+            const float* row = q(r) + i * 4;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 x = r < nrows ? *reinterpret_cast<const float4*>(q(r) + (i + h * LPK) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x = r < nrows ? *reinterpret_cast<const float4*>(row + h * LPK * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
                 qr[r][4 * h] = x.x;
                 qr[r][4 * h + 1] = x.y;
                 qr[r][4 * h + 2] = x.z;
@@ -369,8 +369,9 @@ struct F32Core {
         for (int r = 0; r < RR; ++r) {
             if (r >= nrows) continue;
             const float inv = sink.factor(scratch[r]);
+            auto* to = sink.base(r) + lane * DV;
 #pragma unroll
-            for (int d = 0; d < DV; d += 2) sink.two(r, lane * DV + d, o[r][d] * inv, o[r][d + 1] * inv);
+            for (int d = 0; d < DV; d += 2) store2(to + d, o[r][d] * inv, o[r][d + 1] * inv);
         }
         __syncwarp();
     }
@@ -410,12 +411,7 @@ struct ToResult {
         if (lse != nullptr) lse[r] = bad ? __int_as_float(0x7fc00000) : (m + log2f(l)) * kLn2;
     }
     __device__ __forceinline__ float factor(float l) const { return bad ? __int_as_float(0x7fc00000) : 1.0f / l; }
-    __device__ __forceinline__ void two(int r, int d, float x, float y) const { store2(out + r * D + d, x, y); }
-    // the one rounding of the result
-    static __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
-    static __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
-    }
+    __device__ __forceinline__ Elem* base(int r) const { return out + r * D; }
 };
 template <int D>
 struct ToSlot {
@@ -425,9 +421,7 @@ struct ToSlot {
         l[r] = l_;
     }
     __device__ __forceinline__ float factor(float) const { return 1.0f; }
-    __device__ __forceinline__ void two(int r, int d, float x, float y) const {
-        *reinterpret_cast<float2*>(o + r * D + d) = make_float2(x, y);
-    }
+    __device__ __forceinline__ float* base(int r) const { return o + r * D; }
 };
 
 }  // namespace

@@ -38,11 +38,6 @@ static_assert(kGroups >= kMaxTop && kMaxTop <= 32, "a group for each alternative
 
 typedef unsigned long long Key;  // 0: none
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));

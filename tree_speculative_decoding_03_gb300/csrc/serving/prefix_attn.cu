@@ -9,38 +9,29 @@
 // keys, with its own rows, are items of one schedule, and the last kernel joins what the pieces of
 // both leave.
 //
-// Kernels: a plan (one CTA: checks, items, running sums of their tiles), for bf16 the prefixes on the tensor
-// cores (prefix_tc.cu), the stream of the other tiles, the join.  Lengths stay on the device.  An item's units are (group of query rows, kv head); `team` warps take
-// neighbouring kv heads of the same rows and keys together.  The tiles of all units, item after item,
-// form one row that is divided evenly between `lanes` teams.  A segment that is a whole unit leaves its
-// (m, l, O) at its rows' places, a piece in one of its warp's two slots.
+// Kernels: a plan (one CTA: checks, items, running sums of their tiles), the tiles, the join.  For bf16 the kernel of
+// the tiles (prefix_tc.cu) has CTAs that take the prefixes to the tensor cores and CTAs for the stream of the sequences' own
+// keys; for fp32 it is the stream alone, the prefixes' tiles among the others.  Lengths stay on the device.  An item's units in the stream
+// are (group of query rows, kv head); `team` warps take neighbouring kv heads of the same rows and keys
+// together.  The tiles of all units, item after item, form one row that is divided evenly between `lanes` teams.  A
+// segment that is a whole unit leaves its (m, l, O) at its rows' places, a piece in one of its warp's two slots.
 #include <cuda_bf16.h>
 
 #include "../common.cuh"
 #include "continue_args.cuh"
-#include "decode_core.cuh"
+#include "prefix_stream.cuh"
 
 namespace tsv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kStreamWarps / 2;  // of a CTA of the fp32 stream, two on an SM
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRingBytes = 24576;  // of a warp: eight rings and the block's share fill an SM's shared memory
-constexpr int kMaxTeam = 8;
-constexpr int kScratch = 136;  // floats of a warp beside its ring
+constexpr size_t kSmem = (size_t)kWarps * (kRingBytes + kScratch * sizeof(float));
+constexpr int kMaxTeam = kStreamWarps;
 constexpr int kPlanThreads = 1024;
 
 // ------------------------------------------------------------------ plan
 
-// Tiles of an item: from the tile that holds its first key.
-template <int TILE>
-__device__ __forceinline__ int item_tiles(const int4& it) {
-    return it.z > it.y ? (it.z + TILE - 1) / TILE - it.y / TILE : 0;
-}
-// Units of item i in the stream, a team at a time.  With a tensor-core kernel the prefixes are that one's.
-__device__ __forceinline__ int item_units(const PrefixArgs& a, int i, const int4& it) {
-    return i < a.G && a.tc_lanes > 0 ? 0 : ((it.w + a.rows - 1) / a.rows) * (a.Hkv / a.team);
-}
 // Tiles of a prefix on the tensor cores, over all its units.
 __device__ __forceinline__ long long tc_tiles(const PrefixArgs& a, const int4& it) {
     return (long long)((it.z + kPrefixTcKeys - 1) / kPrefixTcKeys) * ((it.w + kPrefixTcRows - 1) / kPrefixTcRows) * a.Hkv;
@@ -70,15 +61,14 @@ __device__ __forceinline__ long long block_before(long long mine, long long* s_w
 // Lanes that share T tiles: one tile each while there are lanes.
 __device__ __forceinline__ int lanes_for(long long T, int lanes) { return T < lanes ? static_cast<int>(T) : lanes; }
 
-// SMs left to the stream while the tensor-core kernel has the others: both have work that lasts about as
-// long, and neither kernel's start and end leave the GPU empty.  Times measured at full load, in us of an SM: a
+// SMs left to the stream while the tensor-core CTAs have the others: both have work that lasts about as long.  Times measured at full load, in us of an SM: a
 // tile of 128 keys and up to 256 rows 2.5 (heads of 128) or 2 (64) and a unit 3 more; a tile of the stream 1.4 on one of
 // eight warps and a unit 9 more.  (One after the other: 64 samples of a 32k prompt 134 us, with the division then 120; 24
 // ragged groups 162 and 140.)
 __device__ __forceinline__ int stream_sms(const PrefixArgs& a, long long T, long long tc_T) {
     if (T == 0 || tc_T == 0) return a.tc_lanes;
     const float units = static_cast<float>(a.B) * (a.Hkv / a.team) * ((a.gq + a.rows - 1) / a.rows);
-    const float st = (9.0f * units + 1.4f * static_cast<float>(T)) * a.team / (2 * kWarps);
+    const float st = (9.0f * units + 1.4f * static_cast<float>(T)) * a.team / kStreamWarps;
     const float tc = (a.D == 128 ? 2.5f : 2.0f) * static_cast<float>(tc_T) + 3.0f * (static_cast<float>(a.G) * a.Hkv + a.tc_lanes);
     const int k = static_cast<int>(a.tc_lanes * st / (st + tc) + 0.5f), idle = tc_T < a.tc_lanes ? a.tc_lanes - static_cast<int>(tc_T) : 0;
     return min(max(max(k, idle), 1), a.tc_lanes - 1);
@@ -178,8 +168,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     __syncthreads();
     // where each lane begins
     const long long T = s_start[n], tc_T = a.tc_lanes > 0 ? s_tc_start[a.G] : 0;
-    const int sms = a.tc_lanes > 1 ? stream_sms(a, T, tc_T) : 0;
-    const int lanes = lanes_for(T, sms > 0 ? min(a.lanes, max(2 * kWarps * sms / a.team, 1)) : a.lanes);
+    const int sms = a.tc_lanes > 0 ? stream_sms(a, T, tc_T) : 0;
+    const int lanes = lanes_for(T, sms > 0 ? min(a.lanes, kStreamWarps * sms / a.team) : a.lanes);
     const int tc_lanes = lanes_for(tc_T, sms > 0 && T > 0 ? a.tc_lanes - sms : a.tc_lanes);
     if (tid == 0) *a.used = make_int2(lanes, tc_lanes);
     for (int k = tid; k < a.lanes + a.tc_lanes; k += kPlanThreads) {
@@ -188,7 +178,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         const long long all = tc ? tc_T : T;
         int4 p = make_int4(0, 0, 0, 0), it = p;
         int count = 0;
-        if (c < of) {
+        if (tc && c >= tc_lanes) {  // the stream's: its warps, evenly on the CTAs that have it
+            const int warps = (lanes * a.team + a.tc_lanes - tc_lanes - 1) / (a.tc_lanes - tc_lanes);
+            p = make_int4((c - tc_lanes) * warps, warps, 0, 0);
+        } else if (c < of) {
             const long long x = lane_start(c, all, of);
             count = static_cast<int>(lane_start(c + 1, all, of) - x);
             const int i = last_not_above(tc ? s_tc_start : s_start, tc ? a.G : n, x);
@@ -209,246 +202,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     }
 }
 
-// ------------------------------------------------------------------ the schedule
-
-// A position in the row of tiles: tile t of the `tiles` of item i, for its `chunk`-th group of rows and
-// the team's `heads`-th run of kv heads.
-struct Place {
-    int i, chunk, heads, t, tiles, units;
-    int4 it;     // first sequence, first key, end, rows
-    int4 ahead;  // the next item, on its way while this one lasts
-    template <int TILE>
-    __device__ __forceinline__ void set(const PrefixArgs& a, int item, const int4& now) {
-        i = item;
-        it = now;
-        if (item + 1 < a.G + a.B) ahead = a.item[item + 1];
-        tiles = item_tiles<TILE>(it);
-        units = item_units(a, i, it);
-    }
-    template <int TILE>
-    __device__ __forceinline__ void next(const PrefixArgs& a) {
-        if (++t < tiles) return;
-        t = 0;
-        ++heads;
-        if (heads * a.team < a.Hkv) return;
-        heads = 0;
-        if (++chunk * a.rows < it.w) return;
-        chunk = 0;
-        do {
-            set<TILE>(a, i + 1, ahead);
-        } while (tiles * units == 0 && i + 1 < a.G + a.B);
-    }
-    __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return heads * a.team + member; }
-    __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk * a.rows); }
-};
-
-// ------------------------------------------------------------------ the stream of tiles
-
-template <typename Core>
-__host__ __device__ constexpr int stages_of() { return kRingBytes / (2 * Core::KEYS * Core::ROWB); }
-constexpr size_t kSmem = (size_t)kWarps * (kRingBytes + kScratch * sizeof(float));
-
-// A warp's stream of tiles: the copies run STAGES - 1 tiles ahead and the block ids one more.
-template <typename Core>
-struct Stream {
-    using Elem = typename Core::Elem;
-    static constexpr int D = Core::D, KEYS = Core::KEYS, STAGES = stages_of<Core>(), RUNS = KEYS / 8;
-    static constexpr uint32_t HALF = KEYS * Core::ROWB, STAGE = 2 * HALF;
-    static constexpr int LANES_ROW = Core::CH < 32 ? Core::CH : 32, ROWS_IT = 32 / LANES_ROW;
-    const PrefixArgs& a;
-    const uint32_t ring;
-    const int member, row_elems, lrow, lane_elems, lch;
-    Place f;           // the tile whose ids were fetched last
-    int ids[RUNS];     // its blocks (8 keys lie in one block); all lanes hold the same
-    uint32_t bad = 0;  // stages holding a tile with a block id outside the cache
-    int left;          // tiles not yet on their way
-    int fill = 0, stage = 0;
-
-    __device__ __forceinline__ Stream(const PrefixArgs& args, uint32_t ring_, int member_, const Place& p, int n)
-        : a(args), ring(ring_), member(member_), row_elems(args.Hkv * D), lrow((threadIdx.x & 31) / LANES_ROW),
-          lane_elems(lrow * row_elems + ((threadIdx.x & 31) % LANES_ROW) * (16 / (int)sizeof(Elem))), lch((threadIdx.x & 31) % LANES_ROW),
-          f(p), left(n) {}
-
-    // the tile's first key; the item's first key may lie behind it
-    __device__ __forceinline__ static int first_key(const Place& p) { return (p.it.y / KEYS + p.t) * KEYS; }
-    __device__ __forceinline__ bool holds(int key) const { return key < f.it.z && key + 8 > f.it.y; }
-    __device__ __forceinline__ void fetch() {
-        const int32_t* bt = a.block_table + (long long)f.it.x * a.max_blocks;
-#pragma unroll
-        for (int u = 0; u < RUNS; ++u) {
-            const int key = first_key(f) + 8 * u;
-            ids[u] = holds(key) ? (TSV_IN_BOUNDS(key >> a.bs_log2, a.max_blocks, nullptr) ? bt[key >> a.bs_log2] : -1) : 0;
-        }
-    }
-    // sends tile f on its way into stage `fill`, then fetches the next tile's ids
-    __device__ __forceinline__ void load() {
-        if (left > 0) {
-            const uint32_t dst = ring + fill * STAGE;
-            const Elem* kc = static_cast<const Elem*>(a.k_cache);
-            const Elem* vc = static_cast<const Elem*>(a.v_cache);
-            const long long head = (long long)f.head(a, member) * D + lane_elems;
-            bool wrong = false;
-#pragma unroll
-            for (int u = 0; u < RUNS; ++u) {
-                const int key = first_key(f) + 8 * u;
-                const bool in = static_cast<unsigned>(ids[u]) < static_cast<unsigned>(a.num_blocks);
-                wrong |= !in && holds(key);
-                const long long at = head + (((long long)(in ? ids[u] : 0) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * row_elems;
-#pragma unroll
-                for (int r0 = 0; r0 < 8; r0 += ROWS_IT) {
-                    // rows outside the item's keys are zeros: they may hold anything, and 0 * NaN is NaN
-                    const int row = key + r0 + lrow;
-                    bool take = in && row >= f.it.y && row < f.it.z;
-                    const long long off = take ? at + (long long)r0 * row_elems : 0;
-                    // (an index check that fails is reported as a bad block)
-                    if (!TSV_IN_BOUNDS(off + 16 / (int)sizeof(Elem) - 1, ((long long)a.num_blocks << a.bs_log2) * row_elems, nullptr))
-                        wrong = true, take = false;
-                    cp16(dst + Core::place(8 * u + r0 + lrow, lch), kc + off, take);
-                    cp16(dst + HALF + Core::place(8 * u + r0 + lrow, lch), vc + off, take);
-                }
-            }
-            bad = (bad & ~(1u << fill)) | (wrong ? 1u << fill : 0u);
-            if (--left > 0) {
-                f.next<KEYS>(a);
-                fetch();
-            }
-        }
-        cp_commit();
-        if (++fill == STAGES) fill = 0;
-    }
-    __device__ __forceinline__ void begin() {
-        if (left > 0) fetch();
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) load();
-    }
-    // the next tile, p: waits for it, keeps the copies ahead, adds it to the core's state
-    __device__ __forceinline__ bool step(Core& core, const Place& p, float* scratch) {
-        cp_wait<STAGES - 2>();
-        __syncwarp();
-        load();
-        const uint32_t src = ring + stage * STAGE;
-        const bool wrong = ((bad >> stage) & 1u) != 0;
-        const int first = first_key(p);
-        core.step(src, src + HALF, p.it.y - first, p.it.z - first, a.scale_log2, scratch);
-        __syncwarp();
-        if (++stage == STAGES) stage = 0;
-        return wrong;
-    }
-};
-
-// Query rows from row `row` of the item on: row r is head r % gq (of the kv head) of its sequence r / gq.
-template <typename Elem, int D>
-struct ItemRows {
-    const Elem* q;  // the kv head's first row of the item's first sequence
-    int row, gq, seq;  // seq: elements from a sequence to the next
-    __device__ __forceinline__ const Elem* operator()(int r) const {
-        const int x = row + r, s = x < gq ? 0 : x / gq;
-        return q + (long long)s * seq + (x - s * gq) * D;
-    }
-};
-template <typename Core>
-__device__ __forceinline__ void load_rows(const PrefixArgs& a, const Place& p, int member, Core& core) {
-    using Elem = typename Core::Elem;
-    const Elem* q = static_cast<const Elem*>(a.q) + ((long long)p.it.x * a.Hq + p.head(a, member) * a.gq) * Core::D;
-    core.load_q(ItemRows<Elem, Core::D>{q, p.chunk * a.rows, a.gq, a.Hq * Core::D}, p.rows(a));
-}
-
-// Where the rows of a whole unit go: each to its own place.
-template <int D>
-struct ToPlaces {
-    float *o, *m, *l;
-    int row, gq, Hq;
-    long long first;  // the place of the item's row 0
-    __device__ __forceinline__ long long place(int r) const {
-        const int x = row + r, s = x < gq ? 0 : x / gq;
-        return first + (long long)s * Hq + (x - s * gq);
-    }
-    __device__ __forceinline__ void row_(int r, float m_, float l_) const {
-        m[place(r)] = m_;
-        l[place(r)] = l_;
-    }
-};
-template <int D>
-struct Leave {
-    ToPlaces<D> whole;
-    ToSlot<D> slot;
-    bool in_slot;
-    __device__ __forceinline__ void row(int r, float m, float l) const {
-        if (in_slot)
-            slot.row(r, m, l);
-        else
-            whole.row_(r, m, l);
-    }
-    __device__ __forceinline__ float factor(float) const { return 1.0f; }
-    __device__ __forceinline__ void two(int r, int d, float x, float y) const {
-        float* o = in_slot ? slot.o + r * D : whole.o + whole.place(r) * D;
-        *reinterpret_cast<float2*>(o + d) = make_float2(x, y);
-    }
-};
-
-// One warp: its tiles.
-template <typename Core>
-__device__ __forceinline__ void stream_tiles(const PrefixArgs& a, uint32_t ring, float* scratch) {
-    constexpr int D = Core::D, KEYS = Core::KEYS;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int me = blockIdx.x * kWarps + warp, which = me / a.team, member = me % a.team;
-    if (which >= a.lanes) return;
-    const int4 begin = a.begin[3 * which], item = a.begin[3 * which + 1];
-    const int n = a.begin[3 * which + 2].x;
-    if (n == 0) return;
-    Place p{};
-    p.set<KEYS>(a, begin.x, item);
-    p.chunk = begin.y;
-    p.heads = begin.z;
-    p.t = begin.w;
-    Stream<Core> stream(a, ring, member, p, n);
-    stream.begin();
-    Core core;
-    load_rows(a, p, member, core);
-    core.reset();
-    bool seg_bad = false;
-    int seg = 0, t_first = p.t;
-    for (int i = 0; i < n; ++i) {
-        seg_bad |= stream.step(core, p, scratch);
-        if (p.t + 1 < p.tiles && i + 1 < n) {
-            ++p.t;
-            continue;
-        }
-        // the segment's end
-        const bool prefix = p.i < a.G, piece = t_first > 0 || p.t + 1 < p.tiles;
-        const long long rows = (long long)a.B * a.Hq, slot = 2LL * me + (seg == 0 ? 0 : 1);
-        const int row0 = p.chunk * a.rows;
-        if (!TSV_IN_BOUNDS(slot, 2LL * a.lanes * a.team, a.seq_err + p.it.x)) return;
-        const Leave<D> to{
-            {a.whole_o, a.whole_m, a.whole_l, row0, a.gq, a.Hq, (prefix ? 0 : rows) + (long long)p.it.x * a.Hq + p.head(a, member) * a.gq},
-            {a.part_o + slot * a.rows * D, a.part_m + slot * a.rows, a.part_l + slot * a.rows},
-            piece};
-        core.finish(p.rows(a), to, scratch);
-        if (seg_bad)  // the sequences of the unit's rows are told
-            for (int s = row0 / a.gq + lane; s <= (row0 + p.rows(a) - 1) / a.gq; s += 32) atomicOr(a.seq_err + p.it.x + s, TSV_DERR_BLOCK);
-        if (i + 1 < n) {
-            p.next<KEYS>(a);
-            t_first = 0;
-            seg_bad = false;
-            ++seg;
-            load_rows(a, p, member, core);
-            core.reset();
-        }
-    }
-}
+// ------------------------------------------------------------------ the stream of tiles, fp32
 
 template <typename Core>
 __global__ void __launch_bounds__(kThreads, 2) prefix_stream_kernel(const __grid_constant__ PrefixArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     float* scratch = reinterpret_cast<float*>(smem + kWarps * kRingBytes) + warp * kScratch;
-    // After the tensor-core kernel this one starts as that one's CTAs end: it needs only the plan, which that
-    // kernel had waited for before it let this one start, and waits for that kernel itself at its end (so
-    // that the join, which waits for this one, has both).
-    if (a.tc_lanes == 0) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
-    stream_tiles<Core>(a, smem_u32(smem) + warp * kRingBytes, scratch);
-    if (a.tc_lanes > 0) pdl_wait();
+    stream_tiles<Core>(a, blockIdx.x * kWarps + warp, smem_u32(smem) + warp * kRingBytes, scratch);
 }
 
 // ------------------------------------------------------------------ join
@@ -554,9 +317,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     const int h = blockIdx.x * (kJoinThreads / 32 / wpr) + warp / wpr;  // query row of all
     const bool in = h < a.B * a.Hq;
     const int b = in ? h / a.Hq : 0, j = in ? (h % a.Hq) % a.gq : 0, kvh = in ? (h % a.Hq) / a.gq : 0;
-    // The plan is complete (the kernels in between waited for it before they let the next one start), so the
-    // pieces are known when the wait ends: lane 0 looks up those of the sequence's own keys, 1 those of the
-    // prefix, 2 its odd ones.
+    pdl_wait();
+    pdl_launch_dependents();
+    const int err = a.seq_err[b];
+    // lane 0 looks up the pieces of the sequence's own keys, 1 those of the prefix, 2 its odd ones
     Pieces mine;
     if (in) {
         const long long T = a.start[a.G + a.B];
@@ -568,9 +332,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         else if (lane < 3 && tc)
             mine = find_tc_pieces(a, g, b, kvh, j, used.y, lane == 2);
     }
-    pdl_wait();
-    pdl_launch_dependents();
-    const int err = a.seq_err[b];
     float M = -INFINITY, sum = 0.0f, acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.0f;
@@ -643,7 +404,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     // no keys at all: zeros (and an lse of -infinity)
     const float inv = err == 0 && a.seq_lens[b] == 0 ? 0.0f : to.factor(sum);
 #pragma unroll
-    for (int c = 0; c < C; c += 2) to.two(0, lane * C + c, acc[c] * inv, acc[c + 1] * inv);
+    for (int c = 0; c < C; c += 2) store2(to.base(0) + lane * C + c, acc[c] * inv, acc[c + 1] * inv);
     if (lane == 0) to.row(0, M, sum);
 }
 
@@ -652,38 +413,48 @@ constexpr size_t plan_smem(int B, int G) {
 }
 static_assert(plan_smem(kPagesMaxSeqs, kPagesMaxSeqs) <= 232448 - 1024, "the plan's sums fit an SM's shared memory");
 
-template <typename Core>
-cudaError_t launch_core(const PrefixArgs& a, cudaStream_t stream) {
-    using Elem = typename Core::Elem;
-    thread_local int smem_dev = -1;
+// Sets a kernel's dynamic shared memory once per device and host thread.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, int& of_dev) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev != smem_dev) {
-        e = cudaFuncSetAttribute(prefix_stream_kernel<Core>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefix_plan_kernel<Core::KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(plan_smem(kPagesMaxSeqs, kPagesMaxSeqs)));
-        if (e != cudaSuccess) return e;
-        smem_dev = dev;
-    }
-    e = launch_pdl(prefix_plan_kernel<Core::KEYS>, dim3(1), dim3(kPlanThreads), plan_smem(a.B, a.G), stream, 1u, a);
-    if (e != cudaSuccess) return e;
-    if (a.tc_lanes > 0) e = launch_prefix_tc(a, stream);
+    if (e != cudaSuccess || dev == of_dev) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) of_dev = dev;
+    return e;
+}
+
+template <typename Core>
+cudaError_t launch_stream(const PrefixArgs& a, cudaStream_t stream) {
+    thread_local int smem_dev = -1;
+    const cudaError_t e = allow_smem(prefix_stream_kernel<Core>, kSmem, smem_dev);
     if (e != cudaSuccess) return e;
     const int warps = a.lanes * a.team;
-    e = launch_pdl(prefix_stream_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), kSmem, stream, 1u, a);
+    return launch_pdl(prefix_stream_kernel<Core>, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)), dim3(kThreads), kSmem, stream, 1u, a);
+}
+
+template <typename Elem, int D>
+cudaError_t launch_kernels(const PrefixArgs& a, cudaStream_t stream) {
+    constexpr bool bf16 = sizeof(Elem) == 2;
+    constexpr int TILE = tile_keys(bf16, D);
+    thread_local int smem_dev = -1;
+    cudaError_t e = allow_smem(prefix_plan_kernel<TILE>, plan_smem(kPagesMaxSeqs, kPagesMaxSeqs), smem_dev);
+    if (e == cudaSuccess) e = launch_pdl(prefix_plan_kernel<TILE>, dim3(1), dim3(kPlanThreads), plan_smem(a.B, a.G), stream, 1u, a);
+    if (e != cudaSuccess) return e;
+    if constexpr (bf16)
+        e = launch_prefix_tc(a, stream);
+    else
+        e = a.rows <= 4 ? launch_stream<F32Core<D, 4>>(a, stream) : launch_stream<F32Core<D, 8>>(a, stream);
     if (e != cudaSuccess) return e;
     // warps to a row of the join: more where there are few rows, whose keys then lie in many pieces
     const int rows = a.B * a.Hq, wpr = rows <= 256 ? 8 : rows <= 1024 ? 2 : 1, per = kJoinThreads / 32 / wpr;
-    return launch_pdl(prefix_join_kernel<Elem, Core::D, Core::KEYS>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kJoinThreads), 0,
-                      stream, 1u, a, wpr);
+    return launch_pdl(prefix_join_kernel<Elem, D, TILE>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kJoinThreads), 0, stream, 1u,
+                      a, wpr);
 }
 
 template <int D>
 cudaError_t launch_dim(const PrefixArgs& a, bool bf16, cudaStream_t stream) {
-    if (bf16) return a.rows <= 16 ? launch_core<Bf16Core<D, 1>>(a, stream) : launch_core<Bf16Core<D, 2>>(a, stream);
-    return a.rows <= 4 ? launch_core<F32Core<D, 4>>(a, stream) : launch_core<F32Core<D, 8>>(a, stream);
+    return bf16 ? launch_kernels<__nv_bfloat16, D>(a, stream) : launch_kernels<float, D>(a, stream);
 }
 
 size_t aligned(size_t x) { return (x + 255) & ~size_t(255); }
@@ -695,11 +466,12 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     const int gq = Hq / Hkv;
     // a unit's rows: one or two 16-row fragments (bf16), 4 or 8 (fp32)
     const long long rows = (long long)B * gq;
-    // bf16 prefixes go to the tensor-core kernel at any number of rows.  In the stream, whose warp-level products
+    // bf16 prefixes go to the tensor cores at any number of rows.  In the stream, whose warp-level products
     // take 32 rows at a time, they are behind from some 16 rows on and ahead by little below: one prefix of
     // 16384 keys, 8 / 16 / 32 / 128 rows of 128: 36 / 36 / 43 / 49 us there, 29 / 38 / 95 / 256 in the stream; 12 of 4096
     // keys: 70 / 71 / 72 / 108 against 168 / 248 / 246 / 878.
-    p.tc_lanes = bf16 ? num_sms : 0;
+    // (one CTA an SM, at least one for the prefixes and one for the stream)
+    p.tc_lanes = bf16 ? (num_sms > 1 ? num_sms : 2) : 0;
     p.rows = bf16 ? (gq <= 16 ? 16 : 32) : (rows <= 4 ? 4 : 8);
     p.team = 1;
     for (int t = 2; t <= kMaxTeam; ++t)
@@ -709,7 +481,7 @@ PrefixPlan make_prefix_plan(int B, int G, int Hq, int Hkv, int D, int block_size
     const int tile = tile_keys(bf16, D);
     const long long cap_tiles = ((long long)max_blocks * block_size + tile - 1) / tile + 1;
     const long long units = (rows / p.rows + G) + (long long)B * ((gq + p.rows - 1) / p.rows);
-    long long lanes = 2LL * kWarps * num_sms / p.team;
+    long long lanes = (long long)kStreamWarps * num_sms / p.team;
     const long long most = units * (Hkv / p.team) * cap_tiles;
     p.lanes = static_cast<int>(lanes < 1 ? 1 : lanes < most ? lanes : most);
     const size_t slots = 2 * (size_t)p.lanes * p.team * p.rows, whole = 3 * (size_t)B * Hq;

@@ -22,6 +22,10 @@
 // (the second part's products take half as long again as the others together; with one part alone the result is off by
 // another rounding of bf16).  Both lie in the columns of S that the weights came from.
 //
+// The CTAs that the plan leaves without prefix tiles take the stream of the sequences' own keys, up to eight warps each
+// (prefix_stream.cuh).  They are CTAs of this kernel and not a kernel of their own: that one could run beside this one
+// only if it did not wait for it, and what the plan has written is promised to a kernel that has waited.
+//
 // Every wait is bounded.  One that gives up sets TSV_DERR_TIMEOUT for the sequences of all groups from its own
 // to the CTA's last: a CTA does nothing more after it.
 #include <cuda_bf16.h>
@@ -29,6 +33,7 @@
 #include "../common.cuh"
 #include "../tc_ptx.cuh"
 #include "continue_args.cuh"
+#include "prefix_stream.cuh"
 
 namespace tsv {
 namespace {
@@ -38,8 +43,9 @@ constexpr int kTileKeys = kPrefixTcKeys;
 constexpr int kUnitRows = kPrefixTcRows;
 constexpr uint32_t kHalfBytes = 128 * 128;  // 128 rows x 64 bf16 (one 128B-swizzled half)
 constexpr int kMaxSlots = 12;
-constexpr uint32_t kRegsProducer = 96, kRegsSoftmax = 200;
+constexpr uint32_t kRegsProducer = 96, kRegsSoftmax = 200, kRegsIdle = 24, kRegsStream = 240;
 static_assert(128 * kRegsProducer + 256 * kRegsSoftmax <= 384 * 168, "register split exceeds the launch");
+static_assert(128 * kRegsIdle + 256 * kRegsStream <= 384 * 168, "register split exceeds the launch");
 
 // Shared memory: Q tiles | ring of K/V slots | barriers.
 struct Layout {
@@ -145,7 +151,7 @@ __device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
 // Two weights (0 or normal numbers) as the sum of two bf16 each, hi and lo: hi is the weight cut off after bf16's
 // bits, lo the rest and 2^-23 of the weight more, so that a positive weight has two positive parts, which
 // keep an infinite value infinite.
-__device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uint32_t* lo) {
+__device__ __forceinline__ void split_bf16_up(float w0, float w1, uint32_t* hi, uint32_t* lo) {
     const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
     *hi = __byte_perm(u0, u1, 0x7632);
     const float more = 1.0f + 0x1p-23f;
@@ -157,7 +163,7 @@ __device__ __forceinline__ void split_bf16(float w0, float w1, uint32_t* hi, uin
     *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <int D, int QT>
+template <int D, int QT, int MT>  // MT: 16-row fragments of a unit of the stream
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     constexpr int HALVES = D / 64;
@@ -166,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr Layout lay = layout<D, QT>();
     constexpr int nslots = lay.slots;
-    using Place = Slot<nslots>;
+    using Fill = Slot<nslots>;
+    using StreamCore = Bf16Core<D, MT>;
+    static_assert(kStreamWarps * (kRingBytes + kScratch * sizeof(float)) <= lay.bars, "the stream's rings fit in front of the barriers");
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
@@ -215,10 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int my_err = 0;
     int err_g = first.g;  // the group in which a wait of this thread is or gave up
 
-    if (warp < 4) regs_dec<kRegsProducer>();
-    if (count == 0) {
-        if (warp >= 4) regs_inc<kRegsSoftmax>();
-    } else if (warp == 0) {
+    if (count > 0 && warp < 4) regs_dec<kRegsProducer>();
+    if (warp == 0 && count > 0) {
         // ============================ TMA producer: a lane for each block of the tile issues that block's boxes.
         // Block ids come 32 at a time, those of some tiles of a unit, a batch ahead.  (Two warps of 16-byte
         // asynchronous copies instead: 4096 rows of 32768 keys 132 us against 140, 24 ragged groups of 64-wide heads 175
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(bar(Bars::kFull + f % nslots), (f / nslots) & 1, &never)) my_err = 1;
             }
         }
-    } else if (warp < 3) {
+    } else if (warp < 3 && count > 0) {
         // ============================ MMA issuers.  The products are issued as fast as the tensor pipe takes them,
         // and it holds few: what the issuing thread does in between (waits, places in the ring) is time that the
         // pipe stands still.  So places are counted on without divisions.  Streams on the same tiles have one
@@ -318,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kTileKeys / 16; ++k)
                         mma_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
             };
-            auto full = [&](const Place& f) { return mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort); };
-            auto free_slot = [&](const Place& f) { mma_commit(bar(Bars::kEmpty + f.slot)); };
+            auto full = [&](const Fill& f) { return mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort); };
+            auto free_slot = [&](const Fill& f) { mma_commit(bar(Bars::kEmpty + f.slot)); };
             Tile p = first;
             uint32_t n_p[2] = {0, 0};  // tiles of each stream before the segment
             bool ok = true;
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool by_tile = p.by_tile();
                 err_g = p.g;
                 ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
-                Place fK{2 * j % nslots, static_cast<uint32_t>(2 * j / nslots) & 1u}, fV = fK;  // of the next K and V tile
+                Fill fK{2 * j % nslots, static_cast<uint32_t>(2 * j / nslots) & 1u}, fV = fK;  // of the next K and V tile
                 fV.skip(1);
                 if (!by_tile && me_m == 1) {
                     // what a tile's products read besides the weights: one arrival with those of stream 0, and
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             volatile int never = 0;
             if (!mbar_wait(bar(Bars::kDone + me_m), 0, &never)) my_err = 1;
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && count > 0) {
         // ============================ softmax, a stream each warpgroup
         regs_inc<kRegsSoftmax>();
         const int wg = (warp - 4) >> 2, tw = (tid - 128) & 127;  // stream, row of its M tile (TMEM lane)
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * (q32 + q)]), __uint_as_float(sv[2 * (q32 + q) + 1])), sc2, off2), x0, x1);
                             const float p0 = ex2(x0), p1 = ex2(x1);
                             la2[q & 3] = f2_add(la2[q & 3], f2_pack(p0, p1));
-                            split_bf16(p0, p1, &hi[q], &lo[q]);
+                            split_bf16_up(p0, p1, &hi[q], &lo[q]);
                         }
                         tmem_st32(tS + q32, hi);
                         tmem_st32(tS + 64 + q32, lo);
@@ -636,6 +642,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok) my_err = 1;
+    } else if (count == 0) {
+        // ============================ the stream, last in the code: what lies at its beginning is fetched before the
+        // CTAs' work begins, and the other roles' first tiles need it more (the stream in front: 64 samples of a 32k prompt 107
+        // us, this way 102; 8 samples 21.1 and 19.5)
+        if (warp < 4) {
+            regs_dec<kRegsIdle>();
+        } else {
+            regs_inc<kRegsStream>();
+            const int w = warp - 4;
+            if (w < begin.y)
+                stream_tiles<StreamCore>(a, begin.x + w, smem_u32(smem) + w * kRingBytes,
+                                         reinterpret_cast<float*>(smem + kStreamWarps * kRingBytes) + w * kScratch);
+        }
     }
     if (my_err) {
         *s_abort = 1;
@@ -660,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D, int QT>
+template <int D, int QT, int MT>
 cudaError_t launch_tiles(const PrefixArgs& a, cudaStream_t stream) {
     CUtensorMap mk, mv;
     const long long rows = static_cast<long long>(a.num_blocks) << a.bs_log2;
@@ -672,17 +691,21 @@ cudaError_t launch_tiles(const PrefixArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev != smem_dev) {
-        e = cudaFuncSetAttribute(prefix_tc_kernel<D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+        e = cudaFuncSetAttribute(prefix_tc_kernel<D, QT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
         if (e != cudaSuccess) return e;
         smem_dev = dev;
     }
-    return launch_pdl(prefix_tc_kernel<D, QT>, dim3(static_cast<unsigned>(a.tc_lanes)), dim3(kThreads), total, stream, 1u, a, mk, mv);
+    return launch_pdl(prefix_tc_kernel<D, QT, MT>, dim3(static_cast<unsigned>(a.tc_lanes)), dim3(kThreads), total, stream, 1u, a, mk, mv);
 }
 
-template <int D>
+template <int D, int MT>
 cudaError_t launch_dim(const PrefixArgs& a, cudaStream_t stream) {
     // one Q tile where no group can have more rows, which leaves the ring another slot
-    return (long long)a.B * a.gq > 128 ? launch_tiles<D, 2>(a, stream) : launch_tiles<D, 1>(a, stream);
+    return (long long)a.B * a.gq > 128 ? launch_tiles<D, 2, MT>(a, stream) : launch_tiles<D, 1, MT>(a, stream);
+}
+template <int D>
+cudaError_t launch_rows(const PrefixArgs& a, cudaStream_t stream) {
+    return a.rows <= 16 ? launch_dim<D, 1>(a, stream) : launch_dim<D, 2>(a, stream);
 }
 
 }  // namespace
@@ -695,7 +718,7 @@ extern "C" int tsv_test_set_prefix_stall(int mode) {
 #endif
 
 cudaError_t launch_prefix_tc(const PrefixArgs& a, cudaStream_t stream) {
-    return a.D == 64 ? launch_dim<64>(a, stream) : launch_dim<128>(a, stream);
+    return a.D == 64 ? launch_rows<64>(a, stream) : launch_rows<128>(a, stream);
 }
 
 }  // namespace tsv

@@ -147,12 +147,6 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // true iff v is one of the first j rejected tokens xr[0..j-1]
 __device__ __forceinline__ bool is_rejected(int v, int j, const int* xr) {
     for (int i = 0; i < j; ++i)

@@ -13,6 +13,11 @@ constexpr int kStreamWarps = 8;    // of an SM: as many rings as its shared memo
 constexpr int kRingBytes = 24576;  // of a warp
 constexpr int kScratch = 136;      // floats of a warp beside its ring
 
+// Whether an item has tiles in a kernel.  (The product of the two may be 2^32: a prefix of 2^20 fp32 keys with heads of
+// 64 and the 2^19 rows of 8192 sequences of 64 heads to one K/V head.)
+__host__ __device__ constexpr bool has_tiles(int tiles, int units) { return tiles > 0 && units > 0; }
+static_assert(has_tiles(1 << 16, 1 << 16) && !has_tiles(0, 5) && !has_tiles(5, 0), "without the product's 32 bits");
+
 // Tiles of an item: from the tile that holds its first key.
 template <int TILE>
 __device__ __forceinline__ int item_tiles(const int4& it) {
@@ -49,7 +54,7 @@ struct Place {
         chunk = 0;
         do {
             set<TILE>(a, i + 1, ahead);
-        } while (tiles * units == 0 && i + 1 < a.G + a.B);
+        } while (!has_tiles(tiles, units) && i + 1 < a.G + a.B);
     }
     __device__ __forceinline__ int head(const PrefixArgs& a, int member) const { return heads * a.team + member; }
     __device__ __forceinline__ int rows(const PrefixArgs& a) const { return min(a.rows, it.w - chunk * a.rows); }

@@ -111,7 +111,7 @@ struct Tile {
         unit = 0;
         do {
             set(g + 1, a.item[g + 1]);
-        } while (tiles * groups == 0 && g + 1 < a.G);
+        } while (!has_tiles(tiles, groups) && g + 1 < a.G);
     }
     __device__ __forceinline__ int head() const { return unit / groups; }
     __device__ __forceinline__ int row0() const { return unit % groups * kUnitRows; }

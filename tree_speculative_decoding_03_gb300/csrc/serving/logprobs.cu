@@ -615,6 +615,40 @@ __global__ void __launch_bounds__(threads_of(CLUSTER), 1024 / threads_of(CLUSTER
     }
 }
 
+#ifdef TSV_TEST_HOOKS
+int g_test_logprobs_cluster = 8;  // test build: the largest cluster that counts as resident
+#endif
+
+// Whether a cluster of this size can be resident (a partitioned GPU may not have as many SMs in one
+// group); looked up once per device and host thread.
+template <typename Elem, int CLUSTER>
+bool cluster_fits() {
+#ifdef TSV_TEST_HOOKS
+    if (CLUSTER > g_test_logprobs_cluster) return false;
+#endif
+    thread_local int of_dev = -1;
+    thread_local bool fits = false;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev != of_dev) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = CLUSTER;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(CLUSTER);
+        cfg.blockDim = dim3(threads_of(CLUSTER));
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0, n_entropy = 0;
+        fits = cudaOccupancyMaxActiveClusters(&n, token_logprobs_kernel<Elem, CLUSTER, false>, &cfg) == cudaSuccess && n > 0 &&
+               cudaOccupancyMaxActiveClusters(&n_entropy, token_logprobs_kernel<Elem, CLUSTER, true>, &cfg) == cudaSuccess && n_entropy > 0;
+        of_dev = dev;
+    }
+    return fits;
+}
+
 template <typename Elem, int CLUSTER>
 cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t stream) {
     const auto kernel = a.entropy ? token_logprobs_kernel<Elem, CLUSTER, true> : token_logprobs_kernel<Elem, CLUSTER, false>;
@@ -636,15 +670,19 @@ cudaError_t launch_type(const LogprobArgs& a, int num_sms, cudaStream_t stream) 
     const long long vecs = ((long long)a.V + Vec<Elem>::N - 1) / Vec<Elem>::N;
     int n = 1;
     while (n < 8 && 2LL * n * a.T <= 2LL * num_sms && vecs >= 2LL * n * threads_of(2)) n *= 2;
-    switch (n) {
-        case 8: return launch_rows<Elem, 8>(a, stream);
-        case 4: return launch_rows<Elem, 4>(a, stream);
-        case 2: return launch_rows<Elem, 2>(a, stream);
-        default: return launch_rows<Elem, 1>(a, stream);
-    }
+    // (a smaller cluster, or one CTA, where one cannot be resident)
+    if (n >= 8 && cluster_fits<Elem, 8>()) return launch_rows<Elem, 8>(a, stream);
+    if (n >= 4 && cluster_fits<Elem, 4>()) return launch_rows<Elem, 4>(a, stream);
+    if (n >= 2 && cluster_fits<Elem, 2>()) return launch_rows<Elem, 2>(a, stream);
+    return launch_rows<Elem, 1>(a, stream);
 }
 
 }  // namespace
+
+#ifdef TSV_TEST_HOOKS
+// test build only: clusters above this size count as not resident
+extern "C" void tsv_test_set_logprobs_cluster(int most) { g_test_logprobs_cluster = most; }
+#endif
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
     return bf16 ? launch_type<__nv_bfloat16>(a, num_sms, stream) : launch_type<float>(a, num_sms, stream);

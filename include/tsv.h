@@ -510,7 +510,9 @@ tsv_status tsv_kv_copy_blocks(void *k_cache, void *v_cache, const int32_t *copy_
  * Group g is the sequences group_offsets[g] .. group_offsets[g+1] - 1 (group_offsets[0] = 0, ascending,
  * group_offsets[G] = B; a group may be empty).  Its sequences attend to the same first P_g = prefix_lens[g]
  * keys, 0 <= P_g <= seq_lens[b], which are read from the table row of the group's first sequence, once for all
- * of them; keys P_g .. L_b - 1 come from each sequence's own row.  P_g need not be a multiple of the block size.
+ * of them; keys P_g .. L_b - 1 come from each sequence's own row.  P_g need not be a multiple of the block size.  The
+ * first sequence's row has to name the blocks of the P_g keys whatever its own length is: it may have ended (it is
+ * flagged then, the others are not) while others of its group go on, as long as the shared blocks are held.
  * out and lse are those of tsv_decode_attn for tables with these keys, with the same precision: fp32 sums and weights (a bf16 call's
  * weights within 2^-15 of themselves), out rounded once.  A repeated call gives the same bits.
  * L_b = 0: out is zero and lse -infinity.  Slots outside a sequence's keys are never read into the result.

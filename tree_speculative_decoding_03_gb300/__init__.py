@@ -420,7 +420,7 @@ def prefix_decode_attn_workspace_size(B, G, Hq, Hkv, D, block_size, max_blocks, 
 def prefix_decode_attn(q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out, scale: float, workspace=None,
                        seq_err=None, lse=None, stream=None):
     """Attention of one new token per sequence where groups of neighbouring sequences share their first keys,
-    which are read once for the group (see include/tsv.h).  group_offsets [G+1], prefix_lens [G] int32; the others as in
+    which are read once for the group, by the table row of its first sequence (see include/tsv.h).  group_offsets [G+1], prefix_lens [G] int32; the others as in
     decode_attn; seq_err and a workspace of prefix_decode_attn_workspace_size(...) bytes are needed."""
     _check(_marshal().prefix_decode_attn(
         load().addresses["tsv_prefix_decode_attn"], q, k_cache, v_cache, block_table, seq_lens, group_offsets, prefix_lens, out, scale,

@@ -64,7 +64,10 @@ __host__ __device__ constexpr Layout layout() {
     return l;
 }
 
-// A place in the ring: the slot of a fill, and the parity of its barriers' phase.
+// A place in the ring: the slot of a fill, and the parity of its barriers' phase.  A parity tells a phase from the next one
+// only.  So who waits for a fill has seen the slot's last one land, or knows that this one has been sent (for which the
+// producer has waited until the last one was used up): streams on every other tile see each other's fills through neither
+// their waits nor the weights, and with 5 or 6 slots a slot goes from one stream to the other.
 template <int SLOTS>
 struct Slot {
     int slot;
@@ -85,7 +88,8 @@ struct Bars {
     static constexpr int kP = kS + 2;         // [2] its weights are
     static constexpr int kO = kP + 2;         // [2] a segment's last product with V is done
     static constexpr int kQ = kO + 2;         // a segment's Q rows are in shared memory
-    static constexpr int kDone = kQ + 1;  // [2]
+    static constexpr int kSeen = kQ + 1;  // both issuers have seen that
+    static constexpr int kDone = kSeen + 1;  // [2]
     static constexpr int kStall = kDone + 2;  // never completed (test build: the stalled wait)
     static constexpr int kCount = kStall + 1;
 };
@@ -142,6 +146,25 @@ __device__ __forceinline__ uint32_t opaque_u32(uint32_t x) {
     return y;
 }
 
+__device__ __forceinline__ void store_release_smem(uint32_t at, int x) {
+    asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ int load_acquire_smem(uint32_t at) {
+    int x;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+// Bounded wait until fill `fill` has been sent; *sent: the fills that are known to be.
+__device__ __forceinline__ bool wait_sent(uint32_t at, int fill, int* sent, volatile int* abort_flag) {
+    if (fill < *sent) return true;
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+        *sent = load_acquire_smem(at);
+        if (fill < *sent) return true;
+        if (*abort_flag || globaltimer() - t0 > kWaitLimitNs) return false;
+    }
+}
+
 // One warp: the sequences whose rows a unit holds have a block id outside the cache.
 __device__ __forceinline__ void flag_unit(const PrefixArgs& a, const Tile& p) {
     const int r0 = p.row0();
@@ -179,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
     int* s_lost = reinterpret_cast<int*>(smem + lay.bars + 8 * Bars::kCount + 8);  // first group in which a wait gave up
+    const uint32_t sent_at = smem_u32(smem + lay.bars + 8 * Bars::kCount + 12);    // fills sent so far
     const uint32_t bar0 = smem_u32(bars);
     auto bar = [=](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -196,9 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(Bars::kDone + m), 1);
         }
         mbar_init(bar(Bars::kQ), 256);
+        mbar_init(bar(Bars::kSeen), 2);
         mbar_init(bar(Bars::kStall), 1);
         *s_abort = 0;
         *s_lost = a.G;
+        store_release_smem(sent_at, 0);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -273,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint32_t dst = smem_u32(smem + lay.ring + slot * SLOT) + lane * bs * 128;
-                if (lane == 0) mbar_expect_tx(bar(Bars::kFull + slot), static_cast<uint32_t>(nblk * bs * 128 * HALVES));
+                if (lane == 0) {
+                    mbar_expect_tx(bar(Bars::kFull + slot), static_cast<uint32_t>(nblk * bs * 128 * HALVES));
+                    store_release_smem(sent_at, f + 1);
+                }
                 __syncwarp();
                 if (mine) {
 #pragma unroll
@@ -324,7 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kTileKeys / 16; ++k)
                         mma_ts(d, pa + part * 64 + k * 8, vb + ((k * 16 * 128) >> 4), idO, (more || part > 0 || k > 0) ? 1u : 0u);
             };
-            auto full = [&](const Fill& f) { return mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort); };
+            int sent = 0;  // fills that are known to have been sent
+            auto full = [&](const Fill& f, int fill) {
+                return wait_sent(sent_at, fill, &sent, s_abort) && mbar_wait(bar(Bars::kFull + f.slot), f.parity, s_abort);
+            };
             auto free_slot = [&](const Fill& f) { mma_commit(bar(Bars::kEmpty + f.slot)); };
             Tile p = first;
             uint32_t n_p[2] = {0, 0};  // tiles of each stream before the segment
@@ -334,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool by_tile = p.by_tile();
                 err_g = p.g;
                 ok = mbar_wait(bar(Bars::kQ), seg & 1, s_abort);
+                mbar_arrive(bar(Bars::kSeen));
                 Fill fK{2 * j % nslots, static_cast<uint32_t>(2 * j / nslots) & 1u}, fV = fK;  // of the next K and V tile
                 fV.skip(1);
                 if (!by_tile && me_m == 1) {
@@ -341,14 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // not before the last tile's have all come
                     for (int i = 0; i < n && ok; ++i) {
                         fK.skip(2);
-                        ok = full(fV) && (i + 1 == n || full(fK));
+                        ok = full(fV, 2 * (j + i) + 1) && (i + 1 == n || full(fK, 2 * (j + i) + 2));
                         if (!ok) break;
                         mbar_arrive(bar(Bars::kP));
                         fV.skip(2);
-                        ok = mbar_wait(bar(Bars::kP), (n_p[0] + i) & 1, s_abort);
+                        // (after the last tile the next segment's Q says so)
+                        if (i + 1 < n) ok = mbar_wait(bar(Bars::kP), (n_p[0] + i) & 1, s_abort);
                     }
                 } else if (!by_tile) {
-                    ok = ok && full(fK);
+                    ok = ok && full(fK, 2 * j);
                     if (!ok) break;
                     tc_fence_after();
                     for (int m = 0; m < 2; ++m) {
@@ -380,14 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fK.skip(2);
                         fV.skip(2);
                     }
-                    ok = full(fK);
+                    ok = full(fK, 2 * (j + m));
                     if (!ok) break;
                     tc_fence_after();
                     issue_S(m, 0, fK.slot);
                     mma_commit(bar(Bars::kS + m));
                     free_slot(fK);
                     for (int i = m, q = 0; i < n; i += 2, ++q) {
-                        ok = full(fV) && mbar_wait(bar(Bars::kP + m), (n_p[m] + q) & 1, s_abort);
+                        ok = full(fV, 2 * (j + i) + 1) && mbar_wait(bar(Bars::kP + m), (n_p[m] + q) & 1, s_abort);
                         if (!ok) break;
                         tc_fence_after();
                         issue_PV(m, fV.slot, q > 0);
@@ -396,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fV.skip(4);
                         fK.skip(4);
                         if (i + 2 < n) {
-                            ok = full(fK);
+                            ok = full(fK, 2 * (j + i) + 4);
                             if (!ok) break;
                             tc_fence_after();
                             issue_S(m, 0, fK.slot);
@@ -461,6 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 cp_async_wait_all();
                 fence_proxy_async_smem();
+            }
+            // (neither issuer falls two segments behind, even where it has no tile in one.  After a wait that gave up the
+            // arrivals go on: all threads' or none's, since a barrier must not get more of them than its phase has room for)
+            if (seg > 0) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(Bars::kSeen), (seg - 1) & 1, s_abort));
+                if (!ok) *s_abort = 1;
             }
             mbar_arrive(bar(Bars::kQ));
             float m_run = -INFINITY, l_run = 0.0f;
@@ -554,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // NaN); on a tile of both streams the first does it, whose product is issued first
                 if (left < kTileKeys && (by_tile || wg == 0)) {
                     const int fV = 2 * (j + i) + 1;
-                    ok = mbar_wait(bar(Bars::kFull + fV % nslots), (fV / nslots) & 1, s_abort);
+                    int sent = 0;
+                    ok = wait_sent(sent_at, fV, &sent, s_abort) && mbar_wait(bar(Bars::kFull + fV % nslots), (fV / nslots) & 1, s_abort);
                     if (ok) {
                         constexpr int kRowChunks = HALVES * 8, kRowsPerStep = 128 / kRowChunks;
                         uint8_t* vt = smem + lay.ring + (fV % nslots) * SLOT + ((tw % kRowChunks) >> 3) * kHalfBytes + (tw & 7) * 16;

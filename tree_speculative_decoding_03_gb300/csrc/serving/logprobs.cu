@@ -7,7 +7,8 @@
 //
 // The alternatives come from the same pass: a thread's running maximum is the largest of its
 // slice.  Of 64 groups of threads the n-th largest group maximum is a bound that at least n
-// entries reach, so only slices whose maximum reaches it hold alternatives -- some n of 512 --
+// entries reach, so only slices whose maximum reaches it hold alternatives -- some n of 256, or
+// of 512 in a cluster --
 // and those few are read again by all threads.  The entries that reach the bound, hardly more than n, are
 // ranked among themselves; where they are many, warps keep lists in order.  Nothing depends on the values but
 // the time: a row of equal logits is read three times.  (Lists for every row, a slice at a time: 2000 rows of

@@ -61,10 +61,12 @@ __device__ __forceinline__ long long block_before(long long mine, long long* s_w
 // Lanes that share T tiles: one tile each while there are lanes.
 __device__ __forceinline__ int lanes_for(long long T, int lanes) { return T < lanes ? static_cast<int>(T) : lanes; }
 
-// SMs left to the stream while the tensor-core CTAs have the others: both have work that lasts about as long.  Times measured at full load, in us of an SM: a
-// tile of 128 keys and up to 256 rows 2.5 (heads of 128) or 2 (64) and a unit 3 more; a tile of the stream 1.4 on one of
-// eight warps and a unit 9 more.  (One after the other: 64 samples of a 32k prompt 134 us, with the division then 120; 24
-// ragged groups 162 and 140.)
+// SMs left to the stream while the tensor-core CTAs have the others: both have work that lasts about as
+// long.  Times at full load, in us of an SM: a tile of 128 keys and up to 256 rows 2.5 (heads of 128) or 2 (64)
+// and a unit 3 more; a tile of the stream 1.4 on one of eight warps and a unit 9 more.  (Two kernels one after the other, each on
+// all SMs, and with the division: 64 samples of a 32k prompt 114 and 103 us, 24 ragged groups 154 and 130, 8 samples 23 and 20; 300
+// groups of 4 sequences, where the division is off, 356 and 411.  Units at 11 and 13, tiles at 1.2, units of the
+// tensor cores at 2 and 4 gain 10 % on one of ten shapes and lose it on another.)
 __device__ __forceinline__ int stream_sms(const PrefixArgs& a, long long T, long long tc_T) {
     if (T == 0 || tc_T == 0) return a.tc_lanes;
     const float units = static_cast<float>(a.B) * (a.Hkv / a.team) * ((a.gq + a.rows - 1) / a.rows);

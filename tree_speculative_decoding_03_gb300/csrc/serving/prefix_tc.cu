@@ -1,9 +1,9 @@
 // prefix_tc.cu -- the shared prefixes of prefix_attn.cu on the 5th-generation tensor cores (tcgen05,
 // accumulators in TMEM, K/V tiles by TMA), bf16.
 //
-// The rows of a group and kv head -- the group's sequences times the heads of the kv head -- against the
-// group's P keys are a dense product: 4 R P D multiply-adds on 4 P D bytes, so from some 300 rows on the
-// tensor cores are the bound, and below the cache's bytes.
+// The R rows of a group and kv head -- the group's sequences times the heads of the kv head -- against the
+// group's P keys are two dense products, the second with weights in two parts: 3 R P D multiply-adds on 4 P D
+// bytes, so from some 190 rows on the tensor cores are the bound, and below the cache's bytes.
 //
 // Work split: a unit is (group, kv head, 256 rows).  Its keys are cut into 128-key tiles, the tiles of
 // all units form one row, divided evenly between persistent CTAs.  A CTA's segment of a unit ends in

@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int8_t* s_par = reinterpret_cast<int8_t*>(smem + lay.misc + kMiscPar);  // [2][128]
     volatile int* s_meta = reinterpret_cast<volatile int*>(smem + lay.misc + kMiscMeta);  // [kMaxSlots]
     int* s_sched = reinterpret_cast<int*>(smem + lay.misc + kMiscSched);
-    int* s_lost = s_sched + 12;  // first sequence in which a wait gave up (B: none)
     int* s_blk0 = reinterpret_cast<int*>(smem + lay.misc + kMiscBlk0);  // [16]
     volatile int* s_abort = reinterpret_cast<volatile int*>(smem + lay.bars + 8 * Bars::kCount);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + lay.bars + 8 * Bars::kCount + 4);
@@ -305,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(Bars::kDone), 1);
         mbar_init(bar(Bars::kStall), 1);
         *s_abort = 0;
-        *s_lost = a.B;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int count = s_sched[5];  // tiles of this CTA
     const TileIt it0{s_sched[0], s_sched[1], s_sched[2], s_sched[3], s_sched[4]};
     int my_err = 0;
-    int err_b = it0.b;  // sequence in which a wait of this thread is or gave up (of the MMA issuer: the CTA's first)
+    int err_b = it0.b;  // sequence flagged if a wait of this thread gives up
 
     if (warp < 4) regs_dec<kRegsProducer>();  // warpgroup 0: producer, MMA issuer, two idle warps
     if (warp == 0) {
@@ -586,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the Q rows and parents of the next segment's unit are fetched during this
             // segment's last tile, once that tile's S product (the last reader of Q) is done
             const bool more = jt + ntl < count;
-            if (ok) err_b = b;
+            err_b = b;
             if (t_first == 0 && stid == 0 &&
                 TSV_IN_BOUNDS(((long long)b * a.Hkv + g) * nrg + rg, (long long)a.B * a.Hkv * nrg, a.seq_err + b)) {
                 // this lane holds the unit's first piece: record where its pieces are
@@ -806,6 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.part_l[prow] = l_run;
                 }
             }
+            if (!ok && lane == 0) {  // this segment and all after it are lost (seq_err: see below)
+                pdl_wait();
+                atomicOr(&a.seq_err[b], TSV_DERR_TIMEOUT);
+            }
             if (more) it.next_unit(a);
             ++seg;
         }
@@ -817,19 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     if (my_err) {
         *s_abort = 1;
-        atomicMin(s_lost, err_b);
+        atomicOr(&a.seq_err[err_b], TSV_DERR_TIMEOUT);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0 && *s_lost < a.B) {
-        TileIt it{s_sched[0], s_sched[1], s_sched[2], s_sched[3], s_sched[4]};
-        for (int left = s_sched[5]; left > 0;) {
-            if (it.b >= *s_lost) atomicOr(&a.seq_err[it.b], TSV_DERR_TIMEOUT);
-            left -= it.Tb - it.t;
-            if (left > 0) it.next_unit(a);
-        }
-    }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
